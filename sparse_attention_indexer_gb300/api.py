@@ -5,7 +5,8 @@ allocates device memory through torch and passes pointers, sizes and the stream.
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+import contextlib
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -103,3 +104,263 @@ class HostPagedTopK:
                          out_slots=self.out, stream=stream)
         self.out_host.copy_(self.out, non_blocking=True)
         return self.out_host
+
+
+class Kv8Cache:
+    """A paged K/V cache in 8 bits and the attention over it (include/kv8_attention.h).
+
+    k, v      uint8 [num_slots, kv_heads, dim]: e4m3 codes
+    k_scale, v_scale  float32 [num_slots / block_tokens, kv_heads]
+    The tensors stay the caller's; several layers are several caches. The workspace is made
+    when a call first needs it, one for each stream the cache is used on (make the first call
+    of a shape before a stream capture). `status` collects the device status bits of all
+    calls."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, page_size: int, block_tokens: int):
+        for c, s in ((k, k_scale), (v, v_scale)):
+            if c.dtype != torch.uint8 or c.dim() != 3 or not c.is_cuda or not c.is_contiguous():
+                raise ValueError("a cache is a contiguous CUDA uint8 tensor [slots, heads, dim]")
+            if block_tokens < 1 or c.shape[0] % block_tokens:
+                raise ValueError("the slots are not a whole number of blocks")
+            if (s.dtype != torch.float32 or s.device != c.device or not s.is_contiguous()
+                    or tuple(s.shape) != (c.shape[0] // block_tokens, c.shape[1])):
+                raise ValueError("scales are contiguous float32 [slots / block_tokens, heads]")
+        if k.shape != v.shape or k.device != v.device:
+            raise ValueError("k and v differ in shape or device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_size, self.block_tokens = int(page_size), int(block_tokens)
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._workspaces = {}
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, dim: int,
+              block_tokens: Optional[int] = None, device: Optional[torch.device] = None):
+        """A cache of num_pages pages holding zeros; block_tokens defaults to the page."""
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        block = page_size if block_tokens is None else block_tokens
+        if block < 1 or page_size % block:
+            raise ValueError("page_size is not a multiple of block_tokens")
+        slots = num_pages * page_size
+        code = lambda: torch.zeros((slots, kv_heads, dim), dtype=torch.uint8, device=device)  # noqa: E731
+        scale = lambda: torch.ones((slots // block, kv_heads), device=device)  # noqa: E731
+        return cls(code(), code(), scale(), scale(), page_size, block)
+
+    def planes(self) -> list:
+        """The cache's tensors page by page, for KvPages."""
+        n = self.k.shape[0] // self.page_size
+        return [t.view(n, -1) for t in (self.k, self.v, self.k_scale, self.v_scale)]
+
+    def store(self, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+              token_table: torch.Tensor, block_table: torch.Tensor, stream=None) -> None:
+        """Quantises k, v [tokens, kv_heads, dim] (bf16 or fp16) into the cache."""
+        if k.shape != v.shape or k.dtype != v.dtype or k.shape[1:] != self.k.shape[1:]:
+            raise ValueError("k and v are [tokens, kv_heads, dim] of one type")
+        _rows(k, "k")
+        _rows(v, "v")
+        _int32(positions, (k.shape[0],), "positions")
+        _int32(token_table, (k.shape[0],), "token_table")
+        _table(block_table)
+        B.kv8_store(k, v, positions, token_table, block_table, self.page_size, self.block_tokens,
+                    self.k, self.v, self.k_scale, self.v_scale, self.status, stream)
+
+    def attention(self, q: torch.Tensor, lens: torch.Tensor, max_len: int,
+                  block_table: torch.Tensor, sm_scale: float, group_rows: int = 1,
+                  group_table: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Row t of q [rows, q_heads, dim] attends to positions [0, lens[t]) of its
+        group's block-table row. Returns (out, lse)."""
+        _rows(q, "q")
+        _int32(lens, (q.shape[0],), "lens")
+        _table(block_table)
+        groups = -(-q.shape[0] // max(1, group_rows))
+        if group_table is not None:
+            _int32(group_table, (groups,), "group_table")
+        with _on(stream):
+            out, lse = self._outputs(q, out, lse)
+        B.kv8_attention(q, sm_scale, lens, max_len, group_rows, group_table, block_table,
+                        self.page_size, self.block_tokens, self.k, self.v, self.k_scale,
+                        self.v_scale, out, lse, self._workspace(q, group_rows, stream),
+                        self.status, stream)
+        return out, lse
+
+    def attention_selected(self, q: torch.Tensor, slots: torch.Tensor, sm_scale: float,
+                           out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None,
+                           stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Row t of q attends to the slots of slots[t] (int32 [rows, k], negative ones
+        skipped): what PagedTopK.select returns. Returns (out, lse)."""
+        _rows(q, "q")
+        if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != q.shape[0]
+                or not _last_contiguous(slots)):
+            raise ValueError("slots is int32 [rows, k]")
+        with _on(stream):
+            out, lse = self._outputs(q, out, lse)
+        B.kv8_attention_selected(q, sm_scale, slots, self.block_tokens, self.k, self.v,
+                                 self.k_scale, self.v_scale, out, lse,
+                                 self._workspace(q, 1, stream), self.status, stream)
+        return out, lse
+
+    def _outputs(self, q, out, lse):
+        if q.shape[2] != self.k.shape[2]:
+            raise ValueError("q and the cache differ in dim")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out has q's shape and type")
+        else:
+            _rows(out, "out")
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        elif lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse is contiguous float32 [rows, q_heads]")
+        return out, lse
+
+    def _workspace(self, q, group_rows, stream):
+        handle = B._stream(stream)
+        key = (handle, q.shape[1], group_rows)
+        ws = self._workspaces.get(key)
+        if ws is None:
+            n = B.kv8_attention_workspace_bytes(q.shape[1], self.k.shape[1], q.shape[2],
+                                                group_rows)
+            with _on(stream):
+                ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+            self._workspaces[key] = ws
+        return ws
+
+
+class KvPages:
+    """Ownership of the pages of one or more paged tensors (include/kv_pages.h).
+
+    block_table  int32 [n_tables, table_ld]: -1 where a sequence has no page
+    refs         int32 [num_pages]: owners of each page, 0 of a free one
+    planes       the tensors that hold the pages' data, each [num_pages, ...]
+    All stay the caller's and are changed in place. One instance serves one stream at a
+    time. `status` collects the device status bits of all calls."""
+
+    def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
+                 planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
+        _table(block_table)
+        if not block_table.is_cuda:
+            raise ValueError("block_table is a CUDA tensor")
+        _int32(refs, (refs.numel(),), "refs")
+        self.block_table, self.refs, self.page_size = block_table, refs, int(page_size)
+        self.num_pages = refs.shape[0]
+        self.tensors = list(planes)  # keeps the planes' memory alive
+        self._planes = B.kvpages_planes(self.tensors, self.num_pages)
+        self.max_rows = int(max_rows)
+        dev = refs.device
+        self.workspace = torch.empty(B.kvpages_workspace_bytes(self.max_rows, self.num_pages),
+                                     dtype=torch.uint8, device=dev)
+        self.new_ids = torch.empty(self.num_pages, dtype=torch.int32, device=dev)
+        self.counts = torch.zeros(2, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def reserve(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
+                stream=None) -> None:
+        """Makes positions [old_lens[i], new_lens[i]) of rows[i] writable."""
+        n = rows.shape[0]
+        for t, name in ((rows, "rows"), (old_lens, "old_lens"), (new_lens, "new_lens")):
+            _int32(t, (n,), name)
+        if n > self.max_rows:
+            raise ValueError(f"more than max_rows = {self.max_rows} rows")
+        B.kvpages_reserve(rows, old_lens, new_lens, self.block_table, self.page_size, self.refs,
+                          self._planes, len(self.tensors), self.workspace, self.status, stream)
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
+             stream=None) -> None:
+        """children[i] shares the pages of the first lens[i] positions of parents[i]."""
+        n = parents.shape[0]
+        for t, name in ((parents, "parents"), (children, "children"), (lens, "lens")):
+            _int32(t, (n,), name)
+        B.kvpages_fork(parents, children, lens, self.block_table, self.page_size, self.refs,
+                       self.status, stream)
+
+    def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+        """rows[i] gives up its pages past the first keep_lens[i] positions (all of them)."""
+        _int32(rows, (rows.shape[0],), "rows")
+        if keep_lens is not None:
+            _int32(keep_lens, (rows.shape[0],), "keep_lens")
+        B.kvpages_free(rows, keep_lens, self.block_table, self.page_size, self.refs, self.status,
+                       stream)
+
+    def compact(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Moves the live pages into the lowest ids. Returns (new_ids, counts): the new id
+        of each page (-1 of a free one) and {live pages, pages moved}; both are this
+        instance's buffers, overwritten by the next call."""
+        B.kvpages_compact(self.block_table, self.refs, self._planes, len(self.tensors),
+                          self.new_ids, self.counts, self.workspace, self.status, stream)
+        return self.new_ids, self.counts
+
+    def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+        """Copies page src[i] to page dst[i] in every plane."""
+        n = src.shape[0]
+        _int32(src, (n,), "src")
+        _int32(dst, (n,), "dst")
+        B.kvpages_copy(src, dst, self.num_pages, self._planes, len(self.tensors), self.status,
+                       stream)
+
+
+def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor,
+                  uniforms: torch.Tensor, n_drafts: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Speculative sampling's verification (include/draft_verify.h): target float32 [reqs,
+    drafts + 1, vocab], draft float32 [reqs, drafts, vocab] or None (point masses), tokens
+    int32 [reqs, drafts], uniforms float32 [reqs, drafts + 1]. Returns (out_tokens [reqs,
+    drafts + 1], kept [reqs]): the kept drafts, one drawn token, then -1."""
+    _int32(tokens, tuple(tokens.shape), "tokens")
+    reqs, drafts = tokens.shape
+    if (target.dtype != torch.float32 or target.dim() != 3
+            or tuple(target.shape[:2]) != (reqs, drafts + 1) or not _last_contiguous(target)):
+        raise ValueError("target is float32 [reqs, drafts + 1, vocab]")
+    if draft is not None and (draft.dtype != torch.float32
+                              or tuple(draft.shape) != (reqs, drafts, target.shape[2])
+                              or not _last_contiguous(draft)):
+        raise ValueError("draft is float32 [reqs, drafts, vocab]")
+    if (uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (reqs, drafts + 1)
+            or not uniforms.is_contiguous()):
+        raise ValueError("uniforms is contiguous float32 [reqs, drafts + 1]")
+    if n_drafts is not None:
+        _int32(n_drafts, (reqs,), "n_drafts")
+    with _on(stream):
+        out = torch.empty((reqs, drafts + 1), dtype=torch.int32, device=tokens.device)
+        kept = torch.empty(reqs, dtype=torch.int32, device=tokens.device)
+    B.draft_verify(target, draft, tokens, uniforms, out, kept, n_drafts, status, stream)
+    return out, kept
+
+
+def _on(stream):
+    """Memory for work on `stream` comes from that stream's pool."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        if not int(stream):
+            return torch.cuda.stream(torch.cuda.default_stream())
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _int32(t: torch.Tensor, shape, name: str) -> None:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} is contiguous int32 {list(shape)}")
+
+
+def _rows(t: torch.Tensor, name: str) -> None:
+    """[rows, heads, dim] of bf16 / fp16 whose rows may be strided."""
+    if t.dtype not in (torch.bfloat16, torch.float16) or t.dim() != 3:
+        raise ValueError(f"{name} is bf16 or fp16 [rows, heads, dim]")
+    if t.numel() and (not _last_contiguous(t) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name}: a row's heads are contiguous")
+
+
+def _table(t: torch.Tensor) -> None:
+    # table_ld is a row's width as well as its stride
+    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("block_table is contiguous int32 [n_tables, table_ld]")
+
+
+def _last_contiguous(t: torch.Tensor) -> bool:
+    return t.shape[-1] <= 1 or t.numel() == 0 or t.stride(-1) == 1

@@ -34,6 +34,9 @@ EXPORTS = (
     "topk_status_str", "topk_grid_size", "topk_plan_host", "topk_layout_info",
     "topk_select_paged_noalloc", "indexer_k_prologue", "hisparse_resolve",
     "topk_select_paged_test", "indexer_mqa_logits", "hisparse_resolve_mtp",
+    "kv8_store", "kv8_attention", "kv8_attention_selected", "kv8_attention_workspace_bytes",
+    "kvpages_workspace_bytes", "kvpages_reserve", "kvpages_fork", "kvpages_free",
+    "kvpages_compact", "kvpages_copy", "draft_verify",
 )
 
 
@@ -79,6 +82,30 @@ _SIGS = {
                                         _c.c_int, _VP, _c.c_int64, _VP, _VP, _VP, _c.c_int,
                                         _c.c_int, _VP, _VP, _c.c_int64, _VP, _c.c_int64, _c.c_int,
                                         _VP, _VP, _VP, _VP]),
+    "kv8_store": (_c.c_int, [_VP, _c.c_int64, _VP, _c.c_int64, _c.c_int, _c.c_int, _c.c_int,
+                             _c.c_int, _VP, _VP, _VP, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
+                             _VP, _VP, _VP, _VP, _c.c_int64, _VP, _VP]),
+    "kv8_attention_workspace_bytes": (_c.c_int64, [_c.c_int, _c.c_int, _c.c_int, _c.c_int]),
+    "kv8_attention": (_c.c_int, [_VP, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                                 _c.c_int, _c.c_float, _VP, _c.c_int, _c.c_int, _VP, _VP,
+                                 _c.c_int, _c.c_int64, _c.c_int, _c.c_int, _VP, _VP, _VP, _VP,
+                                 _c.c_int64, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP, _VP]),
+    "kv8_attention_selected": (_c.c_int, [_VP, _c.c_int64, _c.c_int, _c.c_int, _c.c_int,
+                                          _c.c_int, _c.c_int, _c.c_float, _VP, _c.c_int,
+                                          _c.c_int64, _c.c_int, _VP, _VP, _VP, _VP, _c.c_int64,
+                                          _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP, _VP]),
+    "kvpages_workspace_bytes": (_c.c_size_t, [_c.c_int, _c.c_int]),
+    "kvpages_reserve": (_c.c_int, [_VP, _VP, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64, _c.c_int,
+                                   _VP, _c.c_int, _VP, _c.c_int, _VP, _c.c_size_t, _VP, _VP]),
+    "kvpages_fork": (_c.c_int, [_VP, _VP, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64, _c.c_int,
+                                _VP, _c.c_int, _VP, _VP]),
+    "kvpages_free": (_c.c_int, [_VP, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64, _c.c_int, _VP,
+                                _c.c_int, _VP, _VP]),
+    "kvpages_compact": (_c.c_int, [_VP, _c.c_int, _c.c_int64, _VP, _c.c_int, _VP, _c.c_int, _VP,
+                                   _VP, _VP, _c.c_size_t, _VP, _VP]),
+    "kvpages_copy": (_c.c_int, [_VP, _VP, _c.c_int, _c.c_int, _VP, _c.c_int, _VP, _VP]),
+    "draft_verify": (_c.c_int, [_VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64, _c.c_int64, _VP,
+                                _VP, _VP, _c.c_int, _c.c_int, _c.c_int, _VP, _VP, _VP, _VP]),
 }
 
 # include/hisparse_resolver.h
@@ -335,6 +362,231 @@ def hisparse_resolve_mtp(positions, block_table, page_size: int, token_to_hot, h
         _stream(stream))
     if code < 0:
         raise ResolverError(code)
+    return code
+
+
+# include/kv8_attention.h
+KV8_BF16 = 0
+KV8_FP16 = 1
+KV8_ERR_NULL = -1
+KV8_ERR_SHAPE = -2
+KV8_ERR_ALIGN = -3
+KV8_ERR_CUDA = -4
+KV8_ERR_WORKSPACE = -5
+KV8_STATUS_LEN = 1
+KV8_STATUS_TABLE_WIDTH = 2
+KV8_STATUS_TABLE_ENTRY = 4
+KV8_STATUS_SLOT = 8
+KV8_STATUS_TABLE_ROW = 16
+KV8_STATUS_POSITION = 32
+
+_KV8_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_FP16}
+
+
+class Kv8Error(RuntimeError):
+    def __init__(self, code: int, what: str):
+        super().__init__(f"{what}: {code}")
+        self.code = code
+
+
+def _kv8(code: int, what: str) -> int:
+    if code < 0:
+        raise Kv8Error(code, what)
+    return code
+
+
+def _ld(t) -> int:
+    """Stride of the first dimension; a lone row's may be anything, so its length."""
+    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else t.stride(0)
+
+
+def kv8_store(k, v, positions, token_table, block_table, page_size: int, block_tokens: int,
+              k_cache, v_cache, k_scale, v_scale, status=None, stream=None) -> int:
+    """kv8_store of include/kv8_attention.h on CUDA tensors: k, v bf16 / fp16 [tokens,
+    kv_heads, dim] (rows may be strided), positions / token_table int32 [tokens],
+    block_table int32 [n_tables, table_ld], caches uint8 [num_slots, kv_heads, dim],
+    scales float32 [num_slots / block_tokens, kv_heads], status int32 [1] or None.
+    Argument marshalling only."""
+    tokens, heads, dim = k.shape
+    return _kv8(lib().kv8_store(
+        _ptr(k), _ld(k), _ptr(v), _ld(v), _KV8_TYPES[k.dtype], tokens, heads, dim,
+        _ptr(positions), _ptr(token_table), _ptr(block_table), block_table.shape[0],
+        block_table.shape[1], page_size, block_tokens, _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(status), _stream(stream)),
+        "kv8_store")
+
+
+def kv8_attention_workspace_bytes(q_heads: int, kv_heads: int, dim: int,
+                                  group_rows: int) -> int:
+    return _kv8(lib().kv8_attention_workspace_bytes(int(q_heads), int(kv_heads), int(dim),
+                                                    int(group_rows)),
+                "kv8_attention_workspace_bytes")
+
+
+def kv8_attention(q, sm_scale: float, lens, max_len: int, group_rows: int, group_table,
+                  block_table, page_size: int, block_tokens: int, k_cache, v_cache, k_scale,
+                  v_scale, out, lse, workspace, status=None, stream=None) -> int:
+    """kv8_attention of include/kv8_attention.h on CUDA tensors: q and out bf16 / fp16
+    [rows, q_heads, dim] (rows may be strided), lens int32 [rows], group_table int32
+    [groups] or None, lse float32 [rows, q_heads] or None, the cache as in kv8_store.
+    Argument marshalling only."""
+    rows, heads, dim = q.shape
+    return _kv8(lib().kv8_attention(
+        _ptr(q), _ld(q), _KV8_TYPES[q.dtype], rows, heads, k_cache.shape[1], dim, sm_scale,
+        _ptr(lens), max_len, group_rows, _ptr(group_table), _ptr(block_table),
+        block_table.shape[0], block_table.shape[1], page_size, block_tokens, _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(out), _ld(out),
+        _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)), "kv8_attention")
+
+
+def kv8_attention_selected(q, sm_scale: float, slots, block_tokens: int, k_cache, v_cache,
+                           k_scale, v_scale, out, lse, workspace, status=None,
+                           stream=None) -> int:
+    """kv8_attention_selected of include/kv8_attention.h: slots int32 [rows, k], the rest
+    as in kv8_attention. Argument marshalling only."""
+    rows, heads, dim = q.shape
+    return _kv8(lib().kv8_attention_selected(
+        _ptr(q), _ld(q), _KV8_TYPES[q.dtype], rows, heads, k_cache.shape[1], dim, sm_scale,
+        _ptr(slots), slots.shape[1], _ld(slots), block_tokens, _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(out), _ld(out),
+        _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)), "kv8_attention_selected")
+
+
+# include/kv_pages.h
+KVPAGES_MAX_PLANES = 240
+KVPAGES_ERR_NULL = -1
+KVPAGES_ERR_SHAPE = -2
+KVPAGES_ERR_ALIGN = -3
+KVPAGES_ERR_CUDA = -4
+KVPAGES_ERR_WORKSPACE = -5
+KVPAGES_STATUS_ROW = 1
+KVPAGES_STATUS_LEN = 2
+KVPAGES_STATUS_PAGE = 4
+KVPAGES_STATUS_NO_PAGE = 8
+KVPAGES_STATUS_CHILD = 16
+KVPAGES_STATUS_REFS = 32
+
+
+class KvPlane(_c.Structure):
+    """kvpages_plane of include/kv_pages.h."""
+    _fields_ = [("base", _c.c_void_p), ("page_bytes", _c.c_int64)]
+
+
+class KvPagesError(RuntimeError):
+    def __init__(self, code: int, what: str):
+        super().__init__(f"{what}: {code}")
+        self.code = code
+
+
+def _kvp(code: int, what: str) -> int:
+    if code < 0:
+        raise KvPagesError(code, what)
+    return code
+
+
+def kvpages_workspace_bytes(n: int, num_pages: int) -> int:
+    return int(lib().kvpages_workspace_bytes(int(n), int(num_pages)))
+
+
+def kvpages_planes(tensors, num_pages: int):
+    """The plane array of the pages' tensors: CUDA tensors whose first dimension is a
+    page (num_pages of them) and whose rest is contiguous."""
+    planes = (KvPlane * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        if not t.is_cuda or t.shape[0] != num_pages or not t.is_contiguous():
+            raise ValueError("a plane is a contiguous CUDA tensor [num_pages, ...]")
+        planes[i].base = t.data_ptr()
+        planes[i].page_bytes = t[0].numel() * t.element_size() if num_pages else 4
+    return planes
+
+
+def kvpages_reserve(rows, old_lens, new_lens, block_table, page_size: int, refs, planes,
+                    n_planes: int, workspace, status=None, stream=None) -> int:
+    """kvpages_reserve of include/kv_pages.h: rows / old_lens / new_lens int32 [n],
+    block_table int32 [n_tables, table_ld] (contiguous), refs int32 [num_pages], planes
+    from kvpages_planes. Argument marshalling only."""
+    return _kvp(lib().kvpages_reserve(
+        _ptr(rows), _ptr(old_lens), _ptr(new_lens), rows.shape[0], _ptr(block_table),
+        block_table.shape[0], block_table.shape[1], page_size, _ptr(refs), refs.shape[0], planes,
+        n_planes, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)), "kvpages_reserve")
+
+
+def kvpages_fork(parents, children, lens, block_table, page_size: int, refs, status=None,
+                 stream=None) -> int:
+    """kvpages_fork of include/kv_pages.h (arguments as in kvpages_reserve)."""
+    return _kvp(lib().kvpages_fork(
+        _ptr(parents), _ptr(children), _ptr(lens), parents.shape[0], _ptr(block_table),
+        block_table.shape[0], block_table.shape[1], page_size, _ptr(refs), refs.shape[0],
+        _ptr(status), _stream(stream)), "kvpages_fork")
+
+
+def kvpages_free(rows, keep_lens, block_table, page_size: int, refs, status=None,
+                 stream=None) -> int:
+    """kvpages_free of include/kv_pages.h: keep_lens int32 [n] or None (keeps nothing)."""
+    return _kvp(lib().kvpages_free(
+        _ptr(rows), _ptr(keep_lens), rows.shape[0], _ptr(block_table), block_table.shape[0],
+        block_table.shape[1], page_size, _ptr(refs), refs.shape[0], _ptr(status),
+        _stream(stream)), "kvpages_free")
+
+
+def kvpages_compact(block_table, refs, planes, n_planes: int, new_ids, counts, workspace,
+                    status=None, stream=None) -> int:
+    """kvpages_compact of include/kv_pages.h: new_ids int32 [num_pages], counts int32 [2]
+    or None."""
+    return _kvp(lib().kvpages_compact(
+        _ptr(block_table), block_table.shape[0], block_table.shape[1], _ptr(refs),
+        refs.shape[0], planes, n_planes, _ptr(new_ids), _ptr(counts), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+        "kvpages_compact")
+
+
+def kvpages_copy(src, dst, num_pages: int, planes, n_planes: int, status=None,
+                 stream=None) -> int:
+    """kvpages_copy of include/kv_pages.h: src / dst int32 [n]."""
+    return _kvp(lib().kvpages_copy(_ptr(src), _ptr(dst), src.shape[0], num_pages, planes,
+                                   n_planes, _ptr(status), _stream(stream)), "kvpages_copy")
+
+
+# include/draft_verify.h
+VERIFY_MAX_DRAFTS = 31
+VERIFY_ERR_NULL = -1
+VERIFY_ERR_SHAPE = -2
+VERIFY_ERR_ALIGN = -3
+VERIFY_ERR_CUDA = -4
+VERIFY_STATUS_COUNT = 1
+VERIFY_STATUS_TOKEN = 2
+VERIFY_STATUS_PROB = 4
+VERIFY_STATUS_EMPTY = 8
+VERIFY_STATUS_UNIFORM = 16
+
+
+class VerifyError(RuntimeError):
+    def __init__(self, code: int):
+        super().__init__(f"draft_verify: {code}")
+        self.code = code
+
+
+def draft_verify(target, draft, tokens, uniforms, out_tokens, kept, n_drafts=None, status=None,
+                 stream=None) -> int:
+    """draft_verify of include/draft_verify.h on CUDA tensors: target float32 [reqs,
+    drafts + 1, vocab] and draft float32 [reqs, drafts, vocab] or None (last dimension
+    contiguous), tokens int32 [reqs, drafts], uniforms float32 [reqs, drafts + 1],
+    out_tokens int32 [reqs, drafts + 1], kept int32 [reqs], n_drafts int32 [reqs] or
+    None. Argument marshalling only."""
+    reqs, drafts = tokens.shape
+    vocab = target.shape[2]
+    # the stride of a dimension of one row may be anything
+    row = lambda t: t.stride(1) if t is not None and t.shape[1] > 1 else vocab  # noqa: E731
+    code = lib().draft_verify(
+        _ptr(target), target.stride(0), row(target), _ptr(draft),
+        draft.stride(0) if draft is not None else 0, row(draft),
+        _ptr(tokens), _ptr(n_drafts), _ptr(uniforms), reqs, drafts, vocab,
+        _ptr(out_tokens), _ptr(kept), _ptr(status), _stream(stream))
+    if code < 0:
+        raise VerifyError(code)
     return code
 
 

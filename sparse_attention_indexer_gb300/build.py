@@ -1,8 +1,7 @@
 """Builds the CUDA library libtopk_paged.so in-tree for sm_103a with nvcc.
 
-Ten translation units are compiled in parallel and linked into one shared library
-that exports the C ABI of include/topk_paged.h, include/indexer_prologue.h,
-include/indexer_logits.h and include/hisparse_resolver.h (no torch types cross it).
+The translation units are compiled in parallel and linked into one shared library that
+exports the C ABI of the headers in include/ (no torch types cross it).
 """
 from __future__ import annotations
 
@@ -18,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtopk_paged.so")
 SOURCES = ["select.cu", "short.cu", "medium.cu", "rowcluster.cu", "plan.cu", "abi.cu", "noalloc.cu",
-           "prologue.cu", "resolver.cu", "logits.cu"]
+           "prologue.cu", "resolver.cu", "logits.cu", "kv8_store.cu", "kv8_attention.cu",
+           "kv_pages.cu", "draft_verify.cu"]
 HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -53,7 +53,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", h)
                                                         for h in ("topk_paged.h", "indexer_prologue.h",
                                                                   "indexer_logits.h",
-                                                                  "hisparse_resolver.h")]
+                                                                  "hisparse_resolver.h",
+                                                                  "kv8_attention.h",
+                                                                  "kv_pages.h", "draft_verify.h")]
     objs = []
     jobs = []
     for src in SOURCES:
