@@ -1,7 +1,32 @@
 // Attention over the 8-bit paged KV cache (formulas and rules in include/kv8_attention.h).
 //
-// One CTA per query row and query head; its warps take the keys in turn with a running
-// maximum and sum each, and meet in shared memory. Lane l holds channels l * dim / 32 ...
+// Bound by HBM: a decode step reads 2 * dim bytes per key and head and does 4 * dim * M
+// operations on them, M = query rows of the group * query heads per key head (1 .. 128).
+//
+// Work split. A unit is a (group of query rows, key head): its M query rows attend to the
+// same keys. The units' tiles of 32 keys are laid end to end, and CTA i of N takes the tiles
+// [i * W / N, (i + 1) * W / N) of the W there are, whatever the lengths: the loads are even
+// for one long row and for a ragged batch alike, with no plan from the host. A unit that
+// several CTAs share is joined by the last of them to arrive, from partial sums in the
+// workspace, in the order of the CTAs (so the result does not depend on who is last).
+//
+// A tile. The four warps of a CTA form KW groups that take a segment's tiles in turn, WM warps to
+// a group, each with MT * 16 of the M rows. A group keeps kStages tiles of codes and scales
+// in flight with cp.async (a key that is masked or missing is filled with zeros and its
+// score set to -inf, so what lies there never enters). Products run on mma.sync m16n8k16
+// fp16 with fp32 accumulators; at M <= 128 rows and one pass over the keys they are not what
+// bounds the kernel, and the codes have to be widened on the way anyway:
+//   - q . k: an fp16 times an e4m3 (widened, exact) product is exact. Rows of bf16 q are
+//     brought to [2^14, 2^15) by a power of two, which fp16 then holds exactly but for
+//     channels 2^-38 below the row's largest. The channels may be summed in any order, so
+//     lane t of a quad takes 16 contiguous bytes of a key, one shared-memory load for four
+//     mma steps, and the query fragments are laid out to match.
+//   - p . v: ldmatrix.trans hands each lane pairs of channels of two keys; one byte
+//     permutation sorts them into the two fragments of the even and the odd channels.
+//   - the value scale of a block is folded into its weights before these are rounded to
+//     fp16: w' = 2^(x + log2 sv - M), M the running maximum of x + log2 sv. With the
+//     largest w' at 1, a block of small weights and large values loses no more than one of large weights
+//     and small values. The sum of the weights keeps its own maximum m.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -9,18 +34,25 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv8_attention.h"
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 32;   // keys of a tile
+constexpr int kStages = 3;  // tiles in flight per warp group
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 2048;
 
 struct Params {
   const uint16_t* q;
   int64_t q_ld;
   int q_heads, kv_heads;
   float scale;  // sm_scale * log2(e)
+  int rows;
   const int32_t* lens;
   int max_len;
   int group_rows;
@@ -29,9 +61,11 @@ struct Params {
   int n_tables;
   int64_t table_ld;
   int page_size;
+  int page_shift;  // log2 where a power of two, else -1
   const int32_t* slots;  // the selected form: slots[row * slots_ld + i], i < max_len
   int64_t slots_ld;
   int block;
+  int block_shift;
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
   int64_t num_slots;
@@ -39,99 +73,712 @@ struct Params {
   int64_t out_ld;
   float* lse;
   int32_t* status;
+  int32_t* counters;  // workspace: arrivals at a shared unit, by its first CTA
+  float* parts;       // workspace: two partial results per CTA
 };
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-template <int DIM, bool FP16, bool SELECTED>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attention_kernel(Params p) {
-  constexpr int E = DIM / 32;
-  const int row = blockIdx.x, head = blockIdx.y, tid = threadIdx.x;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int h = head / (p.q_heads / p.kv_heads);
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][DIM];
-  int err = 0, len = p.max_len, table = 0;
-  if (!SELECTED) {
-    len = p.lens[row];
-    const int g = row / p.group_rows;
-    table = p.group_table ? p.group_table[g] : g;
-    if (len < 0 || len > p.max_len) {
-      err |= KV8_STATUS_LEN;
-      len = 0;
-    } else if (table < 0 || table >= p.n_tables) {
-      err |= KV8_STATUS_TABLE_ROW;
-      len = 0;
-    } else if (((int64_t)len + p.page_size - 1) / p.page_size > p.table_ld) {
-      err |= KV8_STATUS_TABLE_WIDTH;
-      len = 0;
+// 16 / 4 bytes to shared memory, zeros where !in (the source is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ldmatrix_trans(uint32_t a) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Two e4m3 codes (low 16 bits) as two fp16: exact.
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------ layout in shared memory
+template <int DIM, int MT, int WM>
+struct Smem {
+  static constexpr int kGroups = kWarps / WM;
+  static constexpr int kRows = 16 * MT * WM;
+  static constexpr int kTile = kKeys * DIM;  // bytes of the K (or V) codes of a tile
+  static constexpr int kRing = kGroups * kStages * 2 * kTile;
+  static constexpr int kJoin = kWarps * 16 * MT * DIM * 4;  // the warps' sums, over the ring
+  static constexpr int kQ = (kRing > kJoin ? kRing : kJoin);
+  static constexpr int kScale = kQ + kRows * DIM * 2;
+  static constexpr int kMask = kScale + kGroups * kStages * 2 * kKeys * 4;
+  static constexpr int kStat = kMask + ((kGroups * kStages * 4 + 15) & ~15);  // m, M, l
+  static constexpr int kMul = kStat + kGroups * kRows * 3 * 4;
+  static constexpr int kLen = kMul + kRows * 4;
+  static constexpr int kTotal = kLen + kRows * 4;
+};
+
+// A row of codes is DIM / 16 pieces of 16 bytes, permuted so that both the reads of q . k (4
+// pieces of each of 8 keys) and those of p . v (one piece of 8 keys) meet every bank once.
+template <int DIM>
+__device__ __forceinline__ int piece_at(int key, int piece) {
+  if (DIM == 128) return key * 128 + ((piece ^ (key & 7)) << 4);
+  return (key >> 1) * 128 + ((((key & 1) * 4 + piece) ^ ((key >> 1) & 3)) << 4);
+}
+
+// ------------------------------------------------------------------ lengths
+// Keys that group g attends to at most: the largest length of its rows that pass the checks;
+// len_of(row) is 0 for one that does not. `err` collects what is wrong.
+__device__ __forceinline__ int row_len(const Params& p, int row, int table, int* err) {
+  const int len = __ldg(p.lens + row);
+  if (len < 0 || len > p.max_len) {
+    *err |= KV8_STATUS_LEN;
+    return 0;
+  }
+  if (table < 0 || table >= p.n_tables) {
+    *err |= KV8_STATUS_TABLE_ROW;
+    return 0;
+  }
+  if ((int64_t)len > p.table_ld * p.page_size) {
+    *err |= KV8_STATUS_TABLE_WIDTH;
+    return 0;
+  }
+  return len;
+}
+
+__device__ __forceinline__ int group_len(const Params& p, int g, int* err) {
+  const int table = p.group_table ? __ldg(p.group_table + g) : g;
+  int len = 0;
+  const int64_t r0 = (int64_t)g * p.group_rows;
+  for (int i = 0; i < p.group_rows && r0 + i < p.rows; ++i)
+    len = max(len, row_len(p, (int)(r0 + i), table, err));
+  return len;
+}
+
+// A unit has at least one tile, so that rows without keys are written too.
+__device__ __forceinline__ int tiles_of(int len) {
+  return max(1, (int)(((uint32_t)len + kKeys - 1) / kKeys));
+}
+
+// 0xFF in each byte that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
+  return __vcmpeq4(c & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// ------------------------------------------------------------------ kernel
+template <int DIM, bool FP16, bool SELECTED, int MT, int WM>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+kv8_attention_kernel(const __grid_constant__ Params p) {
+  using L = Smem<DIM, MT, WM>;
+  constexpr int kGroups = L::kGroups, kRows = L::kRows;
+  constexpr int kPieces = DIM / 16;   // 16-byte pieces of a row of codes
+  constexpr int kSteps = DIM / 16;    // mma steps of q . k
+  constexpr int kOut = DIM / 8;       // mma tiles of p . v
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_sum[kThreads];
+  __shared__ int64_t s_first;
+  __shared__ int s_group, s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kg = warp / WM, wm = warp % WM;
+  const int quad = lane >> 2, t = lane & 3;
+  const int ratio = p.q_heads / p.kv_heads;
+  const int groups = SELECTED ? p.rows : (p.rows + p.group_rows - 1) / p.group_rows;
+  const int live = (SELECTED ? 1 : p.group_rows) * ratio;  // rows of a unit, <= kRows
+  int err = 0;
+
+  // ---- this CTA's tiles [w0, w1) and the unit of the first
+  int64_t all, first_tile = 0;  // tiles of the launch; first tile of the unit at hand
+  int g = 0, h = 0, len = p.max_len;
+  int64_t w0, w1;
+  int64_t n = gridDim.x;  // CTAs that take part: each gets a tile for each of its warp groups
+  const int64_t me = blockIdx.x;
+  if (SELECTED) {
+    const int64_t tiles = tiles_of(len);
+    all = tiles * groups * p.kv_heads;
+    n = min(n, (all + kGroups - 1) / kGroups);
+    w0 = me * all / n;
+    w1 = me < n ? (me + 1) * all / n : w0;
+    const int64_t u = w0 / tiles;
+    g = (int)(u / p.kv_heads);
+    h = (int)(u % p.kv_heads);
+    first_tile = u * tiles;
+  } else {
+    const int per = (groups + kThreads - 1) / kThreads;
+    const int64_t g0 = min((int64_t)groups, (int64_t)tid * per);
+    const int64_t g1 = min((int64_t)groups, g0 + per);
+    int64_t mine = 0;
+    for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len(p, (int)i, &err));
+    if (me) err = 0;  // CTA 0 reports for all
+    s_sum[tid] = mine;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < kThreads; ++i) {
+      const int64_t x = s_sum[i];
+      if (i < tid) before += x;
+      total += x;
     }
-  }
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < E; ++i) {
-    const uint16_t b = p.q[row * p.q_ld + (int64_t)head * DIM + lane * E + i];
-    q[i] = FP16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
-    o[i] = 0.0f;
-  }
-  for (int i = warp; i < len; i += kWarps) {
-    int64_t slot;
-    if (SELECTED) {
-      slot = p.slots[row * p.slots_ld + i];
-      if (slot < 0) continue;
-    } else {
-      const int32_t page = p.block_table[table * p.table_ld + i / p.page_size];
-      if (page < 0) {
-        err |= KV8_STATUS_TABLE_ENTRY;
-        continue;
+    all = total * p.kv_heads;
+    n = min(n, (all + kGroups - 1) / kGroups);
+    w0 = me * all / n;
+    w1 = me < n ? (me + 1) * all / n : w0;
+    if (w0 < w1 && w0 >= before * p.kv_heads && w0 < (before + mine) * p.kv_heads) {
+      int ignored = 0;
+      int64_t i = g0, at = before * p.kv_heads;
+      for (;; ++i) {
+        const int64_t here = (int64_t)tiles_of(group_len(p, (int)i, &ignored)) * p.kv_heads;
+        if (w0 < at + here) break;
+        at += here;
       }
-      slot = (int64_t)page * p.page_size + i % p.page_size;
+      s_group = (int)i;
+      s_first = at;
     }
-    if (slot >= p.num_slots) {
-      err |= KV8_STATUS_SLOT;
-      continue;
+    __syncthreads();
+    if (w0 < w1) {
+      int ignored = 0;
+      g = s_group;
+      first_tile = s_first;
+      len = group_len(p, g, &ignored);
+      const int tiles = tiles_of(len);
+      h = (int)((w0 - first_tile) / tiles);
+      first_tile += (int64_t)h * tiles;
     }
-    const int64_t at = (slot * p.kv_heads + h) * DIM + lane * E;
-    const int64_t sc = (slot / p.block) * p.kv_heads + h;
-    float x = 0.0f;
-    for (int e = 0; e < E; ++e)
-      x += q[e] * __half2float(__half(__nv_cvt_fp8_to_halfraw(p.k[at + e], __NV_E4M3)));
-    x = warp_sum(x) * p.scale * p.k_scale[sc];
-    const float top = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
-    const float w = x == -INFINITY ? 0.0f : exp2f(x - top);
-    const float sv = p.v_scale[sc];
-    m = top;
-    l = l * keep + w;
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * keep +
-             w * sv * __half2float(__half(__nv_cvt_fp8_to_halfraw(p.v[at + e], __NV_E4M3)));
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  if (tid < DIM) {
-    float top = -INFINITY, sum = 0.0f, val = 0.0f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - top);
-      sum += s_l[w] * f;
-      if (f != 0.0f) val += s_o[w][tid] * f;
+
+  const uint32_t ring = smem_u32(smem) + kg * kStages * 2 * L::kTile;
+  const uint32_t scales = smem_u32(smem + L::kScale) + kg * kStages * 2 * kKeys * 4;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::kMask) + kg * kStages;
+  float* s_stat = reinterpret_cast<float*>(smem + L::kStat);
+  float* s_mul = reinterpret_cast<float*>(smem + L::kMul);
+  int* s_len = reinterpret_cast<int*>(smem + L::kLen);
+
+  int64_t w = w0;
+  while (w < w1) {
+    const int tiles = tiles_of(len);
+    const int tile0 = (int)(w - first_tile);
+    const int tile1 = (int)min((int64_t)tiles, w1 - first_tile);
+    const int table = SELECTED ? 0 : p.group_table ? __ldg(p.group_table + g) : g;
+
+    // ---- keys of a tile: this lane's key is tile * 32 + lane
+    auto slot_of = [&](int tile) -> int {
+      const int64_t i = (int64_t)tile * kKeys + lane;
+      if (tile >= tile1 || i >= len) return -1;
+      int64_t slot;
+      if (SELECTED) {
+        slot = __ldg(p.slots + g * p.slots_ld + i);
+        if (slot < 0) return -1;
+      } else {
+        const int pos = (int)i;
+        const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+        const int32_t page = __ldg(p.block_table + table * p.table_ld + pg);
+        if (page < 0) {
+          err |= KV8_STATUS_TABLE_ENTRY;
+          return -1;
+        }
+        slot = (int64_t)page * p.page_size + (pos - pg * p.page_size);
+      }
+      if (slot >= p.num_slots) {
+        err |= KV8_STATUS_SLOT;
+        return -1;
+      }
+      return (int)slot;
+    };
+    auto issue = [&](int stage, int slot) {
+      const uint32_t k_at = ring + stage * 2 * L::kTile, v_at = k_at + L::kTile;
+      constexpr int kKeysPerPass = 32 / kPieces;
+      constexpr int kPasses = kKeys / kKeysPerPass / WM;
+      const int piece = lane % kPieces;
+#pragma unroll
+      for (int j = 0; j < kPasses; ++j) {
+        const int key = (j * WM + wm) * kKeysPerPass + lane / kPieces;
+        const int s = __shfl_sync(0xffffffffu, slot, key);
+        const int64_t off = ((int64_t)max(s, 0) * p.kv_heads + h) * DIM + piece * 16;
+        const int at = piece_at<DIM>(key, piece);
+        copy16(k_at + at, p.k + off, s >= 0);
+        copy16(v_at + at, p.v + off, s >= 0);
+      }
+      if (wm == 0) {
+        const int sl = max(slot, 0);
+        const int b = p.block_shift >= 0 ? sl >> p.block_shift : sl / p.block;
+        const int64_t off = (int64_t)b * p.kv_heads + h;
+        const uint32_t at = scales + (stage * 2 * kKeys + lane) * 4;
+        copy4(at, p.k_scale + off, slot >= 0);
+        copy4(at + kKeys * 4, p.v_scale + off, slot >= 0);
+        const uint32_t in = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0) masks[stage] = in;
+      }
+    };
+
+    // ---- first tiles on their way
+    int next = tile0 + kg;  // the tile that is issued next
+    int slot = slot_of(next);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      issue(i, slot);
+      copy_commit();
+      next += kGroups;
+      slot = slot_of(next);
     }
-    val = sum == 0.0f ? 0.0f : val / sum;
-    p.out[row * p.out_ld + (int64_t)head * DIM + tid] =
-        FP16 ? __half_as_ushort(__float2half_rn(val))
-             : __bfloat16_as_ushort(__float2bfloat16_rn(val));
-    if (tid == 0 && p.lse)
-      p.lse[(int64_t)row * p.q_heads + head] =
-          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+
+    // ---- queries: row r of the unit is row r / ratio of the group, head r % ratio of h's
+    for (int x = tid; x < kRows * kPieces; x += kThreads) {
+      const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
+      const int row = g * (SELECTED ? 1 : p.group_rows) + r / ratio;
+      const bool in = r < live && row < p.rows;
+      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (in) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + row * p.q_ld + (int64_t)(h * ratio + r % ratio) * DIM + c * 16);
+        v[0] = __ldg(src);
+        v[1] = __ldg(src + 1);
+      }
+      uint32_t wds[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      float mul = p.scale;
+      if (!FP16) {
+        uint32_t top = 0;  // largest magnitude bits of the row
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top = max(top, max(wds[i] & 0x7FFFu, (wds[i] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = kPieces / 2; o; o >>= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^up brings the row's largest magnitude into [2^14, 2^15)
+        const int e = (int)(top >> 7);  // biased exponent
+        const int up = e == 255 || top == 0 ? 0 : min(126, 14 - (e - 127));
+        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+        mul *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          wds[i] = pack_half(__uint_as_float(wds[i] << 16) * f,
+                             __uint_as_float(wds[i] & 0xFFFF0000u) * f);
+      }
+      // fragment of step s of 64 channels: lane (r % 8) * 4 + t holds channels 16 t + 4 s ..
+      const int half = c >> 2, tt = c & 3;
+      uint8_t* base = smem + L::kQ + (r >> 4) * (kSteps * 512) + ((r & 7) * 4 + tt) * 16 +
+                      ((r >> 3) & 1) * 8;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        *reinterpret_cast<uint2*>(base + (half * 4 + s) * 512) =
+            make_uint2(wds[2 * s], wds[2 * s + 1]);
+      if (c == 0) {
+        int ignored = 0;
+        s_mul[r] = mul;
+        // only rows that end before the unit's keys do need the comparison with their length
+        s_len[r] = !in || SELECTED ? INT32_MAX : row_len(p, row, table, &ignored);
+      }
+    }
+    __syncthreads();
+
+    const int row0 = wm * 16 * MT;  // this warp's rows
+    float mul[MT][2];
+    int lim[MT][2], least = INT32_MAX;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        mul[i][b] = s_mul[row0 + i * 16 + b * 8 + quad];
+        lim[i][b] = s_len[row0 + i * 16 + b * 8 + quad];
+        least = min(least, lim[i][b]);
+      }
+    float o[MT][kOut][4];
+    float m[MT][2], mv[MT][2], sum[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int j = 0; j < kOut; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        m[i][b] = mv[i][b] = -INFINITY;
+        sum[i][b] = 0.0f;
+      }
+    }
+
+    int stage = 0;
+    for (int tile = tile0 + kg; tile < tile1; tile += kGroups) {
+      copy_wait<kStages - 2>();
+      // the group's warps see this tile, and are done with the one that the next copy replaces
+      if (WM == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * WM) : "memory");
+      issue(stage == 0 ? kStages - 1 : stage - 1, slot);
+      copy_commit();
+      next += kGroups;
+      slot = slot_of(next);
+
+      const uint32_t k_at = ring + stage * 2 * L::kTile, v_at = k_at + L::kTile;
+      float s[MT][4][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[i][j][c] = 0.0f;
+#pragma unroll
+      for (int half = 0; half < DIM / 64; ++half) {
+        uint4 kr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kr[j] = lds128(k_at + piece_at<DIM>(j * 8 + quad, half * 4 + t));
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          uint4 a[MT];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            a[i] = lds128(smem_u32(smem + L::kQ) +
+                          ((wm * MT + i) * kSteps + half * 4 + st) * 512 + lane * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t c = st == 0 ? kr[j].x : st == 1 ? kr[j].y : st == 2 ? kr[j].z : kr[j].w;
+            const uint32_t b0 = widen2(c), b1 = widen2(c >> 16);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) mma(s[i][j], a[i].x, a[i].z, a[i].y, a[i].w, b0, b1);
+          }
+        }
+      }
+
+      // ---- scores to weights: x = acc * mul * key scale (log2 units), xv = x + log2 sv
+      const uint32_t in = masks[stage];
+      float lv[4][2];
+      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) +
+                        (kg * kStages + stage) * 2 * kKeys;
+      // some row of this warp ends inside this tile or before it
+      const bool ragged = __any_sync(0xffffffffu, (int64_t)(tile + 1) * kKeys > least);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 ks = *reinterpret_cast<const float2*>(sc + j * 8 + 2 * t);
+        const float2 vs = *reinterpret_cast<const float2*>(sc + kKeys + j * 8 + 2 * t);
+        lv[j][0] = log2_fast(vs.x);
+        lv[j][1] = log2_fast(vs.y);
+        const float out0 = (in >> (j * 8 + 2 * t)) & 1 ? 0.0f : -INFINITY;
+        const float out1 = (in >> (j * 8 + 2 * t + 1)) & 1 ? 0.0f : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            s[i][j][2 * b] = fmaf(s[i][j][2 * b] * mul[i][b], ks.x, out0);
+            s[i][j][2 * b + 1] = fmaf(s[i][j][2 * b + 1] * mul[i][b], ks.y, out1);
+          }
+      }
+      if (ragged) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int64_t pos = (int64_t)tile * kKeys + j * 8 + 2 * t + c;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (pos >= lim[i][b]) s[i][j][2 * b + c] = -INFINITY;
+          }
+      }
+      uint32_t pa[MT][2][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        float keep[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float tm = -INFINITY, tv = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tm = fmaxf(tm, s[i][j][2 * b + c]);
+              tv = fmaxf(tv, s[i][j][2 * b + c] + lv[j][c]);  // NaN is no maximum
+            }
+#pragma unroll
+          for (int x = 1; x <= 2; x <<= 1) {
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
+            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
+          }
+          tm = fmaxf(tm, m[i][b]);
+          tv = fmaxf(tv, mv[i][b]);
+          // a row that has no key yet keeps -inf; 0 stands in for it in the differences
+          const float um = tm == -INFINITY ? 0.0f : tm, uv = tv == -INFINITY ? 0.0f : tv;
+          sum[i][b] *= exp2_fast(m[i][b] - um);
+          keep[b] = exp2_fast(mv[i][b] - uv);
+          m[i][b] = tm;
+          mv[i][b] = tv;
+          float add = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float wv[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float x = s[i][j][2 * b + c];
+              add += exp2_fast(x - um);
+              // a key outside the row weighs 0, whatever the scale of its block is
+              wv[c] = x == -INFINITY ? 0.0f : exp2_fast(x + lv[j][c] - uv);
+            }
+            pa[i][j >> 1][(j & 1) * 2 + b] = pack_half(wv[0], wv[1]);
+          }
+          sum[i][b] += add;
+        }
+        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+          for (int j = 0; j < kOut; ++j) {
+            o[i][j][0] *= keep[0];
+            o[i][j][1] *= keep[0];
+            o[i][j][2] *= keep[1];
+            o[i][j][3] *= keep[1];
+          }
+        }
+      }
+      // ---- weights times values
+      auto add_values = [&](auto clean) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const int key = kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+          for (int cp = 0; cp < kPieces / 2; ++cp) {
+            const uint4 r = ldmatrix_trans(v_at + piece_at<DIM>(key, cp * 2 + (lane >> 4)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // bytes: (key 2t, channels 2n, 2n + 1), (key 2t + 1, the same)
+              uint32_t x = __byte_perm(e ? r.z : r.x, 0, 0x3120);
+              uint32_t y = __byte_perm(e ? r.w : r.y, 0, 0x3120);
+              if (decltype(clean)::value) {
+                x &= ~nan_codes(x);
+                y &= ~nan_codes(y);
+              }
+              const uint32_t b0 = widen2(x), b1 = widen2(y);
+              const uint32_t c0 = widen2(x >> 16), c1 = widen2(y >> 16);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                mma(o[i][cp * 4 + e * 2], pa[i][kk][0], pa[i][kk][1], pa[i][kk][2], pa[i][kk][3],
+                    b0, b1);
+                mma(o[i][cp * 4 + e * 2 + 1], pa[i][kk][0], pa[i][kk][1], pa[i][kk][2],
+                    pa[i][kk][3], c0, c1);
+              }
+            }
+          }
+        }
+      };
+      // A NaN code must not reach the rows that end before it (0 * NaN is NaN in a product).
+      // Only a tile in which a row ends can hold one that some rows see and others do not.
+      bool dirty = false;
+      if (ragged) {
+        uint32_t nan = 0;
+#pragma unroll
+        for (int j = 0; j < L::kTile / 512; ++j) {
+          const uint4 c = lds128(v_at + (j * 32 + lane) * 16);
+          nan |= nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w);
+        }
+        dirty = __any_sync(0xffffffffu, nan != 0);
+      }
+      if (!dirty) {
+        add_values(std::false_type());
+      } else {
+        add_values(std::true_type());
+        for (int key = 0; key < kKeys; ++key) {
+          const int64_t pos = (int64_t)tile * kKeys + key;
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) {  // this thread's channels: 16 c + 4 t ..
+            uint32_t codes;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(codes)
+                         : "r"(v_at + piece_at<DIM>(key, c) + 4 * t));
+            const uint32_t nan = nan_codes(codes);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              if ((nan >> (8 * d)) & 1)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int b = 0; b < 2; ++b)
+                    if (pos < lim[i][b]) o[i][2 * c + (d & 1)][2 * b + (d >> 1)] = NAN;
+          }
+        }
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    __syncthreads();  // the ring is free: it takes the warps' sums
+
+    // ---- join the warp groups
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float x = sum[i][b];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const int r = row0 + i * 16 + b * 8 + quad;
+        if (t == 0) {
+          float* st = s_stat + (kg * kRows + r) * 3;
+          st[0] = m[i][b];
+          st[1] = mv[i][b];
+          st[2] = x;
+        }
+        float4* dst = reinterpret_cast<float4*>(smem) + (kg * kRows + r) * (DIM / 4) + t;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c)
+          dst[c * 4] = make_float4(o[i][2 * c][2 * b], o[i][2 * c + 1][2 * b],
+                                   o[i][2 * c][2 * b + 1], o[i][2 * c + 1][2 * b + 1]);
+      }
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == tiles;
+    // CTAs a .. b share the unit
+    const int64_t a = ((first_tile + 1) * n - 1) / all, b = ((first_tile + tiles) * n - 1) / all;
+    constexpr int kPart = kRows * (DIM + 4);
+    auto part_of = [&](int64_t cta) { return p.parts + (cta == a ? 2 * cta + 1 : 2 * cta) * kPart; };
+    auto write_row = [&](int r, int c4, float4 v, float top, float topv, float l) {
+      // v is relative to 2^topv, l to 2^top
+      const bool none = l == 0.0f;  // no key: one that counts adds 1 to l, a NaN makes it NaN
+      const float f = none ? 0.0f : exp2f(topv - top) / l;
+      const int row = g * (SELECTED ? 1 : p.group_rows) + r / ratio;
+      if (row >= p.rows) return;
+      const int head = h * ratio + r % ratio;
+      uint2 packed;
+      const float x[4] = {none ? 0.0f : v.x * f, none ? 0.0f : v.y * f, none ? 0.0f : v.z * f,
+                          none ? 0.0f : v.w * f};
+      if (FP16) {
+        packed = make_uint2(pack_half(x[0], x[1]), pack_half(x[2], x[3]));
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
+        packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                            *reinterpret_cast<const uint32_t*>(&hi));
+      }
+      *reinterpret_cast<uint2*>(p.out + row * p.out_ld + (int64_t)head * DIM + c4 * 4) = packed;
+      if (c4 == 0 && p.lse)
+        p.lse[(int64_t)row * p.q_heads + head] =
+            none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+    };
+    float* part = whole ? nullptr : part_of(me);
+    for (int x = tid; x < live * (DIM / 4); x += kThreads) {
+      const int r = x / (DIM / 4), c4 = x % (DIM / 4);
+      float top = -INFINITY, topv = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        top = fmaxf(top, s_stat[(k * kRows + r) * 3]);
+        topv = fmaxf(topv, s_stat[(k * kRows + r) * 3 + 1]);
+      }
+      const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const float* st = s_stat + (k * kRows + r) * 3;
+        l += st[2] * exp2_fast(st[0] - ut);
+        const float f = exp2_fast(st[1] - uv);
+        const float4 y = reinterpret_cast<const float4*>(smem)[(k * kRows + r) * (DIM / 4) + c4];
+        v.x += y.x * f;
+        v.y += y.y * f;
+        v.z += y.z * f;
+        v.w += y.w * f;
+      }
+      if (whole) {
+        write_row(r, c4, v, top, topv, l);
+      } else {
+        reinterpret_cast<float4*>(part)[r * (DIM / 4) + c4] = v;
+        if (c4 == 0) {
+          float* st = part + kRows * DIM + r * 4;
+          st[0] = top;
+          st[1] = topv;
+          st[2] = l;
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int before = atomicAdd(p.counters + a, 1);
+        s_last = before == (int)(b - a);
+        if (s_last) p.counters[a] = 0;  // as the next call needs it
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int x = tid; x < live * (DIM / 4); x += kThreads) {
+          const int r = x / (DIM / 4), c4 = x % (DIM / 4);
+          float top = -INFINITY, topv = -INFINITY, l = 0.0f;
+          for (int64_t c = a; c <= b; ++c) {
+            const float4 st = __ldcg(reinterpret_cast<const float4*>(part_of(c) + kRows * DIM) + r);
+            top = fmaxf(top, st.x);
+            topv = fmaxf(topv, st.y);
+          }
+          const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
+          float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+          for (int64_t c = a; c <= b; ++c) {
+            const float* q = part_of(c);
+            const float4 st = __ldcg(reinterpret_cast<const float4*>(q + kRows * DIM) + r);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(q) + r * (DIM / 4) + c4);
+            l += st.z * exp2_fast(st.x - ut);
+            const float f = exp2_fast(st.y - uv);
+            v.x += y.x * f;
+            v.y += y.y * f;
+            v.z += y.z * f;
+            v.w += y.w * f;
+          }
+          write_row(r, c4, v, top, topv, l);
+        }
+      }
+    }
+    __syncthreads();  // the shared arrays are free for the next unit
+
+    // ---- next unit
+    w = first_tile + tile1;
+    if (tile1 == tiles) {
+      first_tile += tiles;
+      if (++h == p.kv_heads) {
+        h = 0;
+        ++g;
+        int ignored = 0;
+        if (!SELECTED && w < w1) len = group_len(p, g, &ignored);
+      }
+    }
   }
-  if (err && lane == 0 && p.status) atomicOr(p.status, err);
+  if (err && p.status) atomicOr(p.status, err);
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
@@ -164,21 +811,109 @@ int check_common(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, 
   return KV8_OK;
 }
 
-template <bool SELECTED>
-int launch(const Params& p, int rows, int dim, int dtype, cudaStream_t s) {
-  const dim3 grid((unsigned)rows, (unsigned)p.q_heads);
-  if (dim == 128) {
-    if (dtype == KV8_FP16)
-      kv8_attention_kernel<128, true, SELECTED><<<grid, kWarps * 32, 0, s>>>(p);
-    else
-      kv8_attention_kernel<128, false, SELECTED><<<grid, kWarps * 32, 0, s>>>(p);
-  } else {
-    if (dtype == KV8_FP16)
-      kv8_attention_kernel<64, true, SELECTED><<<grid, kWarps * 32, 0, s>>>(p);
-    else
-      kv8_attention_kernel<64, false, SELECTED><<<grid, kWarps * 32, 0, s>>>(p);
-  }
+// CTAs of a launch on the current device, or < 0.
+int grid_size() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return -1;
+  return sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+}
+
+// Rows that the variant for a unit of `live` rows pads to.
+int padded_rows(int live) { return live <= 16 ? 16 : live <= 32 ? 32 : live <= 64 ? 64 : 128; }
+
+int shift_of(int x) {
+  if (x & (x - 1)) return -1;
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+template <int DIM, bool FP16, bool SELECTED, int MT, int WM>
+int launch(const Params& p, int grid, cudaStream_t s) {
+  using L = Smem<DIM, MT, WM>;
+  const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, MT, WM>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) !=
+      cudaSuccess)
+    return KV8_ERR_CUDA;
+  kernel<<<(unsigned)grid, kThreads, L::kTotal, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
+}
+
+template <int DIM, bool FP16, bool SELECTED>
+int launch_rows(const Params& p, int live, int grid, cudaStream_t s) {
+  switch (padded_rows(live)) {
+    case 16: return launch<DIM, FP16, SELECTED, 1, 1>(p, grid, s);
+    case 32: return launch<DIM, FP16, SELECTED, 2, 1>(p, grid, s);
+    case 64: return launch<DIM, FP16, SELECTED, 2, 2>(p, grid, s);
+    default: return launch<DIM, FP16, SELECTED, 2, 4>(p, grid, s);
+  }
+}
+
+// The selected form has at most 16 rows to a unit.
+template <int DIM, bool FP16>
+int launch_rows_selected(const Params& p, int grid, cudaStream_t s) {
+  return launch<DIM, FP16, true, 1, 1>(p, grid, s);
+}
+
+Params common(const void* q, int64_t q_ld, int rows, int q_heads, int kv_heads, float sm_scale,
+              int block_tokens, const uint8_t* k_cache, const uint8_t* v_cache,
+              const float* k_scale, const float* v_scale, int64_t num_slots, void* out,
+              int64_t out_ld, float* lse, int32_t* status) {
+  Params p = {};
+  p.q = (const uint16_t*)q;
+  p.q_ld = q_ld;
+  p.rows = rows;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.scale = sm_scale * 1.44269504088896341f;
+  p.block = block_tokens;
+  p.block_shift = shift_of(block_tokens);
+  p.k = k_cache;
+  p.v = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_slots = num_slots;
+  p.out = (uint16_t*)out;
+  p.out_ld = out_ld;
+  p.lse = lse;
+  p.status = status;
+  return p;
+}
+
+// Fills in the workspace and launches the variant for these sizes.
+template <bool SELECTED>
+int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaStream_t s) {
+  const int rows = SELECTED ? 1 : p.group_rows;
+  const int64_t need = kv8_attention_workspace_bytes(p.q_heads, p.kv_heads, dim, rows);
+  if (need < 0) return (int)need;
+  if (ws_bytes < need) return KV8_ERR_WORKSPACE;
+  const int most = grid_size();
+  if (most < 0) return KV8_ERR_CUDA;
+  // one tile for each warp of a CTA at least, where there is that little work
+  const int64_t groups = ((int64_t)p.rows + rows - 1) / rows;
+  const int64_t tiles = p.max_len < kKeys ? 1 : ((int64_t)p.max_len + kKeys - 1) / kKeys;
+  const int64_t units = groups * p.kv_heads;
+  if (units > (int64_t(1) << 33)) return KV8_ERR_SHAPE;
+  const int64_t want = units * ((tiles + kWarps - 1) / kWarps);
+  const int grid = (int)(want < most ? want : most);
+  p.counters = reinterpret_cast<int32_t*>(workspace);
+  p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kMaxCtas * 4);
+  const int live = rows * (p.q_heads / p.kv_heads);
+  if constexpr (SELECTED) {
+    if (dim == 128)
+      return dtype == KV8_FP16 ? launch_rows_selected<128, true>(p, grid, s)
+                               : launch_rows_selected<128, false>(p, grid, s);
+    return dtype == KV8_FP16 ? launch_rows_selected<64, true>(p, grid, s)
+                             : launch_rows_selected<64, false>(p, grid, s);
+  } else {
+    if (dim == 128)
+      return dtype == KV8_FP16 ? launch_rows<128, true, false>(p, live, grid, s)
+                               : launch_rows<128, false, false>(p, live, grid, s);
+    return dtype == KV8_FP16 ? launch_rows<64, true, false>(p, live, grid, s)
+                             : launch_rows<64, false, false>(p, live, grid, s);
+  }
 }
 
 }  // namespace
@@ -186,7 +921,10 @@ int launch(const Params& p, int rows, int dim, int dtype, cudaStream_t s) {
 extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
                                                  int group_rows) {
   if (!heads_ok(q_heads, kv_heads, dim, group_rows)) return KV8_ERR_SHAPE;
-  return 16;
+  const int ctas = grid_size();
+  if (ctas < 0) return KV8_ERR_CUDA;
+  return kMaxCtas * 4 +
+         (int64_t)ctas * 2 * padded_rows(group_rows * (q_heads / kv_heads)) * (dim + 4) * 4;
 }
 
 extern "C" int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,
@@ -208,15 +946,18 @@ extern "C" int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, i
   if (!lens || !block_table) return KV8_ERR_NULL;
   if (!aligned(lens, 4) || !aligned(group_table, 4) || !aligned(block_table, 4))
     return KV8_ERR_ALIGN;
-  const int64_t need = kv8_attention_workspace_bytes(q_heads, kv_heads, dim, group_rows);
-  if (need < 0) return (int)need;
-  if (ws_bytes < need) return KV8_ERR_WORKSPACE;
-  const Params p{(const uint16_t*)q, q_ld,     q_heads,    kv_heads,    sm_scale * 1.44269504f,
-                 lens,               max_len,  group_rows, group_table, block_table,
-                 n_tables,           table_ld, page_size,  nullptr,     0,
-                 block_tokens,       k_cache,  v_cache,    k_scale,     v_scale,
-                 num_slots,          (uint16_t*)out, out_ld, lse,       status};
-  return launch<false>(p, rows, dim, dtype, (cudaStream_t)stream);
+  Params p = common(q, q_ld, rows, q_heads, kv_heads, sm_scale, block_tokens, k_cache, v_cache,
+                    k_scale, v_scale, num_slots, out, out_ld, lse, status);
+  p.lens = lens;
+  p.max_len = max_len;
+  p.group_rows = group_rows;
+  p.group_table = group_table;
+  p.block_table = block_table;
+  p.n_tables = n_tables;
+  p.table_ld = table_ld;
+  p.page_size = page_size;
+  p.page_shift = shift_of(page_size);
+  return run<false>(p, dim, dtype, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" int kv8_attention_selected(const void* q, int64_t q_ld, int dtype, int rows,
@@ -234,13 +975,11 @@ extern "C" int kv8_attention_selected(const void* q, int64_t q_ld, int dtype, in
   if (err || rows == 0) return err;
   if (k > 0 && !slots) return KV8_ERR_NULL;
   if (!aligned(slots, 4)) return KV8_ERR_ALIGN;
-  const int64_t need = kv8_attention_workspace_bytes(q_heads, kv_heads, dim, 1);
-  if (need < 0) return (int)need;
-  if (ws_bytes < need) return KV8_ERR_WORKSPACE;
-  const Params p{(const uint16_t*)q, q_ld,     q_heads,  kv_heads,  sm_scale * 1.44269504f,
-                 nullptr,            k,        1,        nullptr,   nullptr,
-                 1,                  0,        block_tokens, slots, slots_ld,
-                 block_tokens,       k_cache,  v_cache,  k_scale,   v_scale,
-                 num_slots,          (uint16_t*)out, out_ld, lse,   status};
-  return launch<true>(p, rows, dim, dtype, (cudaStream_t)stream);
+  Params p = common(q, q_ld, rows, q_heads, kv_heads, sm_scale, block_tokens, k_cache, v_cache,
+                    k_scale, v_scale, num_slots, out, out_ld, lse, status);
+  p.slots = slots;
+  p.slots_ld = slots_ld;
+  p.max_len = k;
+  p.group_rows = 1;
+  return run<true>(p, dim, dtype, workspace, ws_bytes, (cudaStream_t)stream);
 }

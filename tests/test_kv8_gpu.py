@@ -305,6 +305,51 @@ def test_zero_scales():
     d.check()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_nan_seen_by_the_later_rows_alone(dim):
+    """NaN codes and scales in the last draft's key and value: the rows before it are as
+    without them, the rows that see them are NaN where the definition says so."""
+    d = Dense(24, [97, 98, 99, 100], 4, 8, 2, dim, 64, 16, "bf16", poison=False)
+    slot = K8.row_slots(d.table, 0, 100, 100, 64, d.cache[0].shape[0])[0]
+    d.cache[1][slot[99], 1, 5] = 0x7F       # a value: channel 5 of the last row, key head 1
+    d.cache[1][slot[98], 0, 40] = 0xFF      # rows 2 and 3, key head 0
+    d.cache[0][slot[99], 0, 7] = 0x7F       # a key: everything of the last row, key head 0
+    h = d.handle()
+    out, lse = h.attention(*d.args())
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for r in (0, 1):
+        close(o[r], l[r], d.ref(r)[0], "bf16", f"row {r}")
+    nan = np.zeros((4, 8, dim), bool)
+    nan[2, :4, 40] = True
+    nan[3, :4] = True
+    nan[3, 4:, 5] = True
+    assert np.array_equal(np.isnan(o), nan)
+    assert np.isnan(l[3, :4]).all() and not np.isnan(l[:3]).any() and not np.isnan(l[3, 4:]).any()
+    d.cache[3][slot[96] // 16] = np.nan     # the scale of a block that starts at position 96
+    h = d.handle()
+    d.lens[:] = [96, 96, 97, 100]
+    o = h.attention(*d.args())[0].double().cpu().numpy()
+    for r in (0, 1):
+        close(o[r], l[r] * 0 + d.ref(r)[0][1], d.ref(r)[0], "bf16", f"row {r}")
+    assert np.isnan(o[2:]).all()
+
+
+def test_nan_and_infinite_queries():
+    d = Dense(25, [50, 60, 70], 3, 8, 2, 64, 16, 16, "bf16")
+    ref = [d.ref(r)[0] for r in range(3)]
+    d.q[1, 2] = float("nan")
+    d.q[2, 7] = float("inf")
+    out, lse = d.handle().attention(*d.args())
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isnan(o[1, 2]).all() and np.isnan(l[1, 2])
+    assert np.isnan(o[2, 7]).any() or not np.isfinite(l[2, 7])
+    keep = np.ones((3, 8), bool)
+    keep[1, 2] = keep[2, 7] = False
+    for r in range(3):
+        at = keep[r]
+        close(o[r][at], l[r][at], [x[at] for x in ref[r]], "bf16")
+
+
 def test_tiny_and_large_queries():
     for gain in (1e-30, 1e30):
         d = Dense(17, [90, 33], 1, 4, 2, 64, 16, 16, "bf16", q_gain=gain)
