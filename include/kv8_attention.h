@@ -102,7 +102,7 @@ int kv8_store(const uint16_t* k, int64_t k_ld, const uint16_t* v, int64_t v_ld, 
  * Queries the device. Negative: a KV8_ERR_* code. */
 int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim, int group_rows);
 
-/* Attention through a block table. One launch.
+/* Attention through a block table. Two launches.
  *   q            device bf16 / fp16 [rows, q_ld], head i at columns [i * dim, ..)
  *   lens         device int32 [rows]: row t attends to positions [0, lens[t])
  *   max_len      bound on every length
@@ -112,8 +112,8 @@ int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim, int gr
  *   block_table  device int32 [n_tables, table_ld]; entries past a length are not read
  *   out          device, q's type [rows, out_ld], 16-byte aligned; may not overlap q
  *   lse          device float32 [rows, q_heads] or NULL
- *   workspace    device, 16-byte aligned, zero-filled before its first use; every call
- *                leaves its counters zero. One workspace serves one stream at a time. */
+ *   workspace    device, 16-byte aligned; what it holds before and after is of no account.
+ *                One workspace serves one stream at a time. */
 int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads,
                   int dim, float sm_scale, const int32_t* lens, int max_len, int group_rows,
                   const int32_t* group_table, const int32_t* block_table, int n_tables,
@@ -122,7 +122,7 @@ int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,
                   int64_t num_slots, void* out, int64_t out_ld, float* lse, void* workspace,
                   int64_t ws_bytes, int32_t* status, kv8_stream_t stream);
 
-/* Attention over a list of slots per query row. One launch. Arguments as above, and
+/* Attention over a list of slots per query row. Two launches. Arguments as above, and
  *   slots        device int32 [rows, slots_ld]: k slots per row; negative ones are
  *                skipped; a slot given twice counts twice */
 int kv8_attention_selected(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,

@@ -225,7 +225,7 @@ class Kv8Cache:
             n = B.kv8_attention_workspace_bytes(q.shape[1], self.k.shape[1], q.shape[2],
                                                 group_rows)
             with _on(stream):
-                ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+                ws = torch.empty(n, dtype=torch.uint8, device=q.device)
             self._workspaces[key] = ws
         return ws
 

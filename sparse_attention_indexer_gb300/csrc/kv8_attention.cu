@@ -7,8 +7,9 @@
 // same keys. The units' tiles of 32 keys are laid end to end, and CTA i of N takes the tiles
 // [i * W / N, (i + 1) * W / N) of the W there are, whatever the lengths: the loads are even
 // for one long row and for a ragged batch alike, with no plan from the host. A unit that
-// several CTAs share is joined by the last of them to arrive, from partial sums in the
-// workspace, in the order of the CTAs (so the result does not depend on who is last).
+// several CTAs share leaves its parts in the workspace, and a second, small launch joins them
+// in the order of the CTAs. (The last CTA to arrive joining its unit alone took 250 of 334 us
+// for 56 rows to a unit of 80K keys: 38 parts of 28 KB through one SM.)
 //
 // A tile. The four warps of a CTA form KW groups that take a segment's tiles in turn, WM warps to
 // a group, each with MT * 16 of the M rows. A group keeps kStages tiles of codes and scales
@@ -24,9 +25,10 @@
 //   - p . v: ldmatrix.trans hands each lane pairs of channels of two keys; one byte
 //     permutation sorts them into the two fragments of the even and the odd channels.
 //   - the value scale of a block is folded into its weights before these are rounded to
-//     fp16: w' = 2^(x + log2 sv - M), M the running maximum of x + log2 sv. With the
-//     largest w' at 1, a block of small weights and large values loses no more than one of large weights
-//     and small values. The sum of the weights keeps its own maximum m.
+//     fp16: w' = 2^(x - m) * sv * 2^-d, m the row's running maximum. While the scales met so
+//     far lie within 2^8 of each other, one d for all rows keeps the row's largest w' in
+//     [1, 2^9), and fp16 holds what is 2^-24 of it; else d is chosen per row so that the
+//     largest w' is about 1.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -46,6 +48,11 @@ constexpr int kKeys = 32;   // keys of a tile
 constexpr int kStages = 3;  // tiles in flight per warp group
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 2048;
+
+// The unit whose first part CTA i has and whose last part CTA `last` > i has; last < 0: none.
+struct __align__(16) Shared {
+  int32_t g, h, last, pad;
+};
 
 struct Params {
   const uint16_t* q;
@@ -73,8 +80,8 @@ struct Params {
   int64_t out_ld;
   float* lse;
   int32_t* status;
-  int32_t* counters;  // workspace: arrivals at a shared unit, by its first CTA
-  float* parts;       // workspace: two partial results per CTA
+  Shared* shared;  // workspace: the shared unit that starts in each CTA
+  float* parts;    // workspace: two partial results per CTA
 };
 
 // ------------------------------------------------------------------ PTX
@@ -213,6 +220,42 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
   return __vcmpeq4(c & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
 
+// A part of a unit in the workspace: ROWS x DIM sums, then {m, m + d, sum} per row.
+template <int DIM, int ROWS>
+struct Part {
+  static constexpr int kStat = ROWS * DIM;
+  static constexpr int kFloats = ROWS * (DIM + 4);
+};
+
+// Channels [N * c, N * c + N) of row r of unit (g, h): v relative to 2^topv over l relative to
+// 2^top, and with c == 0 the row's lse.
+template <int DIM, bool FP16, int N>
+__device__ __forceinline__ void write_row(const Params& p, int g, int h, int r, int c,
+                                          const float* v, float top, float topv, float l) {
+  const int ratio = p.q_heads / p.kv_heads;
+  const int64_t row = (int64_t)g * p.group_rows + r / ratio;
+  if (row >= p.rows) return;
+  const int head = h * ratio + r % ratio;
+  const bool none = l == 0.0f;  // no key: one that counts adds 1 to l, a NaN makes it NaN
+  const float f = none ? 0.0f : exp2f(topv - top) / l;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float x = none ? 0.0f : v[2 * i] * f, y = none ? 0.0f : v[2 * i + 1] * f;
+    if (FP16) {
+      w[i] = pack_half(x, y);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  uint16_t* dst = p.out + row * p.out_ld + (int64_t)head * DIM + c * N;
+  if (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[N / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (c == 0 && p.lse)
+    p.lse[row * p.q_heads + head] = none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+}
+
 // ------------------------------------------------------------------ kernel
 template <int DIM, bool FP16, bool SELECTED, int MT, int WM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -223,9 +266,10 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   constexpr int kSteps = DIM / 16;    // mma steps of q . k
   constexpr int kOut = DIM / 8;       // mma tiles of p . v
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_sum[kThreads];
+  asm volatile("griddepcontrol.launch_dependents;");  // the join, which waits for this launch
+  __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_first;
-  __shared__ int s_group, s_last;
+  __shared__ int s_group;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kg = warp / WM, wm = warp % WM;
@@ -258,12 +302,19 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     int64_t mine = 0;
     for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len(p, (int)i, &err));
     if (me) err = 0;  // CTA 0 reports for all
-    s_sum[tid] = mine;
+    int64_t before = mine, total = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) s_sum[warp] = before;
     __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int i = 0; i < kThreads; ++i) {
+    before -= mine;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
       const int64_t x = s_sum[i];
-      if (i < tid) before += x;
+      if (i < warp) before += x;
       total += x;
     }
     all = total * p.kv_heads;
@@ -300,6 +351,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   float* s_mul = reinterpret_cast<float*>(smem + L::kMul);
   int* s_len = reinterpret_cast<int*>(smem + L::kLen);
 
+  Shared mine = {0, 0, -1, 0};
   int64_t w = w0;
   while (w < w1) {
     const int tiles = tiles_of(len);
@@ -429,7 +481,9 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         least = min(least, lim[i][b]);
       }
     float o[MT][kOut][4];
-    float m[MT][2], mv[MT][2], sum[MT][2];
+    // m: running maximum of x; o is relative to 2^(m + d), sum to 2^m
+    float m[MT][2], d[MT][2], sum[MT][2];
+    uint32_t sv_top = 0, sv_low = 255;  // exponents of the value scales so far
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -438,8 +492,8 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        m[i][b] = mv[i][b] = -INFINITY;
-        sum[i][b] = 0.0f;
+        m[i][b] = -INFINITY;
+        d[i][b] = sum[i][b] = 0.0f;
       }
     }
 
@@ -484,40 +538,49 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         }
       }
 
-      // ---- scores to weights: x = acc * mul * key scale (log2 units), xv = x + log2 sv
+      // ---- scores to weights: x = acc * mul * key scale (log2 units)
       const uint32_t in = masks[stage];
-      float lv[4][2];
       const float* sc = reinterpret_cast<const float*>(smem + L::kScale) +
                         (kg * kStages + stage) * 2 * kKeys;
+      {
+        // exponents of the scales of the values (zeros weigh nothing and do not count)
+        const uint32_t e = __float_as_uint(sc[kKeys + lane]) >> 23;
+        const bool some = ((in >> lane) & 1) && sc[kKeys + lane] != 0.0f;
+        sv_top = max(sv_top, __reduce_max_sync(0xffffffffu, some ? e : 0u));
+        sv_low = min(sv_low, __reduce_min_sync(0xffffffffu, some ? e : 255u));
+      }
+      const bool near = sv_top <= sv_low + 8 || sv_low == 255;
       // some row of this warp ends inside this tile or before it
       const bool ragged = __any_sync(0xffffffffu, (int64_t)(tile + 1) * kKeys > least);
+      float vs[4][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 ks = *reinterpret_cast<const float2*>(sc + j * 8 + 2 * t);
-        const float2 vs = *reinterpret_cast<const float2*>(sc + kKeys + j * 8 + 2 * t);
-        lv[j][0] = log2_fast(vs.x);
-        lv[j][1] = log2_fast(vs.y);
-        const float out0 = (in >> (j * 8 + 2 * t)) & 1 ? 0.0f : -INFINITY;
-        const float out1 = (in >> (j * 8 + 2 * t + 1)) & 1 ? 0.0f : -INFINITY;
+        const float2 v2 = *reinterpret_cast<const float2*>(sc + kKeys + j * 8 + 2 * t);
+        vs[j][0] = v2.x;
+        vs[j][1] = v2.y;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            s[i][j][2 * b] = fmaf(s[i][j][2 * b] * mul[i][b], ks.x, out0);
-            s[i][j][2 * b + 1] = fmaf(s[i][j][2 * b + 1] * mul[i][b], ks.y, out1);
+            s[i][j][2 * b] *= mul[i][b] * ks.x;
+            s[i][j][2 * b + 1] *= mul[i][b] * ks.y;
           }
       }
-      if (ragged) {
+      const bool masked = ragged || in != 0xffffffffu;
+      if (masked) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int64_t pos = (int64_t)tile * kKeys + j * 8 + 2 * t + c;
+            const int at = j * 8 + 2 * t + c;
+            const int64_t pos = (int64_t)tile * kKeys + at;
+            const bool out = !((in >> at) & 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
               for (int b = 0; b < 2; ++b)
-                if (pos >= lim[i][b]) s[i][j][2 * b + c] = -INFINITY;
+                if (out || pos >= lim[i][b]) s[i][j][2 * b + c] = -INFINITY;
           }
       }
       uint32_t pa[MT][2][4];
@@ -526,39 +589,51 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         float keep[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float tm = -INFINITY, tv = -INFINITY;
+          float tm = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tm = fmaxf(tm, s[i][j][2 * b + c]);
-              tv = fmaxf(tv, s[i][j][2 * b + c] + lv[j][c]);  // NaN is no maximum
-            }
-#pragma unroll
-          for (int x = 1; x <= 2; x <<= 1) {
-            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
-            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
-          }
+            tm = fmaxf(tm, fmaxf(s[i][j][2 * b], s[i][j][2 * b + 1]));  // NaN is no maximum
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
           tm = fmaxf(tm, m[i][b]);
-          tv = fmaxf(tv, mv[i][b]);
           // a row that has no key yet keeps -inf; 0 stands in for it in the differences
-          const float um = tm == -INFINITY ? 0.0f : tm, uv = tv == -INFINITY ? 0.0f : tv;
-          sum[i][b] *= exp2_fast(m[i][b] - um);
-          keep[b] = exp2_fast(mv[i][b] - uv);
+          const float um = tm == -INFINITY ? 0.0f : tm;
+          // d: 2^8 below the largest scale while all of them lie within 2^8, so that the row's
+          // largest weight * scale is 2^d times a number in [1, 2^9); else what makes it 1.
+          // 2^d and its reciprocal stay in range.
+          float dn = sv_low == 255 ? 0.0f : (float)max((int)sv_top - 127 - 8, -120);
+          if (!near) {
+            float tv = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                tv = fmaxf(tv, s[i][j][2 * b + c] + log2_fast(vs[j][c]));
+            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 1));
+            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 2));
+            // what there is already is at most 2^9 above 2^(m + d)
+            dn = fmaxf(tv, m[i][b] + d[i][b]) - um;
+            dn = dn > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : 0.0f;
+          }
+          const float drop = exp2_fast(m[i][b] - um);
+          sum[i][b] *= drop;
+          keep[b] = dn == d[i][b] ? drop : exp2_fast(m[i][b] + d[i][b] - um - dn);
           m[i][b] = tm;
-          mv[i][b] = tv;
+          d[i][b] = dn;
+          const float f = exp2_fast(-dn);
           float add = 0.0f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float wv[2];
+            float w2[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float x = s[i][j][2 * b + c];
-              add += exp2_fast(x - um);
+              const float e = exp2_fast(s[i][j][2 * b + c] - um);
+              add += e;
+              w2[c] = e * vs[j][c] * f;  // in this order: f may be large where e is 0
               // a key outside the row weighs 0, whatever the scale of its block is
-              wv[c] = x == -INFINITY ? 0.0f : exp2_fast(x + lv[j][c] - uv);
+              if (masked && s[i][j][2 * b + c] == -INFINITY) w2[c] = 0.0f;
             }
-            pa[i][j >> 1][(j & 1) * 2 + b] = pack_half(wv[0], wv[1]);
+            pa[i][j >> 1][(j & 1) * 2 + b] = pack_half(w2[0], w2[1]);
           }
           sum[i][b] += add;
         }
@@ -628,13 +703,13 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
                          : "r"(v_at + piece_at<DIM>(key, c) + 4 * t));
             const uint32_t nan = nan_codes(codes);
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-              if ((nan >> (8 * d)) & 1)
+            for (int e = 0; e < 4; ++e)
+              if ((nan >> (8 * e)) & 1)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                   for (int b = 0; b < 2; ++b)
-                    if (pos < lim[i][b]) o[i][2 * c + (d & 1)][2 * b + (d >> 1)] = NAN;
+                    if (pos < lim[i][b]) o[i][2 * c + (e & 1)][2 * b + (e >> 1)] = NAN;
           }
         }
       }
@@ -655,7 +730,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         if (t == 0) {
           float* st = s_stat + (kg * kRows + r) * 3;
           st[0] = m[i][b];
-          st[1] = mv[i][b];
+          st[1] = m[i][b] + d[i][b];
           st[2] = x;
         }
         float4* dst = reinterpret_cast<float4*>(smem) + (kg * kRows + r) * (DIM / 4) + t;
@@ -666,34 +741,9 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       }
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == tiles;
-    // CTAs a .. b share the unit
-    const int64_t a = ((first_tile + 1) * n - 1) / all, b = ((first_tile + tiles) * n - 1) / all;
-    constexpr int kPart = kRows * (DIM + 4);
-    auto part_of = [&](int64_t cta) { return p.parts + (cta == a ? 2 * cta + 1 : 2 * cta) * kPart; };
-    auto write_row = [&](int r, int c4, float4 v, float top, float topv, float l) {
-      // v is relative to 2^topv, l to 2^top
-      const bool none = l == 0.0f;  // no key: one that counts adds 1 to l, a NaN makes it NaN
-      const float f = none ? 0.0f : exp2f(topv - top) / l;
-      const int row = g * (SELECTED ? 1 : p.group_rows) + r / ratio;
-      if (row >= p.rows) return;
-      const int head = h * ratio + r % ratio;
-      uint2 packed;
-      const float x[4] = {none ? 0.0f : v.x * f, none ? 0.0f : v.y * f, none ? 0.0f : v.z * f,
-                          none ? 0.0f : v.w * f};
-      if (FP16) {
-        packed = make_uint2(pack_half(x[0], x[1]), pack_half(x[2], x[3]));
-      } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
-        packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                            *reinterpret_cast<const uint32_t*>(&hi));
-      }
-      *reinterpret_cast<uint2*>(p.out + row * p.out_ld + (int64_t)head * DIM + c4 * 4) = packed;
-      if (c4 == 0 && p.lse)
-        p.lse[(int64_t)row * p.q_heads + head] =
-            none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-    };
-    float* part = whole ? nullptr : part_of(me);
+    // the CTA that has the unit's first tile keeps its part in its second place (its first may
+    // hold the end of the unit before); the others theirs in their first
+    float* part = p.parts + (2 * me + (tile0 == 0)) * Part<DIM, kRows>::kFloats;
     for (int x = tid; x < live * (DIM / 4); x += kThreads) {
       const int r = x / (DIM / 4), c4 = x % (DIM / 4);
       float top = -INFINITY, topv = -INFINITY, l = 0.0f;
@@ -703,67 +753,33 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         topv = fmaxf(topv, s_stat[(k * kRows + r) * 3 + 1]);
       }
       const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
-      float4 v = make_float4(0, 0, 0, 0);
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         const float* st = s_stat + (k * kRows + r) * 3;
         l += st[2] * exp2_fast(st[0] - ut);
         const float f = exp2_fast(st[1] - uv);
         const float4 y = reinterpret_cast<const float4*>(smem)[(k * kRows + r) * (DIM / 4) + c4];
-        v.x += y.x * f;
-        v.y += y.y * f;
-        v.z += y.z * f;
-        v.w += y.w * f;
+        v[0] += y.x * f;
+        v[1] += y.y * f;
+        v[2] += y.z * f;
+        v[3] += y.w * f;
       }
       if (whole) {
-        write_row(r, c4, v, top, topv, l);
+        write_row<DIM, FP16, 4>(p, g, h, r, c4, v, top, topv, l);
       } else {
-        reinterpret_cast<float4*>(part)[r * (DIM / 4) + c4] = v;
+        reinterpret_cast<float4*>(part)[r * (DIM / 4) + c4] =
+            make_float4(v[0], v[1], v[2], v[3]);
         if (c4 == 0) {
-          float* st = part + kRows * DIM + r * 4;
+          float* st = part + Part<DIM, kRows>::kStat + r * 4;
           st[0] = top;
           st[1] = topv;
           st[2] = l;
         }
       }
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int before = atomicAdd(p.counters + a, 1);
-        s_last = before == (int)(b - a);
-        if (s_last) p.counters[a] = 0;  // as the next call needs it
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int x = tid; x < live * (DIM / 4); x += kThreads) {
-          const int r = x / (DIM / 4), c4 = x % (DIM / 4);
-          float top = -INFINITY, topv = -INFINITY, l = 0.0f;
-          for (int64_t c = a; c <= b; ++c) {
-            const float4 st = __ldcg(reinterpret_cast<const float4*>(part_of(c) + kRows * DIM) + r);
-            top = fmaxf(top, st.x);
-            topv = fmaxf(topv, st.y);
-          }
-          const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
-          float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-          for (int64_t c = a; c <= b; ++c) {
-            const float* q = part_of(c);
-            const float4 st = __ldcg(reinterpret_cast<const float4*>(q + kRows * DIM) + r);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(q) + r * (DIM / 4) + c4);
-            l += st.z * exp2_fast(st.x - ut);
-            const float f = exp2_fast(st.y - uv);
-            v.x += y.x * f;
-            v.y += y.y * f;
-            v.z += y.z * f;
-            v.w += y.w * f;
-          }
-          write_row(r, c4, v, top, topv, l);
-        }
-      }
-    }
+    if (!whole && tile0 == 0)
+      mine = {g, h, (int32_t)(((first_tile + tiles) * n - 1) / all), 0};
     __syncthreads();  // the shared arrays are free for the next unit
 
     // ---- next unit
@@ -778,7 +794,69 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       }
     }
   }
+  if (tid == 0) p.shared[me] = mine;
   if (err && p.status) atomicOr(p.status, err);
+}
+
+// Joins the parts of the shared units: CTA (i, y) the rows y, y + gridDim.y, .. of the unit
+// that starts in CTA i of the launch before. A warp takes a row: the lanes look at the parts'
+// maxima, then each sums its channels over the parts, in the order of the parts.
+constexpr int kJoinThreads = 256;
+
+template <int DIM, bool FP16, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Params p) {
+  using Q = Part<DIM, ROWS>;
+  constexpr int kVec = DIM / 32;  // channels of a lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int a = blockIdx.x;
+  const Shared u = p.shared[a];
+  if (u.last < 0) return;
+  const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  const float* first = p.parts + (2 * (int64_t)a + 1) * Q::kFloats;
+  const float* rest = p.parts + 2 * (int64_t)a * Q::kFloats;  // + 2 c parts on, c >= 1
+  const int parts = u.last - a + 1;
+  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < live;
+       r += gridDim.y * (kJoinThreads / 32)) {
+    auto at = [&](int c) { return c == 0 ? first : rest + 2 * (int64_t)c * Q::kFloats; };
+    float top = -INFINITY, topv = -INFINITY;
+    for (int c = lane; c < parts; c += 32) {
+      const float2 st = __ldcg(reinterpret_cast<const float2*>(at(c) + Q::kStat + r * 4));
+      top = fmaxf(top, st.x);
+      topv = fmaxf(topv, st.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+    }
+    const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
+    float l = 0.0f, v[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
+#pragma unroll 8
+    for (int c = 0; c < parts; ++c) {
+      const float* q = at(c);
+      const float4 st = __ldcg(reinterpret_cast<const float4*>(q + Q::kStat + r * 4));
+      float y[kVec];
+      if (kVec == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(q + r * DIM) + lane);
+        y[0] = x.x;
+        y[1] = x.y;
+        y[kVec - 2] = x.z;
+        y[kVec - 1] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(q + r * DIM) + lane);
+        y[0] = x.x;
+        y[1] = x.y;
+      }
+      l += st.z * exp2_fast(st.x - ut);
+      const float f = exp2_fast(st.y - uv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] += y[i] * f;
+    }
+    write_row<DIM, FP16, kVec>(p, u.g, u.h, r, lane, v, top, topv, l);
+  }
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
@@ -838,7 +916,21 @@ int launch(const Params& p, int grid, cudaStream_t s) {
       cudaSuccess)
     return KV8_ERR_CUDA;
   kernel<<<(unsigned)grid, kThreads, L::kTotal, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return KV8_ERR_CUDA;
+  // the join is launched while the first kernel runs and waits for its end
+  constexpr int kWarpsJoin = kJoinThreads / 32;
+  const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((live + kWarpsJoin - 1) / kWarpsJoin));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_join_kernel<DIM, FP16, L::kRows>, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
 }
 
 template <int DIM, bool FP16, bool SELECTED>
@@ -898,8 +990,9 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
   if (units > (int64_t(1) << 33)) return KV8_ERR_SHAPE;
   const int64_t want = units * ((tiles + kWarps - 1) / kWarps);
   const int grid = (int)(want < most ? want : most);
-  p.counters = reinterpret_cast<int32_t*>(workspace);
-  p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kMaxCtas * 4);
+  p.shared = reinterpret_cast<Shared*>(workspace);
+  p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
+                                     kMaxCtas * sizeof(Shared));
   const int live = rows * (p.q_heads / p.kv_heads);
   if constexpr (SELECTED) {
     if (dim == 128)
@@ -923,7 +1016,7 @@ extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int 
   if (!heads_ok(q_heads, kv_heads, dim, group_rows)) return KV8_ERR_SHAPE;
   const int ctas = grid_size();
   if (ctas < 0) return KV8_ERR_CUDA;
-  return kMaxCtas * 4 +
+  return kMaxCtas * (int64_t)sizeof(Shared) +
          (int64_t)ctas * 2 * padded_rows(group_rows * (q_heads / kv_heads)) * (dim + 4) * 4;
 }
 
