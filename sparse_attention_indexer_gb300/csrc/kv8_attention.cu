@@ -124,11 +124,12 @@ __device__ __forceinline__ uint4 ldmatrix_trans(uint32_t a) {
   return v;
 }
 
-// Two e4m3 codes (low 16 bits) as two fp16: exact.
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes as fp16, exactly: lo the two lower, hi the two upper.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -531,7 +532,8 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t c = st == 0 ? kr[j].x : st == 1 ? kr[j].y : st == 2 ? kr[j].z : kr[j].w;
-            const uint32_t b0 = widen2(c), b1 = widen2(c >> 16);
+            uint32_t b0, b1;
+            widen4(c, b0, b1);
 #pragma unroll
             for (int i = 0; i < MT; ++i) mma(s[i][j], a[i].x, a[i].z, a[i].y, a[i].w, b0, b1);
           }
@@ -664,8 +666,9 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
                 x &= ~nan_codes(x);
                 y &= ~nan_codes(y);
               }
-              const uint32_t b0 = widen2(x), b1 = widen2(y);
-              const uint32_t c0 = widen2(x >> 16), c1 = widen2(y >> 16);
+              uint32_t b0, b1, c0, c1;
+              widen4(x, b0, c0);
+              widen4(y, b1, c1);
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 mma(o[i][cp * 4 + e * 2], pa[i][kk][0], pa[i][kk][1], pa[i][kk][2], pa[i][kk][3],
