@@ -11,19 +11,22 @@
 // in the order of the CTAs. (The last CTA to arrive joining its unit alone took 250 of 334 us
 // for 56 rows to a unit of 80K keys: 38 parts of 28 KB through one SM.)
 //
-// A tile. The four warps of a CTA form KW groups that take a segment's tiles in turn, WM warps to
-// a group, each with MT * 16 of the M rows. A group keeps kStages tiles of codes and scales
+// A tile. The four warps of a CTA form KW groups that take a segment's tiles in turn, WM warps
+// to a group, each with NT * 8 of the M rows. A group keeps kStages tiles of codes and scales
 // in flight with cp.async (a key that is masked or missing is filled with zeros and its
 // score set to -inf, so what lies there never enters). Products run on mma.sync m16n8k16
-// fp16 with fp32 accumulators; at M <= 128 rows and one pass over the keys they are not what
-// bounds the kernel, and the codes have to be widened on the way anyway:
+// fp16 with fp32 accumulators, keys and channels on its 16 rows and query rows on its 8
+// columns: the 8 query heads of a key head fill it, where query rows on the 16 would leave
+// half of the products, the weights and the registers of the sums idle.
 //   - q . k: an fp16 times an e4m3 (widened, exact) product is exact. Rows of bf16 q are
 //     brought to [2^14, 2^15) by a power of two, which fp16 then holds exactly but for
 //     channels 2^-38 below the row's largest. The channels may be summed in any order, so
 //     lane t of a quad takes 16 contiguous bytes of a key, one shared-memory load for four
 //     mma steps, and the query fragments are laid out to match.
 //   - p . v: ldmatrix.trans hands each lane pairs of channels of two keys; one byte
-//     permutation sorts them into the two fragments of the even and the odd channels.
+//     permutation sorts them into the fragments of the even and the odd channels, which
+//     are rows g and g + 8 of a product of 16 channels. The weights turn from keys x rows
+//     into rows x keys by movmatrix.
 //   - the value scale of a block is folded into its weights before these are rounded to
 //     fp16: w' = 2^(x - m) * sv * 2^-d, m the row's running maximum. While the scales met so
 //     far lie within 2^8 of each other, one d for all rows keeps the row's largest w' in
@@ -45,13 +48,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 32;   // keys of a tile
-constexpr int kStages = 3;  // tiles in flight per warp group
-constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 2048;
 
-// The unit whose first part CTA i has and whose last part CTA `last` > i has; last < 0: none.
+// A unit whose parts CTAs first .. last have; last < 0: none, or one CTA has it whole. Kept by
+// unit where there are at most kMaxCtas units, else by the unit's first CTA.
 struct __align__(16) Shared {
-  int32_t g, h, last, pad;
+  int32_t g, h, first, last;
 };
 
 struct Params {
@@ -146,6 +148,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 matrix of fp16 (lane 4 r + c: row r, columns 2 c, 2 c + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -158,17 +167,20 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // ------------------------------------------------------------------ layout in shared memory
-template <int DIM, int MT, int WM>
+template <int DIM, int NT, int WM>
 struct Smem {
   static constexpr int kGroups = kWarps / WM;
-  static constexpr int kRows = 16 * MT * WM;
-  static constexpr int kTile = kKeys * DIM;  // bytes of the K (or V) codes of a tile
+  static constexpr int kRows = 8 * NT * WM;
+  static constexpr int kStages = NT <= 2 ? 2 : 3;  // tiles in flight per warp group
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;    // CTAs per SM
+  static constexpr int kTile = kKeys * DIM;        // bytes of the K (or V) codes of a tile
   static constexpr int kRing = kGroups * kStages * 2 * kTile;
-  static constexpr int kJoin = kWarps * 16 * MT * DIM * 4;  // the warps' sums, over the ring
-  static constexpr int kQ = (kRing > kJoin ? kRing : kJoin);
+  static constexpr int kLd = DIM + 4;  // floats between the rows of the warps' sums
+  static constexpr int kJoin = kGroups * kRows * kLd * 4;  // these sums, over the ring
+  static constexpr int kQ = kRing > kJoin ? kRing : kJoin;
   static constexpr int kScale = kQ + kRows * DIM * 2;
   static constexpr int kMask = kScale + kGroups * kStages * 2 * kKeys * 4;
-  static constexpr int kStat = kMask + ((kGroups * kStages * 4 + 15) & ~15);  // m, M, l
+  static constexpr int kStat = kMask + ((kGroups * kStages * 4 + 15) & ~15);  // m, m + d, sum
   static constexpr int kMul = kStat + kGroups * kRows * 3 * 4;
   static constexpr int kLen = kMul + kRows * 4;
   static constexpr int kTotal = kLen + kRows * 4;
@@ -258,14 +270,13 @@ __device__ __forceinline__ void write_row(const Params& p, int g, int h, int r, 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int DIM, bool FP16, bool SELECTED, int MT, int WM>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
+__global__ void __launch_bounds__(kThreads, Smem<DIM, NT, WM>::kCtas)
 kv8_attention_kernel(const __grid_constant__ Params p) {
-  using L = Smem<DIM, MT, WM>;
-  constexpr int kGroups = L::kGroups, kRows = L::kRows;
+  using L = Smem<DIM, NT, WM>;
+  constexpr int kGroups = L::kGroups, kRows = L::kRows, kStages = L::kStages;
   constexpr int kPieces = DIM / 16;   // 16-byte pieces of a row of codes
   constexpr int kSteps = DIM / 16;    // mma steps of q . k
-  constexpr int kOut = DIM / 8;       // mma tiles of p . v
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");  // the join, which waits for this launch
   __shared__ int64_t s_sum[kWarps];
@@ -284,12 +295,15 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   int64_t all, first_tile = 0;  // tiles of the launch; first tile of the unit at hand
   int g = 0, h = 0, len = p.max_len;
   int64_t w0, w1;
-  int64_t n = gridDim.x;  // CTAs that take part: each gets a tile for each of its warp groups
+  // CTAs that take part: each gets a tile for each of its warp groups, and a unit is not split
+  // where there are CTAs enough for one each
+  int64_t n = gridDim.x;
+  const int64_t units = (int64_t)groups * p.kv_heads;
   const int64_t me = blockIdx.x;
   if (SELECTED) {
     const int64_t tiles = tiles_of(len);
     all = tiles * groups * p.kv_heads;
-    n = min(n, (all + kGroups - 1) / kGroups);
+    n = min(n, max(units, (all + kGroups - 1) / kGroups));
     w0 = me * all / n;
     w1 = me < n ? (me + 1) * all / n : w0;
     const int64_t u = w0 / tiles;
@@ -319,7 +333,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       total += x;
     }
     all = total * p.kv_heads;
-    n = min(n, (all + kGroups - 1) / kGroups);
+    n = min(n, max(units, (all + kGroups - 1) / kGroups));
     w0 = me * all / n;
     w1 = me < n ? (me + 1) * all / n : w0;
     if (w0 < w1 && w0 >= before * p.kv_heads && w0 < (before + mine) * p.kv_heads) {
@@ -352,7 +366,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   float* s_mul = reinterpret_cast<float*>(smem + L::kMul);
   int* s_len = reinterpret_cast<int*>(smem + L::kLen);
 
-  Shared mine = {0, 0, -1, 0};
+  Shared mine = {0, 0, 0, -1};
   int64_t w = w0;
   while (w < w1) {
     const int tiles = tiles_of(len);
@@ -453,14 +467,12 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
           wds[i] = pack_half(__uint_as_float(wds[i] << 16) * f,
                              __uint_as_float(wds[i] & 0xFFFF0000u) * f);
       }
-      // fragment of step s of 64 channels: lane (r % 8) * 4 + t holds channels 16 t + 4 s ..
+      // fragments of two steps: lane (r % 8) * 4 + t holds channels 16 t + 4 s .. of 64
       const int half = c >> 2, tt = c & 3;
-      uint8_t* base = smem + L::kQ + (r >> 4) * (kSteps * 512) + ((r & 7) * 4 + tt) * 16 +
-                      ((r >> 3) & 1) * 8;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        *reinterpret_cast<uint2*>(base + (half * 4 + s) * 512) =
-            make_uint2(wds[2 * s], wds[2 * s + 1]);
+      uint4* dst = reinterpret_cast<uint4*>(smem + L::kQ) +
+                   ((r >> 3) * (kSteps / 2) + half * 2) * 32 + (r & 7) * 4 + tt;
+      dst[0] = make_uint4(wds[0], wds[1], wds[2], wds[3]);
+      dst[32] = make_uint4(wds[4], wds[5], wds[6], wds[7]);
       if (c == 0) {
         int ignored = 0;
         s_mul[r] = mul;
@@ -470,25 +482,34 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     }
     __syncthreads();
 
-    const int row0 = wm * 16 * MT;  // this warp's rows
-    float mul[MT][2];
-    int lim[MT][2], least = INT32_MAX;
+    // this thread's query rows: row0 + i * 8 + 2 t + b
+    const int row0 = wm * 8 * NT;
+    int least = INT32_MAX;  // where the unit's first row ends
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < (kRows + 31) / 32; ++i)
+      if (i * 32 + lane < kRows) least = min(least, s_len[i * 32 + lane]);
+    least = __reduce_min_sync(0xffffffffu, least);
+    float mul[NT][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        mul[i][b] = s_mul[row0 + i * 16 + b * 8 + quad];
-        lim[i][b] = s_len[row0 + i * 16 + b * 8 + quad];
-        least = min(least, lim[i][b]);
-      }
-    float o[MT][kOut][4];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) mul[i][b] = s_mul[row0 + i * 8 + 2 * t + b];
+    const uint32_t q_at = smem_u32(smem + L::kQ) + wm * NT * (kSteps / 2) * 512 + lane * 16;
+    uint4 qf[NT <= 2 ? NT : 1][kSteps / 2];  // few enough to stay in registers
+    if (NT <= 2) {
+#pragma unroll
+      for (int i = 0; i < (NT <= 2 ? NT : 1); ++i)
+#pragma unroll
+        for (int st = 0; st < kSteps / 2; ++st) qf[i][st] = lds128(q_at + (i * (kSteps / 2) + st) * 512);
+    }
+    float o[NT][kPieces][4];
     // m: running maximum of x; o is relative to 2^(m + d), sum to 2^m
-    float m[MT][2], d[MT][2], sum[MT][2];
+    float m[NT][2], d[NT][2], sum[NT][2];
     uint32_t sv_top = 0, sv_low = 255;  // exponents of the value scales so far
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int j = 0; j < kOut; ++j)
+      for (int j = 0; j < kPieces; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
 #pragma unroll
@@ -497,46 +518,59 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         d[i][b] = sum[i][b] = 0.0f;
       }
     }
+    auto group_sync = [&] {
+      if (WM == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * WM) : "memory");
+    };
 
     int stage = 0;
     for (int tile = tile0 + kg; tile < tile1; tile += kGroups) {
       copy_wait<kStages - 2>();
       // the group's warps see this tile, and are done with the one that the next copy replaces
-      if (WM == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * WM) : "memory");
+      group_sync();
       issue(stage == 0 ? kStages - 1 : stage - 1, slot);
       copy_commit();
       next += kGroups;
       slot = slot_of(next);
 
       const uint32_t k_at = ring + stage * 2 * L::kTile, v_at = k_at + L::kTile;
-      float s[MT][4][4];
+      // scores: s[i][j][2 c + b] is key 16 j + 8 c + quad, row 8 i + 2 t + b
+      float s[NT][2][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[i][j][c] = 0.0f;
 #pragma unroll
       for (int half = 0; half < DIM / 64; ++half) {
-        uint4 kr[4];
+        uint32_t kr[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kr[j] = lds128(k_at + piece_at<DIM>(j * 8 + quad, half * 4 + t));
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = lds128(k_at + piece_at<DIM>(j * 8 + quad, half * 4 + t));
+          kr[j][0] = x.x;
+          kr[j][1] = x.y;
+          kr[j][2] = x.z;
+          kr[j][3] = x.w;
+        }
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          uint4 a[MT];
+        for (int s2 = 0; s2 < 2; ++s2) {
+          uint4 q[NT];
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            a[i] = lds128(smem_u32(smem + L::kQ) +
-                          ((wm * MT + i) * kSteps + half * 4 + st) * 512 + lane * 16);
+          for (int i = 0; i < NT; ++i)
+            q[i] = NT <= 2 ? qf[NT <= 2 ? i : 0][half * 2 + s2]
+                           : lds128(q_at + (i * (kSteps / 2) + half * 2 + s2) * 512);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t c = st == 0 ? kr[j].x : st == 1 ? kr[j].y : st == 2 ? kr[j].z : kr[j].w;
-            uint32_t b0, b1;
-            widen4(c, b0, b1);
+          for (int s1 = 0; s1 < 2; ++s1)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) mma(s[i][j], a[i].x, a[i].z, a[i].y, a[i].w, b0, b1);
-          }
+            for (int j = 0; j < 2; ++j) {
+              uint32_t a0, a1, a2, a3;
+              widen4(kr[2 * j][s2 * 2 + s1], a0, a2);
+              widen4(kr[2 * j + 1][s2 * 2 + s1], a1, a3);
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                mma(s[i][j], a0, a1, a2, a3, s1 ? q[i].z : q[i].x, s1 ? q[i].w : q[i].y);
+            }
         }
       }
 
@@ -546,57 +580,54 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
                         (kg * kStages + stage) * 2 * kKeys;
       {
         // exponents of the scales of the values (zeros weigh nothing and do not count)
-        const uint32_t e = __float_as_uint(sc[kKeys + lane]) >> 23;
-        const bool some = ((in >> lane) & 1) && sc[kKeys + lane] != 0.0f;
+        const float v = sc[kKeys + lane];
+        const bool some = ((in >> lane) & 1) && v != 0.0f;
+        const uint32_t e = __float_as_uint(v) >> 23;
         sv_top = max(sv_top, __reduce_max_sync(0xffffffffu, some ? e : 0u));
         sv_low = min(sv_low, __reduce_min_sync(0xffffffffu, some ? e : 255u));
       }
       const bool near = sv_top <= sv_low + 8 || sv_low == 255;
-      // some row of this warp ends inside this tile or before it
-      const bool ragged = __any_sync(0xffffffffu, (int64_t)(tile + 1) * kKeys > least);
-      float vs[4][2];
+      // some row of the unit ends inside this tile or before it
+      const bool ragged = (int64_t)(tile + 1) * kKeys > least;
+      float vs[2][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 ks = *reinterpret_cast<const float2*>(sc + j * 8 + 2 * t);
-        const float2 v2 = *reinterpret_cast<const float2*>(sc + kKeys + j * 8 + 2 * t);
-        vs[j][0] = v2.x;
-        vs[j][1] = v2.y;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int c = 0; c < 2; ++c) {
+          const float ks = sc[j * 16 + c * 8 + quad];
+          vs[j][c] = sc[kKeys + j * 16 + c * 8 + quad];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            s[i][j][2 * b] *= mul[i][b] * ks.x;
-            s[i][j][2 * b + 1] *= mul[i][b] * ks.y;
-          }
-      }
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s[i][j][2 * c + b] *= mul[i][b] * ks;
+        }
       const bool masked = ragged || in != 0xffffffffu;
       if (masked) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int at = j * 8 + 2 * t + c;
-            const int64_t pos = (int64_t)tile * kKeys + at;
-            const bool out = !((in >> at) & 1);
+          for (int b = 0; b < 2; ++b) {
+            const int end = s_len[row0 + i * 8 + 2 * t + b];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int b = 0; b < 2; ++b)
-                if (out || pos >= lim[i][b]) s[i][j][2 * b + c] = -INFINITY;
+              for (int c = 0; c < 2; ++c) {
+                const int at = j * 16 + c * 8 + quad;
+                if (!((in >> at) & 1) || (int64_t)tile * kKeys + at >= end)
+                  s[i][j][2 * c + b] = -INFINITY;
+              }
           }
       }
-      uint32_t pa[MT][2][4];
+      uint32_t pb[NT][2][2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float keep[2];
+      for (int i = 0; i < NT; ++i) {
+        float keep[2], w2[2][2][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float tm = -INFINITY;
+          float tm = fmaxf(fmaxf(s[i][0][b], s[i][0][2 + b]),
+                           fmaxf(s[i][1][b], s[i][1][2 + b]));  // NaN is no maximum
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tm = fmaxf(tm, fmaxf(s[i][j][2 * b], s[i][j][2 * b + 1]));  // NaN is no maximum
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+          for (int x = 4; x <= 16; x <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
           tm = fmaxf(tm, m[i][b]);
           // a row that has no key yet keeps -inf; 0 stands in for it in the differences
           const float um = tm == -INFINITY ? 0.0f : tm;
@@ -607,12 +638,12 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
           if (!near) {
             float tv = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int c = 0; c < 2; ++c)
-                tv = fmaxf(tv, s[i][j][2 * b + c] + log2_fast(vs[j][c]));
-            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 1));
-            tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 2));
+                tv = fmaxf(tv, s[i][j][2 * c + b] + log2_fast(vs[j][c]));
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
             // what there is already is at most 2^9 above 2^(m + d)
             dn = fmaxf(tv, m[i][b] + d[i][b]) - um;
             dn = dn > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : 0.0f;
@@ -623,66 +654,36 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
           m[i][b] = tm;
           d[i][b] = dn;
           const float f = exp2_fast(-dn);
-          float add = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float w2[2];
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float e = exp2_fast(s[i][j][2 * b + c] - um);
-              add += e;
-              w2[c] = e * vs[j][c] * f;  // in this order: f may be large where e is 0
+              const float e = exp2_fast(s[i][j][2 * c + b] - um);
+              sum[i][b] += e;
+              w2[j][c][b] = e * vs[j][c] * f;  // in this order: f may be large where e is 0
               // a key outside the row weighs 0, whatever the scale of its block is
-              if (masked && s[i][j][2 * b + c] == -INFINITY) w2[c] = 0.0f;
+              if (masked && s[i][j][2 * c + b] == -INFINITY) w2[j][c][b] = 0.0f;
             }
-            pa[i][j >> 1][(j & 1) * 2 + b] = pack_half(w2[0], w2[1]);
-          }
-          sum[i][b] += add;
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            pb[i][j][c] = transpose8(pack_half(w2[j][c][0], w2[j][c][1]));
         if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
 #pragma unroll
-          for (int j = 0; j < kOut; ++j) {
+          for (int j = 0; j < kPieces; ++j) {
             o[i][j][0] *= keep[0];
-            o[i][j][1] *= keep[0];
-            o[i][j][2] *= keep[1];
+            o[i][j][1] *= keep[1];
+            o[i][j][2] *= keep[0];
             o[i][j][3] *= keep[1];
           }
         }
       }
-      // ---- weights times values
-      auto add_values = [&](auto clean) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const int key = kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll
-          for (int cp = 0; cp < kPieces / 2; ++cp) {
-            const uint4 r = ldmatrix_trans(v_at + piece_at<DIM>(key, cp * 2 + (lane >> 4)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // bytes: (key 2t, channels 2n, 2n + 1), (key 2t + 1, the same)
-              uint32_t x = __byte_perm(e ? r.z : r.x, 0, 0x3120);
-              uint32_t y = __byte_perm(e ? r.w : r.y, 0, 0x3120);
-              if (decltype(clean)::value) {
-                x &= ~nan_codes(x);
-                y &= ~nan_codes(y);
-              }
-              uint32_t b0, b1, c0, c1;
-              widen4(x, b0, c0);
-              widen4(y, b1, c1);
-#pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                mma(o[i][cp * 4 + e * 2], pa[i][kk][0], pa[i][kk][1], pa[i][kk][2], pa[i][kk][3],
-                    b0, b1);
-                mma(o[i][cp * 4 + e * 2 + 1], pa[i][kk][0], pa[i][kk][1], pa[i][kk][2],
-                    pa[i][kk][3], c0, c1);
-              }
-            }
-          }
-        }
-      };
-      // A NaN code must not reach the rows that end before it (0 * NaN is NaN in a product).
-      // Only a tile in which a row ends can hold one that some rows see and others do not.
-      bool dirty = false;
+
+      // ---- a NaN code must not reach the rows that end before it (0 * NaN is NaN in a
+      // product). Only a tile in which a row ends can hold one that some rows see and others do
+      // not: there the rows that see it become NaN here, and the code a zero.
       if (ragged) {
         uint32_t nan = 0;
 #pragma unroll
@@ -690,29 +691,56 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
           const uint4 c = lds128(v_at + (j * 32 + lane) * 16);
           nan |= nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w);
         }
-        dirty = __any_sync(0xffffffffu, nan != 0);
+        if (__any_sync(0xffffffffu, nan != 0)) {
+          for (int key = 0; key < kKeys; ++key) {
+            const int64_t pos = (int64_t)tile * kKeys + key;
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {  // this thread's channels: 16 c + 2 quad ..
+              uint16_t codes;
+              asm volatile("ld.shared.u16 %0, [%1];"
+                           : "=h"(codes)
+                           : "r"(v_at + piece_at<DIM>(key, c) + 2 * quad));
+              const uint32_t bad = nan_codes(codes);
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  if (pos < s_len[row0 + i * 8 + 2 * t + b]) {
+                    if (bad & 1) o[i][c][b] = NAN;
+                    if (bad & 256) o[i][c][2 + b] = NAN;
+                  }
+            }
+          }
+          group_sync();
+#pragma unroll 1
+          for (int j = wm; j < L::kTile / 512; j += WM) {
+            const uint32_t at = v_at + (j * 32 + lane) * 16;
+            const uint4 c = lds128(at);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                         "r"(c.x & ~nan_codes(c.x)), "r"(c.y & ~nan_codes(c.y)),
+                         "r"(c.z & ~nan_codes(c.z)), "r"(c.w & ~nan_codes(c.w))
+                         : "memory");
+          }
+          group_sync();
+        }
       }
-      if (!dirty) {
-        add_values(std::false_type());
-      } else {
-        add_values(std::true_type());
-        for (int key = 0; key < kKeys; ++key) {
-          const int64_t pos = (int64_t)tile * kKeys + key;
+
+      // ---- values times weights: o[i][c][2 e + b] is channel 16 c + 2 quad + e, row 8 i + 2 t + b
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) {  // this thread's channels: 16 c + 4 t ..
-            uint32_t codes;
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(codes)
-                         : "r"(v_at + piece_at<DIM>(key, c) + 4 * t));
-            const uint32_t nan = nan_codes(codes);
+      for (int kk = 0; kk < 2; ++kk) {
+        const int key = kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((nan >> (8 * e)) & 1)
+        for (int cp = 0; cp < kPieces / 2; ++cp) {
+          const uint4 r = ldmatrix_trans(v_at + piece_at<DIM>(key, cp * 2 + (lane >> 4)));
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+          for (int e = 0; e < 2; ++e) {
+            // bytes: (key 2t, channels 2 quad, 2 quad + 1), (key 2t + 1, the same)
+            uint32_t a0, a1, a2, a3;
+            widen4(__byte_perm(e ? r.z : r.x, 0, 0x3120), a0, a1);
+            widen4(__byte_perm(e ? r.w : r.y, 0, 0x3120), a2, a3);
 #pragma unroll
-                  for (int b = 0; b < 2; ++b)
-                    if (pos < lim[i][b]) o[i][2 * c + (e & 1)][2 * b + (e >> 1)] = NAN;
+            for (int i = 0; i < NT; ++i)
+              mma(o[i][cp * 2 + e], a0, a1, a2, a3, pb[i][kk][0], pb[i][kk][1]);
           }
         }
       }
@@ -722,25 +750,24 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     __syncthreads();  // the ring is free: it takes the warps' sums
 
     // ---- join the warp groups
+    float* s_sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         float x = sum[i][b];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        const int r = row0 + i * 16 + b * 8 + quad;
-        if (t == 0) {
-          float* st = s_stat + (kg * kRows + r) * 3;
-          st[0] = m[i][b];
-          st[1] = m[i][b] + d[i][b];
-          st[2] = x;
+#pragma unroll
+        for (int y = 4; y <= 16; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+        const int r = kg * kRows + row0 + i * 8 + 2 * t + b;
+        if (quad == 0) {
+          s_stat[r * 3] = m[i][b];
+          s_stat[r * 3 + 1] = m[i][b] + d[i][b];
+          s_stat[r * 3 + 2] = x;
         }
-        float4* dst = reinterpret_cast<float4*>(smem) + (kg * kRows + r) * (DIM / 4) + t;
 #pragma unroll
         for (int c = 0; c < kPieces; ++c)
-          dst[c * 4] = make_float4(o[i][2 * c][2 * b], o[i][2 * c + 1][2 * b],
-                                   o[i][2 * c][2 * b + 1], o[i][2 * c + 1][2 * b + 1]);
+          *reinterpret_cast<float2*>(s_sums + r * L::kLd + 16 * c + 2 * quad) =
+              make_float2(o[i][c][b], o[i][c][2 + b]);
       }
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == tiles;
@@ -762,7 +789,8 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         const float* st = s_stat + (k * kRows + r) * 3;
         l += st[2] * exp2_fast(st[0] - ut);
         const float f = exp2_fast(st[1] - uv);
-        const float4 y = reinterpret_cast<const float4*>(smem)[(k * kRows + r) * (DIM / 4) + c4];
+        const float4 y =
+            *reinterpret_cast<const float4*>(s_sums + (k * kRows + r) * L::kLd + c4 * 4);
         v[0] += y.x * f;
         v[1] += y.y * f;
         v[2] += y.z * f;
@@ -781,8 +809,12 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         }
       }
     }
-    if (!whole && tile0 == 0)
-      mine = {g, h, (int32_t)(((first_tile + tiles) * n - 1) / all), 0};
+    if (tile0 == 0) {
+      const Shared u = {g, h, (int32_t)me,
+                        whole ? -1 : (int32_t)(((first_tile + tiles) * n - 1) / all)};
+      if (units > kMaxCtas) mine = whole ? mine : u;
+      else if (tid == 0) p.shared[(int64_t)g * p.kv_heads + h] = u;
+    }
     __syncthreads();  // the shared arrays are free for the next unit
 
     // ---- next unit
@@ -797,68 +829,112 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       }
     }
   }
-  if (tid == 0) p.shared[me] = mine;
+  if (tid == 0 && units > kMaxCtas) p.shared[me] = mine;
   if (err && p.status) atomicOr(p.status, err);
 }
 
-// Joins the parts of the shared units: CTA (i, y) the rows y, y + gridDim.y, .. of the unit
-// that starts in CTA i of the launch before. A warp takes a row: the lanes look at the parts'
-// maxima, then each sums its channels over the parts, in the order of the parts.
-constexpr int kJoinThreads = 256;
+// Joins the parts of the shared units: CTA (i, y) the rows y, y + gridDim.y, .. of entry i. The
+// warps take a row's parts in turn, each lane 16th .. of its channels, and meet in shared memory in
+// the order of the warps.
+constexpr int kJoinWarps = 8;
 
 template <int DIM, bool FP16, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+kv8_join_kernel(const __grid_constant__ Params p) {
   using Q = Part<DIM, ROWS>;
   constexpr int kVec = DIM / 32;  // channels of a lane
+  __shared__ float s_v[kJoinWarps][DIM];
+  __shared__ float s_st[kJoinWarps][3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int a = blockIdx.x;
-  const Shared u = p.shared[a];
+  const Shared u = p.shared[blockIdx.x];
   if (u.last < 0) return;
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
-  const float* first = p.parts + (2 * (int64_t)a + 1) * Q::kFloats;
-  const float* rest = p.parts + 2 * (int64_t)a * Q::kFloats;  // + 2 c parts on, c >= 1
-  const int parts = u.last - a + 1;
-  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < live;
-       r += gridDim.y * (kJoinThreads / 32)) {
-    auto at = [&](int c) { return c == 0 ? first : rest + 2 * (int64_t)c * Q::kFloats; };
-    float top = -INFINITY, topv = -INFINITY;
-    for (int c = lane; c < parts; c += 32) {
-      const float2 st = __ldcg(reinterpret_cast<const float2*>(at(c) + Q::kStat + r * 4));
-      top = fmaxf(top, st.x);
-      topv = fmaxf(topv, st.y);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
-    }
-    const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
-    float l = 0.0f, v[kVec];
+  const int parts = u.last - u.first + 1;
+  // the first CTA's part is its second one, the others' are their first
+  auto part = [&](int c) {
+    return p.parts + (2 * (int64_t)(u.first + c) + (c == 0)) * Q::kFloats;
+  };
+  for (int r = blockIdx.y; r < live; r += gridDim.y) {
+    float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < parts; ++c) {
-      const float* q = at(c);
-      const float4 st = __ldcg(reinterpret_cast<const float4*>(q + Q::kStat + r * 4));
-      float y[kVec];
-      if (kVec == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(q + r * DIM) + lane);
-        y[0] = x.x;
-        y[1] = x.y;
-        y[kVec - 2] = x.z;
-        y[kVec - 1] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(q + r * DIM) + lane);
-        y[0] = x.x;
-        y[1] = x.y;
-      }
-      l += st.z * exp2_fast(st.x - ut);
-      const float f = exp2_fast(st.y - uv);
+    for (int c0 = warp; c0 < parts; c0 += 4 * kJoinWarps) {
+      float4 st[4];
+      float y[4][kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] += y[i] * f;
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + k * kJoinWarps;
+        if (c < parts) {
+          const float* q = part(c);
+          st[k] = __ldcg(reinterpret_cast<const float4*>(q + Q::kStat + r * 4));
+          const float* src = q + r * DIM + lane * kVec;
+          if (kVec == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            y[k][0] = x.x;
+            y[k][1] = x.y;
+            y[k][kVec - 2] = x.z;
+            y[k][kVec - 1] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            y[k][0] = x.x;
+            y[k][1] = x.y;
+          }
+        } else {
+          st[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) y[k][i] = 0.0f;
+        }
+      }
+      float nt = top, nv = topv;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        nt = fmaxf(nt, st[k].x);
+        nv = fmaxf(nv, st[k].y);
+      }
+      const float ut = nt == -INFINITY ? 0.0f : nt, uv = nv == -INFINITY ? 0.0f : nv;
+      l *= exp2_fast(top - ut);
+      const float keep = exp2_fast(topv - uv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] *= keep;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l += st[k].z * exp2_fast(st[k].x - ut);
+        const float f = exp2_fast(st[k].y - uv);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] += y[k][i] * f;
+      }
+      top = nt;
+      topv = nv;
     }
-    write_row<DIM, FP16, kVec>(p, u.g, u.h, r, lane, v, top, topv, l);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) s_v[warp][lane * kVec + i] = v[i];
+    if (lane == 0) {
+      s_st[warp][0] = top;
+      s_st[warp][1] = topv;
+      s_st[warp][2] = l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) {
+        top = fmaxf(top, s_st[w][0]);
+        topv = fmaxf(topv, s_st[w][1]);
+      }
+      const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
+      l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        l += s_st[w][2] * exp2_fast(s_st[w][0] - ut);
+        const float f = exp2_fast(s_st[w][1] - uv);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] += s_v[w][lane * kVec + i] * f;
+      }
+      write_row<DIM, FP16, kVec>(p, u.g, u.h, r, lane, v, top, topv, l);
+    }
+    __syncthreads();
   }
 }
 
@@ -892,17 +968,19 @@ int check_common(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, 
   return KV8_OK;
 }
 
-// CTAs of a launch on the current device, or < 0.
-int grid_size() {
+// SMs of the current device, or < 0.
+int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return -1;
-  return sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+  return sms;
 }
 
 // Rows that the variant for a unit of `live` rows pads to.
-int padded_rows(int live) { return live <= 16 ? 16 : live <= 32 ? 32 : live <= 64 ? 64 : 128; }
+int padded_rows(int live) {
+  return live <= 8 ? 8 : live <= 16 ? 16 : live <= 32 ? 32 : live <= 64 ? 64 : 128;
+}
 
 int shift_of(int x) {
   if (x & (x - 1)) return -1;
@@ -911,45 +989,60 @@ int shift_of(int x) {
   return s;
 }
 
-template <int DIM, bool FP16, bool SELECTED, int MT, int WM>
-int launch(const Params& p, int grid, cudaStream_t s) {
-  using L = Smem<DIM, MT, WM>;
-  const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, MT, WM>;
+template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
+int launch(const Params& p, int sms, cudaStream_t s) {
+  using L = Smem<DIM, NT, WM>;
+  const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, NT, WM>;
+  const auto join = kv8_join_kernel<DIM, FP16, L::kRows>;
+  // both with the largest share of shared memory: a change of it between them would cost time
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) !=
-      cudaSuccess)
+          cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+          cudaSuccess)
     return KV8_ERR_CUDA;
+  // a tile for each warp group of a CTA, where there is that little work
+  const int64_t groups = ((int64_t)p.rows + p.group_rows - 1) / p.group_rows;
+  const int64_t units = groups * p.kv_heads;
+  const int64_t tiles = p.max_len < kKeys ? 1 : ((int64_t)p.max_len + kKeys - 1) / kKeys;
+  if (units > (int64_t(1) << 33)) return KV8_ERR_SHAPE;
+  const int64_t want = units * ((tiles + L::kGroups - 1) / L::kGroups);
+  const int64_t most = sms * L::kCtas < kMaxCtas ? sms * L::kCtas : kMaxCtas;
+  const int grid = (int)(want < most ? want : most);
   kernel<<<(unsigned)grid, kThreads, L::kTotal, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return KV8_ERR_CUDA;
   // the join is launched while the first kernel runs and waits for its end
-  constexpr int kWarpsJoin = kJoinThreads / 32;
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  const int entries = units > kMaxCtas ? grid : (int)units;
+  const int rows = 4096 / entries < 1 ? 1 : 4096 / entries;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((live + kWarpsJoin - 1) / kWarpsJoin));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3((unsigned)entries, (unsigned)(live < rows ? live : rows));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_join_kernel<DIM, FP16, L::kRows>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
 }
 
 template <int DIM, bool FP16, bool SELECTED>
-int launch_rows(const Params& p, int live, int grid, cudaStream_t s) {
-  switch (padded_rows(live)) {
-    case 16: return launch<DIM, FP16, SELECTED, 1, 1>(p, grid, s);
-    case 32: return launch<DIM, FP16, SELECTED, 2, 1>(p, grid, s);
-    case 64: return launch<DIM, FP16, SELECTED, 2, 2>(p, grid, s);
-    default: return launch<DIM, FP16, SELECTED, 2, 4>(p, grid, s);
+int launch_rows(const Params& p, int live, int sms, cudaStream_t s) {
+  if constexpr (SELECTED) {  // at most 16 rows to a unit
+    return live <= 8 ? launch<DIM, FP16, true, 1, 1>(p, sms, s)
+                     : launch<DIM, FP16, true, 2, 1>(p, sms, s);
+  } else {
+    switch (padded_rows(live)) {
+      case 8: return launch<DIM, FP16, false, 1, 1>(p, sms, s);
+      case 16: return launch<DIM, FP16, false, 2, 1>(p, sms, s);
+      case 32: return launch<DIM, FP16, false, 4, 1>(p, sms, s);
+      case 64: return launch<DIM, FP16, false, 4, 2>(p, sms, s);
+      default: return launch<DIM, FP16, false, 4, 4>(p, sms, s);
+    }
   }
-}
-
-// The selected form has at most 16 rows to a unit.
-template <int DIM, bool FP16>
-int launch_rows_selected(const Params& p, int grid, cudaStream_t s) {
-  return launch<DIM, FP16, true, 1, 1>(p, grid, s);
 }
 
 Params common(const void* q, int64_t q_ld, int rows, int q_heads, int kv_heads, float sm_scale,
@@ -980,36 +1073,21 @@ Params common(const void* q, int64_t q_ld, int rows, int q_heads, int kv_heads, 
 // Fills in the workspace and launches the variant for these sizes.
 template <bool SELECTED>
 int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaStream_t s) {
-  const int rows = SELECTED ? 1 : p.group_rows;
-  const int64_t need = kv8_attention_workspace_bytes(p.q_heads, p.kv_heads, dim, rows);
+  const int64_t need =
+      kv8_attention_workspace_bytes(p.q_heads, p.kv_heads, dim, SELECTED ? 1 : p.group_rows);
   if (need < 0) return (int)need;
   if (ws_bytes < need) return KV8_ERR_WORKSPACE;
-  const int most = grid_size();
-  if (most < 0) return KV8_ERR_CUDA;
-  // one tile for each warp of a CTA at least, where there is that little work
-  const int64_t groups = ((int64_t)p.rows + rows - 1) / rows;
-  const int64_t tiles = p.max_len < kKeys ? 1 : ((int64_t)p.max_len + kKeys - 1) / kKeys;
-  const int64_t units = groups * p.kv_heads;
-  if (units > (int64_t(1) << 33)) return KV8_ERR_SHAPE;
-  const int64_t want = units * ((tiles + kWarps - 1) / kWarps);
-  const int grid = (int)(want < most ? want : most);
+  const int sms = sm_count();
+  if (sms < 0) return KV8_ERR_CUDA;
   p.shared = reinterpret_cast<Shared*>(workspace);
   p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
                                      kMaxCtas * sizeof(Shared));
-  const int live = rows * (p.q_heads / p.kv_heads);
-  if constexpr (SELECTED) {
-    if (dim == 128)
-      return dtype == KV8_FP16 ? launch_rows_selected<128, true>(p, grid, s)
-                               : launch_rows_selected<128, false>(p, grid, s);
-    return dtype == KV8_FP16 ? launch_rows_selected<64, true>(p, grid, s)
-                             : launch_rows_selected<64, false>(p, grid, s);
-  } else {
-    if (dim == 128)
-      return dtype == KV8_FP16 ? launch_rows<128, true, false>(p, live, grid, s)
-                               : launch_rows<128, false, false>(p, live, grid, s);
-    return dtype == KV8_FP16 ? launch_rows<64, true, false>(p, live, grid, s)
-                             : launch_rows<64, false, false>(p, live, grid, s);
-  }
+  const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  if (dim == 128)
+    return dtype == KV8_FP16 ? launch_rows<128, true, SELECTED>(p, live, sms, s)
+                             : launch_rows<128, false, SELECTED>(p, live, sms, s);
+  return dtype == KV8_FP16 ? launch_rows<64, true, SELECTED>(p, live, sms, s)
+                           : launch_rows<64, false, SELECTED>(p, live, sms, s);
 }
 
 }  // namespace
@@ -1017,10 +1095,11 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
 extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
                                                  int group_rows) {
   if (!heads_ok(q_heads, kv_heads, dim, group_rows)) return KV8_ERR_SHAPE;
-  const int ctas = grid_size();
-  if (ctas < 0) return KV8_ERR_CUDA;
-  return kMaxCtas * (int64_t)sizeof(Shared) +
-         (int64_t)ctas * 2 * padded_rows(group_rows * (q_heads / kv_heads)) * (dim + 4) * 4;
+  const int sms = sm_count();
+  if (sms < 0) return KV8_ERR_CUDA;
+  const int rows = padded_rows(group_rows * (q_heads / kv_heads));
+  const int64_t ctas = sms * 3 < kMaxCtas ? sms * 3 : kMaxCtas;  // most of any variant
+  return kMaxCtas * (int64_t)sizeof(Shared) + ctas * 2 * rows * (dim + 4) * 4;
 }
 
 extern "C" int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,
