@@ -40,7 +40,8 @@ enum {
   VERIFY_STATUS_COUNT = 1,  /* n_drafts[j] outside [0, drafts]: its outputs are -1, kept 0 */
   VERIFY_STATUS_TOKEN = 2,  /* a tested draft token outside [0, vocab): refused */
   VERIFY_STATUS_PROB = 4,   /* a probability that was read is NaN, negative or > 1: taken as
-                               0, 0 and 1; or a row sums to more than 8 */
+                               0, 0 and 1; or the weights sum to more than 8 (the token is -1
+                             where they sum to 15 or more) */
   VERIFY_STATUS_EMPTY = 8,  /* the row to draw from is 0 everywhere: the token is -1 */
   VERIFY_STATUS_UNIFORM = 16 /* a uniform that was read outside [0, 1) or NaN: clamped (NaN
                                to 0) */

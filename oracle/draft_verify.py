@@ -86,6 +86,9 @@ def verify(target, draft, tokens, uniforms, n_drafts=None, mutant=0):
         else:
             if total > 8 * ONE:
                 w.status |= PROB
+            if total >= 15 * ONE:
+                status |= w.status
+                continue
             at = total * int(Fraction(r) * (1 << 64)) >> 64
             run = 0
             for v, x in enumerate(weights):

@@ -3,10 +3,12 @@
 // A request reads two probabilities per draft for the tests and then one row (the bonus
 // row) or two (target and draft of the refused position) of the vocabulary: bound by HBM for
 // a batch, by latency for one request. A cluster of C CTAs takes a request; every CTA decides
-// the tests for itself (a few loads), each sums its slice of the weights, the slices' sums
-// meet through distributed shared memory, and the CTA, then the warp, whose range holds the
-// drawn point reads its part again (from L2) to find the token. Sums are 64-bit integers, so the split
-// of the row does not show in the result.
+// the tests for itself (a few loads), each warp sums a slice of the weights in steps of 256
+// tokens, 8 consecutive 32s, all loads of a step on their way together, and keeps the sum of
+// each step in shared memory. The slices' sums meet through distributed shared memory; the
+// warp whose slice holds the drawn point finds the step from the sums kept, and reads this
+// step alone again. Sums are 64-bit integers, so the split of the row does not show in the
+// result.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -18,8 +20,8 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kStep = 8;      // tokens of a lane in a step
+constexpr int kRecords = 64;  // sums of steps that a warp keeps
 
 struct Params {
   const float* target;
@@ -37,7 +39,7 @@ struct Params {
 };
 
 __device__ __forceinline__ float checked_prob(float x, int* err) {
-  if (!(x >= 0.0f && x <= 1.0f)) {
+  if (__float_as_uint(x) > 0x3F800000u && !(x == 0.0f)) {  // above 1, negative or NaN
     *err |= VERIFY_STATUS_PROB;
     return x > 1.0f ? 1.0f : 0.0f;
   }
@@ -52,8 +54,16 @@ __device__ __forceinline__ float checked_uniform(float u, int* err) {
   return u;
 }
 
-// A probability in units of 2^-60. x * 2^60 is exact, the conversion drops what is below.
-__device__ __forceinline__ uint64_t units(float x) { return __float2ull_rz(x * 0x1p60f); }
+// A probability in [0, 1] in units of 2^-60, rounded down: its 24 significant bits, shifted. In
+// integer operations, as the conversion to 64 bits is slow: 45 us against MEASURED for 64 requests.
+__device__ __forceinline__ uint64_t units(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const uint32_t e = (b >> 23) & 0xFF, m = (b << 8) | 0x80000000u;
+  const uint32_t s = 130 - e;  // m * 2^32 >> s; 3 for 1.0
+  const uint32_t lo = s <= 32 ? __funnelshift_rc(0, m, s) : s < 64 ? m >> (s - 32) : 0;
+  const uint32_t hi = s < 32 ? m >> s : 0;
+  return ((uint64_t)hi << 32) | lo;  // a subnormal is below the last bit
+}
 
 // max(p - q, 0) in those units; a non-negative q >= p gives 0.
 __device__ __forceinline__ uint64_t weight(float p, float q) {
@@ -63,12 +73,29 @@ __device__ __forceinline__ uint64_t weight(float p, float q) {
 
 enum Row { kBonus, kRefused, kRefusedPoint };
 
-__device__ __forceinline__ uint64_t weight_at(const float* p, const float* q, Row row, int point,
-                                              int v, int* err) {
-  const float a = checked_prob(__ldg(p + v), err);
-  if (row == kRefused) return weight(a, checked_prob(__ldg(q + v), err));
-  if (row == kRefusedPoint && v == point) return 0;
-  return units(a);
+// The weights of tokens v0 + 32 i + lane, i < kStep; 0 past `end`. Tokens past it read the
+// row's last one instead, so that no load waits for a condition.
+__device__ __forceinline__ void step_weights(const float* p, const float* q, Row row, int point,
+                                             int v0, int end, uint64_t (&w)[kStep], int* err) {
+  const int lane = threadIdx.x & 31;
+  float a[kStep], b[kStep];
+#pragma unroll
+  for (int i = 0; i < kStep; ++i) a[i] = __ldg(p + min(v0 + i * 32 + lane, end - 1));
+  if (row == kRefused) {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) b[i] = __ldg(q + min(v0 + i * 32 + lane, end - 1));
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) w[i] = weight(checked_prob(a[i], err), checked_prob(b[i], err));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      w[i] = units(checked_prob(a[i], err));
+      if (row == kRefusedPoint && v0 + i * 32 + lane == point) w[i] = 0;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kStep; ++i)
+    if (v0 + i * 32 + lane >= end) w[i] = 0;
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -77,14 +104,18 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(Params p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(Params p) {
+  constexpr int kWarps = THREADS / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int req = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int s_kept;
   __shared__ uint64_t s_sum[kWarps];
-  __shared__ uint64_t s_cta;  // read by the cluster
+  __shared__ uint64_t s_high[kWarps];
+  __shared__ uint64_t s_cta[2];  // read by the cluster: the sum, and that of its upper halves
+  __shared__ uint64_t s_step[kWarps][kRecords];
   int err = 0;
 
   const int n = p.n_drafts ? __ldg(p.n_drafts + req) : p.drafts;
@@ -131,67 +162,103 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(Params p) {
   const int point = kept < n ? __ldg(tok + kept) : -1;
   Row row = kept == n ? kBonus : qrow ? kRefused : kRefusedPoint;
 
-  // slices: CTA, then warp, each a whole number of 32s
-  const int per_warp = ((p.vocab + ranks * kWarps - 1) / (ranks * kWarps) + 31) & ~31;
-  const int64_t begin64 = ((int64_t)rank * kWarps + warp) * per_warp;
+  // slices: CTA, then warp, each a whole number of steps; a record sums `each` steps
+  constexpr int kTokens = 32 * kStep;
+  const int parts = ranks * kWarps;
+  const int64_t stride = (int64_t)parts * kTokens;
+  const int steps = (int)((p.vocab + stride - 1) / stride);
+  const int each = (steps + kRecords - 1) / kRecords;
+  const int64_t begin64 = ((int64_t)rank * kWarps + warp) * steps * kTokens;
   const int begin = (int)min(begin64, (int64_t)p.vocab);
-  const int end = (int)min(begin64 + per_warp, (int64_t)p.vocab);
+  const int end = (int)min(begin64 + (int64_t)steps * kTokens, (int64_t)p.vocab);
 
-  uint64_t total = 0, before = 0;
+  // A row that sums to 16 or more would wrap the sums: the upper halves tell
+  uint64_t total = 0, before = 0, high = 0;
   for (int round = 0; round < 2; ++round) {
-    uint64_t sum = 0;
-#pragma unroll 8
-    for (int v = begin + lane; v < end; v += 32) sum += weight_at(prow, qrow, row, point, v, &err);
-    sum = warp_sum(sum);
-    if (lane == 0) s_sum[warp] = sum;
+    uint64_t sum = 0, record = 0, upper = 0;
+    int v0 = begin;
+    for (int i = 0; v0 < end; ++i, v0 += kTokens) {
+      uint64_t w[kStep], x = 0;
+      step_weights(prow, qrow, row, point, v0, end, w, &err);
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) x += w[k];
+      upper += x >> 32;
+      x = warp_sum(x);
+      sum += x;
+      record += x;
+      if (i % each == each - 1 || v0 + kTokens >= end) {
+        if (lane == 0) s_step[warp][i / each] = record;
+        record = 0;
+      }
+    }
+    upper = warp_sum(upper);
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_high[warp] = upper;
+    }
     __syncthreads();
-    if (tid == 0) {
-      uint64_t c = 0;
-      for (int w = 0; w < kWarps; ++w) c += s_sum[w];
-      s_cta = c;
+    if (warp == 0) {
+      const uint64_t c = warp_sum(lane < kWarps ? s_sum[lane] : 0);
+      const uint64_t d = warp_sum(lane < kWarps ? s_high[lane] : 0);
+      if (lane == 0) {
+        s_cta[0] = c;
+        s_cta[1] = d;
+      }
     }
     cluster.sync();
-    total = before = 0;
+    total = before = high = 0;
     for (int r = 0; r < ranks; ++r) {
-      const uint64_t c = *cluster.map_shared_rank(&s_cta, r);
-      if (r < rank) before += c;
-      total += c;
+      const uint64_t* c = cluster.map_shared_rank(s_cta, r);
+      if (r < rank) before += c[0];
+      total += c[0];
+      high += c[1];
     }
-    if (total || row == kBonus) break;
+    if (total || high || row == kBonus) break;
     row = kBonus;  // nothing is left of p - q: draw from p itself
     cluster.sync();
   }
 
   const float r = checked_uniform(__ldg(uni + p.drafts), &err);
   const uint64_t at = __umul64hi(total, __float2ull_rz(r * 0x1p64f));  // floor(r * total)
-  if (total > (uint64_t(1) << 63)) err |= VERIFY_STATUS_PROB;
+  const bool lost = high >= uint64_t(15) << 28;
+  if (lost || total > (uint64_t(1) << 63)) err |= VERIFY_STATUS_PROB;
   for (int w = 0; w < warp; ++w) before += s_sum[w];
   const uint64_t mine = s_sum[warp];
   // the warp whose range holds the point: before <= at < before + mine
-  if (total && at >= before && at - before < mine) {
+  if (total && !lost && at >= before && at - before < mine) {
     uint64_t run = before;
+    int i = 0;
+    while (run + s_step[warp][i] <= at) run += s_step[warp][i++];  // ends: run + mine > at
     int ignored = 0;
-    for (int v0 = begin; v0 < end; v0 += 32) {
-      const int v = v0 + lane;
-      uint64_t x = v < end ? weight_at(prow, qrow, row, point, v, &ignored) : 0;
+    for (int v0 = begin + i * each * kTokens;; v0 += kTokens) {
+      uint64_t w[kStep];
+      step_weights(prow, qrow, row, point, v0, end, w, &ignored);
+      int token = -1;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+      for (int k = 0; k < kStep; ++k) {
+        uint64_t x = w[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, run + x > at);
+        if (past && token < 0) token = v0 + k * 32 + __ffs(past) - 1;
+        run += __shfl_sync(0xffffffffu, x, 31);
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, run + x > at);
-      if (past) {
-        if (lane == 0) out[kept] = v0 + __ffs(past) - 1;
+      if (token >= 0 || v0 + kTokens >= end) {
+        if (lane == 0) out[kept] = token;
         break;
       }
-      run += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   if (rank == 0) {
     if (tid <= p.drafts && tid != kept) out[tid] = tid < kept ? __ldg(tok + tid) : -1;
     if (tid == 0) {
       p.kept[req] = kept;
-      if (total == 0) {
+      if (lost) {
+        out[kept] = -1;
+      } else if (total == 0) {
         out[kept] = -1;
         err |= VERIFY_STATUS_EMPTY;
       }
@@ -226,14 +293,19 @@ extern "C" int draft_verify(const float* target, int64_t target_req, int64_t tar
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return VERIFY_ERR_CUDA;
-  // CTAs per request: up to 8 while the batch leaves SMs idle and a CTA keeps 4096 tokens
+  // CTAs per request: up to 8 while they all run at once (1024 threads to an SM) and a warp has
+  // a step to sum. Few requests take CTAs of 512 threads, more of them smaller ones, which
+  // spread evenly: 64 requests of 100K tokens 256 x 512 threads MEASURED, 512 x 256 MEASURED.
+  const int threads = (int64_t)reqs * 8 <= 2 * sms ? 512 : 256;
   int c = 8;
-  while (c > 1 && ((int64_t)reqs * c > 2 * sms || vocab / c < 4096)) c >>= 1;
+  while (c > 1 && ((int64_t)reqs * c * threads > (int64_t)1024 * sms ||
+                   vocab <= c / 2 * threads * kStep))
+    c >>= 1;
   const Params p{target,   target_req, target_row, draft, draft_req,  draft_row, tokens,
                  n_drafts, uniforms,   drafts,     vocab, out_tokens, kept,      status};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(reqs * c));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -241,6 +313,7 @@ extern "C" int draft_verify(const float* target, int64_t target_req, int64_t tar
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, draft_verify_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, threads == 512 ? draft_verify_kernel<512> : draft_verify_kernel<256>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? VERIFY_OK : VERIFY_ERR_CUDA;
 }

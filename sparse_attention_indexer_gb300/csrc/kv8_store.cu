@@ -2,14 +2,17 @@
 // and e4m3 codes (the rule is stated in include/kv8_attention.h).
 //
 // Work split. A run is a maximal stretch of consecutive tokens of the call that lie in one
-// block; run x head x {K, V} is one CTA's work, since its scale needs every token of the
-// run and, where the block has earlier tokens, their old scale and codes. The first token
+// block; (run, head, K or V) is a unit of work, a warp's, since its scale needs every token of
+// the run and, where the block has earlier tokens, their old scale and codes. The first token
 // of a run is found from its neighbour (same table row, position one less, same block), so
-// the launch needs no lengths from the host: CTA c looks at tokens [c * chunk, (c + 1) *
-// chunk) and serves the runs that start there.
+// the launch needs no lengths from the host: CTA (c, y) looks at tokens [c * chunk, (c + 1) *
+// chunk), and its warps serve the runs that start there for the four units of share y.
 //
-// A row of dim 16-bit values is one 16-byte load per lane of dim / 8 lanes. The run's rows
-// stay in registers between the maximum and the rounding, so each input byte is read once.
+// Bound by HBM for a prefill (6 bytes per element moved), by the chain of loads (positions,
+// page, values) for a decode step. A warp asks for all rows of its unit at once with cp.async,
+// 16 bytes to a lane: they stay in shared memory between the maximum and the rounding, so that each
+// input byte is read once, and no warp waits for another after the marks of the starts are made.
+// (With the rows in registers, half as many bytes were on their way.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -22,8 +25,9 @@
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHold = 8;        // rows a thread keeps in registers
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunk = 128;  // tokens whose run starts one CTA looks for
+constexpr int kWindow = 384;    // tokens from a CTA's first whose marks it keeps
 
 struct Params {
   const uint16_t* x[2];  // K, V
@@ -42,6 +46,7 @@ struct Params {
   int64_t num_slots;
   int32_t* status;
   int chunk;
+  int hold;  // rows of a unit that stay in shared memory
 };
 
 // Whether token t starts a run: it does not continue token t - 1 inside one block.
@@ -71,29 +76,46 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// Magnitudes of two 16-bit values order like their bits without the sign: running maxima of the
+// lower and the upper halves, infinities and NaN among them.
+__device__ __forceinline__ uint32_t max8(const uint4& v, uint32_t m) {
+  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+  return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+
+// The same over the finite values alone.
 template <bool FP16>
-__device__ __forceinline__ float amax8(const uint4& v, float a) {
+__device__ __forceinline__ uint32_t max8_finite(const uint4& v, uint32_t m) {
+  constexpr uint32_t kInf = FP16 ? 0x7C007C00u : 0x7F807F80u;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = widen<FP16>(w[i]);
-    const float x = fabsf(f.x), y = fabsf(f.y);
-    a = fmaxf(a, x < INFINITY ? x : 0.0f);  // finite magnitudes only
-    a = fmaxf(a, y < INFINITY ? y : 0.0f);
+    const uint32_t x = w[i] & 0x7FFF7FFFu;
+    m = __vmaxu2(m, x & ~__vcmpgeu2(x, kInf));
   }
-  return a;
+  return m;
 }
 
 // x / s as codes. A power of two divides exactly by its reciprocal; a scale that the cache
 // came with may be any number and takes the division.
 template <bool FP16>
-__device__ __forceinline__ uint2 codes8(const uint4& v, float s, float inv, bool pow2) {
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+  const float2 a = widen<FP16>(v.x), b = widen<FP16>(v.y), c = widen<FP16>(v.z),
+               d = widen<FP16>(v.w);
+  return make_uint2(e4m3x2(a.x * inv, a.y * inv) | (e4m3x2(b.x * inv, b.y * inv) << 16),
+                    e4m3x2(c.x * inv, c.y * inv) | (e4m3x2(d.x * inv, d.y * inv) << 16));
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint2 codes8_div(const uint4& v, float s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = widen<FP16>(w[i]);
-    c[i] = pow2 ? e4m3x2(f.x * inv, f.y * inv) : e4m3x2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    c[i] = e4m3x2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
@@ -110,35 +132,60 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
   return out;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int DIM, bool FP16>
-__global__ void __launch_bounds__(kThreads) kv8_store_kernel(Params p) {
-  constexpr int kLanes = DIM / 8;                // lanes of one token's row
-  constexpr int kRows = kThreads / kLanes;       // rows per pass
+__global__ void __launch_bounds__(kThreads) kv8_store_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = DIM / 8;       // lanes of one token's row
+  constexpr int kRows = 32 / kLanes;    // rows a warp loads at a time
+  extern __shared__ __align__(16) uint4 s_rows[];
+  __shared__ uint8_t s_start[kWindow];
   __shared__ int s_first[kMaxChunk];
-  __shared__ int s_runs, s_len;
-  __shared__ float s_max[kThreads / 32];
-  const int tid = threadIdx.x;
-  const int head = blockIdx.y, kv = blockIdx.z;
+  __shared__ int s_runs;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int t0 = blockIdx.x * p.chunk;
 
-  if (p.chunk == 1) {
-    if (!starts_run(p, t0)) return;  // the same for every thread
-    if (tid == 0) {
-      s_runs = 1;
-      s_first[0] = t0;
-    }
-  } else {
-    if (tid == 0) s_runs = 0;
-    __syncthreads();
-    if (tid < p.chunk && t0 + tid < p.tokens && starts_run(p, t0 + tid))
-      s_first[atomicAdd(&s_runs, 1)] = t0 + tid;  // the order does not matter
+  if (tid == 0) s_runs = 0;
+  const int window = min(min(p.chunk + p.block, kWindow), p.tokens - t0);
+#pragma unroll
+  for (int i = 0; i < kWindow / kThreads; ++i) {
+    const int x = i * kThreads + tid;
+    if (x < window) s_start[x] = starts_run(p, t0 + x);
   }
   __syncthreads();
+  if (tid < p.chunk && tid < window && s_start[tid])
+    s_first[atomicAdd(&s_runs, 1)] = t0 + tid;  // the order does not matter
+  __syncthreads();
   const int runs = s_runs;
+
+  const int u = blockIdx.y * kWarps + warp;  // unit: head u / 2, K or V
+  if (u >= 2 * p.heads) return;
+  const int head = u >> 1, kv = u & 1;
+  const int lane = tid % kLanes, sub = (tid & 31) / kLanes;
+  uint4* rows = s_rows + (int64_t)warp * p.hold * kLanes;
+  const int64_t ld = p.ld[kv];
+  const int64_t step = (int64_t)p.heads * DIM;
 
   for (int r = 0; r < runs; ++r) {
     const int t = s_first[r];
     const int pos = __ldg(p.positions + t), row = __ldg(p.token_table + t);
+    // length of the run: up to the next start, the block's end or the last token
+    const int off = pos > 0 ? pos % p.block : 0;
+    int n = min(p.block - off, p.tokens - t);
+    for (int i0 = 1; i0 < n; i0 += 32) {
+      const int i = i0 + (tid & 31), x = t - t0 + i;
+      const bool start = i < n && (x < window ? s_start[x] != 0 : starts_run(p, t + i));
+      const uint32_t m = __ballot_sync(0xffffffffu, start);
+      if (m) n = i0 + __ffs(m) - 1;
+    }
+
+    const uint16_t* src = p.x[kv] + t * ld + (int64_t)head * DIM + lane * 8;
+    const int held = min(n, p.hold);
+    for (int i = sub; i < held; i += kRows)
+      copy16((uint32_t)__cvta_generic_to_shared(rows + i * kLanes + lane), src + i * ld);
+    asm volatile("cp.async.commit_group;" ::: "memory");
     int err = 0;
     int64_t slot = -1;
     if (pos < 0) {
@@ -153,52 +200,33 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(Params p) {
       if (page < 0) err = KV8_STATUS_TABLE_ENTRY;
       else if (slot >= p.num_slots) err = KV8_STATUS_SLOT;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (err) {  // holds for the whole run: its tokens share the page
-      if (tid == 0 && p.status) atomicOr(p.status, err);
+      if (tid % 32 == 0 && p.status) atomicOr(p.status, err);
       continue;
     }
-    const int off = pos % p.block;
-    // length of the run
-    if (tid == 0) s_len = min(p.block - off, p.tokens - t);
-    __syncthreads();
-    for (int i = 1 + tid; i < min(p.block - off, p.tokens - t); i += kThreads)
-      if (starts_run(p, t + i)) atomicMin(&s_len, i);
-    __syncthreads();
-    const int n = s_len;
-
-    const int lane = tid % kLanes, sub = tid / kLanes;
-    const uint16_t* src = p.x[kv] + (int64_t)t * p.ld[kv] + (int64_t)head * DIM + lane * 8;
-    uint4 hold[kHold];
-    float a = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-      const int i = j * kRows + sub;
-      if (i < n) hold[j] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)i * p.ld[kv]));
-    }
-#pragma unroll
-    for (int j = 0; j < kHold; ++j)
-      if (j * kRows + sub < n) a = amax8<FP16>(hold[j], a);
-    for (int i = kHold * kRows + sub; i < n; i += kRows)
-      a = amax8<FP16>(__ldg(reinterpret_cast<const uint4*>(src + (int64_t)i * p.ld[kv])), a);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (tid % 32 == 0) s_max[tid / 32] = a;
-    __syncthreads();
-    a = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-
+    // each lane reads back what it copied itself
     float* scale_at = p.scale[kv] + (slot / p.block) * p.heads + head;
-    const float least = least_scale(a);
-    float s = least;
-    float before = 0.0f;
-    if (off) {
-      before = *scale_at;
-      s = fmaxf(before, least);
+    const float before = off ? *scale_at : 0.0f;
+    const int rest = held + (sub + kRows - held % kRows) % kRows;  // this lane's first beyond
+    auto row_at = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + i * ld)); };
+    uint32_t top = 0;
+#pragma unroll 8
+    for (int i = sub; i < held; i += kRows) top = max8(rows[i * kLanes + lane], top);
+    for (int i = rest; i < n; i += kRows) top = max8(row_at(i), top);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    if (top >= (FP16 ? 0x7C00u : 0x7F80u)) {  // not finite: once more without what is not
+      top = 0;
+      for (int i = sub; i < held; i += kRows) top = max8_finite<FP16>(rows[i * kLanes + lane], top);
+      for (int i = rest; i < n; i += kRows) top = max8_finite<FP16>(row_at(i), top);
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     }
+    const float a = widen<FP16>(top).x;
+
+    const float s = off ? fmaxf(before, least_scale(a)) : least_scale(a);
     const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0 && s >= 0x1p-120f;
     const float inv = __fdiv_rn(1.0f, s);
     uint8_t* dst = p.cache[kv] + (slot * p.heads + head) * DIM + lane * 8;
-    const int64_t step = (int64_t)p.heads * DIM;
-    __syncthreads();  // every thread has read the old scale
     if (off && s > before) {
       const float ratio = __fdiv_rn(before, s);
       for (int i = sub; i < off; i += kRows) {
@@ -207,18 +235,31 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(Params p) {
         *at = make_uint2(rescale4(c.x, ratio), rescale4(c.y, ratio));
       }
     }
-    if (tid == 0) *scale_at = s;
-#pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-      const int i = j * kRows + sub;
-      if (i < n)
-        *reinterpret_cast<uint2*>(dst + (int64_t)i * step) = codes8<FP16>(hold[j], s, inv, pow2);
+    __syncwarp();  // every lane has read the old scale
+    if (tid % 32 == 0) *scale_at = s;
+    if (pow2) {
+#pragma unroll 8
+      for (int i = sub; i < held; i += kRows)
+        *reinterpret_cast<uint2*>(dst + i * step) = codes8<FP16>(rows[i * kLanes + lane], inv);
+    } else {
+      for (int i = sub; i < held; i += kRows)
+        *reinterpret_cast<uint2*>(dst + i * step) = codes8_div<FP16>(rows[i * kLanes + lane], s);
     }
-    for (int i = kHold * kRows + sub; i < n; i += kRows)
-      *reinterpret_cast<uint2*>(dst + (int64_t)i * step) = codes8<FP16>(
-          __ldg(reinterpret_cast<const uint4*>(src + (int64_t)i * p.ld[kv])), s, inv, pow2);
-    // s_len, s_max are written again only after the barriers of the next run
+    for (int i = rest; i < n; i += kRows)
+      *reinterpret_cast<uint2*>(dst + i * step) =
+          pow2 ? codes8<FP16>(row_at(i), inv) : codes8_div<FP16>(row_at(i), s);
   }
+}
+
+template <int DIM, bool FP16>
+int launch(const Params& p, dim3 grid, cudaStream_t s) {
+  const size_t bytes = (size_t)kWarps * p.hold * DIM * 2;
+  const auto kernel = kv8_store_kernel<DIM, FP16>;
+  if (bytes > 40960 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kWarps * 8192 * 2) != cudaSuccess)
+    return KV8_ERR_CUDA;
+  kernel<<<grid, kThreads, bytes, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
 }
 
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
@@ -232,7 +273,7 @@ extern "C" int kv8_store(const uint16_t* k, int64_t k_ld, const uint16_t* v, int
                          uint8_t* v_cache, float* k_scale, float* v_scale, int64_t num_slots,
                          int32_t* status, kv8_stream_t stream) {
   if ((dtype != KV8_BF16 && dtype != KV8_FP16) || tokens < 0 || kv_heads < 1 ||
-      kv_heads > 65535 || (dim != 64 && dim != 128) || n_tables < 1 || table_ld < 1 ||
+      kv_heads > 32767 || (dim != 64 && dim != 128) || n_tables < 1 || table_ld < 1 ||
       page_size < 1 || block_tokens < 16 || block_tokens % 16 || page_size % block_tokens ||
       num_slots < 0 || num_slots >= (int64_t(1) << 31) || num_slots % page_size ||
       k_ld < (int64_t)kv_heads * dim || (k_ld & 7) || v_ld < (int64_t)kv_heads * dim ||
@@ -247,21 +288,20 @@ extern "C" int kv8_store(const uint16_t* k, int64_t k_ld, const uint16_t* v, int
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(status, 4))
     return KV8_ERR_ALIGN;
   // A CTA per token finds the runs of a decode step at once; for a prefill most tokens start
-  // no run, and a CTA per block of tokens launches as many CTAs as there is work.
-  int chunk = 1;
-  if ((int64_t)tokens * kv_heads * 2 > 16384)
+  // no run, and a CTA per block of tokens launches as many CTAs as there is work. Runs of a
+  // decode step are a few tokens, those of a prefill a block: 16 KB a warp hold 64 rows of 128.
+  int chunk = 1, hold = 8;
+  if ((int64_t)tokens * kv_heads * 2 > 16384) {
     chunk = block_tokens < kMaxChunk ? block_tokens : kMaxChunk;
-  Params p{{k, v},   {k_ld, v_ld}, tokens,    kv_heads,     positions,        token_table,
-           block_table, n_tables,  table_ld,  page_size,    block_tokens,     {k_cache, v_cache},
-           {k_scale, v_scale},     num_slots, status,       chunk};
-  const dim3 grid((unsigned)((tokens + (int64_t)chunk - 1) / chunk), (unsigned)kv_heads, 2);
-  cudaStream_t s = (cudaStream_t)stream;
-  if (dim == 128) {
-    if (dtype == KV8_FP16) kv8_store_kernel<128, true><<<grid, kThreads, 0, s>>>(p);
-    else kv8_store_kernel<128, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (dtype == KV8_FP16) kv8_store_kernel<64, true><<<grid, kThreads, 0, s>>>(p);
-    else kv8_store_kernel<64, false><<<grid, kThreads, 0, s>>>(p);
+    hold = block_tokens < 8192 / dim ? block_tokens : 8192 / dim;
   }
-  return cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
+  const Params p{{k, v},   {k_ld, v_ld}, tokens,    kv_heads,     positions,        token_table,
+                 block_table, n_tables,  table_ld,  page_size,    block_tokens,
+                 {k_cache, v_cache},     {k_scale, v_scale},      num_slots, status, chunk, hold};
+  const dim3 grid((unsigned)((tokens + (int64_t)chunk - 1) / chunk),
+                  (unsigned)((2 * kv_heads + kWarps - 1) / kWarps));
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dim == 128)
+    return dtype == KV8_FP16 ? launch<128, true>(p, grid, s) : launch<128, false>(p, grid, s);
+  return dtype == KV8_FP16 ? launch<64, true>(p, grid, s) : launch<64, false>(p, grid, s);
 }

@@ -127,6 +127,29 @@ def test_rows_that_sum_to_more_than_eight():
     assert check(p, None, np.zeros((1, 0), np.int32), np.array([[0.5]], np.float32))[2] == DV.PROB
 
 
+def test_rows_that_would_wrap_the_sums():
+    p = np.full((2, 1, 4000), 1.0, np.float32)
+    p[1] = 1.0 / 4096
+    o, k, s = check(p, None, np.zeros((2, 0), np.int32), np.array([[0.5], [0.5]], np.float32))
+    assert s == DV.PROB and o[0, 0] == -1 and o[1, 0] == 2000
+
+
+@pytest.mark.parametrize("vocab", [255, 256, 257, 4095, 16384, 32768, 32769, 65537, 1100000])
+def test_slices_and_steps(vocab):
+    """One token's weight at a step's, a slice's and the row's ends."""
+    at = sorted({0, vocab - 1, vocab // 2, *[x for s in (256, 2048, 16384, 131072)
+                                             for x in (s - 1, s, s + 1) if x < vocab]})
+    p = np.zeros((len(at), 1, vocab), np.float32)
+    for j, x in enumerate(at):
+        p[j, 0, x] = 0.75
+        p[j, 0, 0] += 0.25
+    u = np.tile(np.array([[0.25], [0.2499]], np.float32), (len(at), 1))[:len(at)]
+    t = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    out, kept = verify_drafts(t(p), None, t(np.zeros((len(at), 0), np.int32)), t(u))
+    want = [0 if u[j, 0] < 0.25 or x == 0 else x for j, x in enumerate(at)]
+    assert out[:, 0].tolist() == want and kept.tolist() == [0] * len(at)
+
+
 def test_every_run_and_a_graph_agree():
     p, q, tok, u = make(9, 4, 6, 20000)
     t = [torch.from_numpy(x).cuda() for x in (p, q, tok, u)]
