@@ -9,7 +9,7 @@
  *     if a = n (p_a where max(p_a - q_a, 0) is 0 everywhere): the least v with
  *     w(0) + .. + w(v) > floor(r * (w(0) + .. + w(V - 1))).
  * Without draft probabilities the draft is a point mass: q_i is 1 at d_i, 0 elsewhere.
- * For the draw, probabilities are whole multiples of 2^-60 (rounded towards zero),
+ * For the draw, probabilities are whole multiples of 2^-60 (rounded to nearest even),
  * subtracted and summed as 64-bit integers, so the result does not depend on the order
  * of the sums: it is the same on every run and for every split of the vocabulary.
  */

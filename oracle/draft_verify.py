@@ -40,7 +40,7 @@ class _Row:
         return u
 
     def units(self, row):
-        return [int(Fraction(self.prob(x)) * ONE) for x in row]
+        return [round(Fraction(self.prob(x)) * ONE) for x in row]
 
 
 def verify(target, draft, tokens, uniforms, n_drafts=None, mutant=0):

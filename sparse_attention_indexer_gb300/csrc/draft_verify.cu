@@ -54,48 +54,76 @@ __device__ __forceinline__ float checked_uniform(float u, int* err) {
   return u;
 }
 
-// A probability in [0, 1] in units of 2^-60, rounded down: its 24 significant bits, shifted. In
-// integer operations, as the conversion to 64 bits is slow: 45 us against MEASURED for 64 requests.
-__device__ __forceinline__ uint64_t units(float x) {
-  const uint32_t b = __float_as_uint(x);
-  const uint32_t e = (b >> 23) & 0xFF, m = (b << 8) | 0x80000000u;
-  const uint32_t s = 130 - e;  // m * 2^32 >> s; 3 for 1.0
-  const uint32_t lo = s <= 32 ? __funnelshift_rc(0, m, s) : s < 64 ? m >> (s - 32) : 0;
-  const uint32_t hi = s < 32 ? m >> s : 0;
-  return ((uint64_t)hi << 32) | lo;  // a subnormal is below the last bit
+// A probability in [0, 1] as a whole number of 2^-60, in three signed digits of 20 bits: adding
+// 1.5 * 2^k rounds to the sum's last place (2^-20, 2^-40, 2^-60) and leaves the digit in its
+// bits, and the differences are exact. Ten operations, seven of them on the wide fp32 pipe; a
+// conversion to a 64-bit integer, or shifts, held the sums to 1.5 TB/s.
+struct Digits {
+  int a, b, c;
+};
+
+__device__ __forceinline__ Digits digits(float x) {
+  constexpr float k1 = 0x1.8p3f, k2 = 0x1.8p-17f, k3 = 0x1.8p-37f;
+  const float t1 = x + k1;
+  const float r1 = x - (t1 - k1);
+  const float t2 = r1 + k2;
+  const float t3 = (r1 - (t2 - k2)) + k3;
+  return {__float_as_int(t1) - __float_as_int(k1), __float_as_int(t2) - __float_as_int(k2),
+          __float_as_int(t3) - __float_as_int(k3)};
 }
 
-// max(p - q, 0) in those units; a non-negative q >= p gives 0.
-__device__ __forceinline__ uint64_t weight(float p, float q) {
-  const uint64_t a = units(p), b = units(q);
-  return a > b ? a - b : 0;
+__device__ __forceinline__ uint64_t value(const Digits& d) {
+  return ((uint64_t)(int64_t)d.a << 40) + ((uint64_t)(int64_t)d.b << 20) + (uint64_t)(int64_t)d.c;
 }
 
 enum Row { kBonus, kRefused, kRefusedPoint };
 
-// The weights of tokens v0 + 32 i + lane, i < kStep; 0 past `end`. Tokens past it read the
-// row's last one instead, so that no load waits for a condition.
+// The weights of tokens v0 + 32 i + lane, i < kStep, in digits; 0 past `end`. Loads past it
+// read the row's last token instead, so that none waits for a condition.
 __device__ __forceinline__ void step_weights(const float* p, const float* q, Row row, int point,
-                                             int v0, int end, uint64_t (&w)[kStep], int* err) {
-  const int lane = threadIdx.x & 31;
+                                             int v0, int end, Digits (&w)[kStep], int* err) {
+  const int v = v0 + (threadIdx.x & 31);
+  const bool whole = v0 + 32 * kStep <= end;
   float a[kStep], b[kStep];
+  bool bad = false;  // above 1, negative or NaN (or -0)
 #pragma unroll
-  for (int i = 0; i < kStep; ++i) a[i] = __ldg(p + min(v0 + i * 32 + lane, end - 1));
+  for (int i = 0; i < kStep; ++i) a[i] = __ldg(p + (whole ? v + i * 32 : min(v + i * 32, end - 1)));
   if (row == kRefused) {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) b[i] = __ldg(q + min(v0 + i * 32 + lane, end - 1));
+    for (int i = 0; i < kStep; ++i)
+      b[i] = __ldg(q + (whole ? v + i * 32 : min(v + i * 32, end - 1)));
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) w[i] = weight(checked_prob(a[i], err), checked_prob(b[i], err));
+    for (int i = 0; i < kStep; ++i) bad |= __float_as_uint(b[i]) > 0x3F800000u;
   } else {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
-      w[i] = units(checked_prob(a[i], err));
-      if (row == kRefusedPoint && v0 + i * 32 + lane == point) w[i] = 0;
-    }
+    for (int i = 0; i < kStep; ++i) b[i] = 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < kStep; ++i)
-    if (v0 + i * 32 + lane >= end) w[i] = 0;
+  for (int i = 0; i < kStep; ++i) bad |= __float_as_uint(a[i]) > 0x3F800000u;
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      a[i] = checked_prob(a[i], err);
+      b[i] = checked_prob(b[i], err);
+    }
+  }
+  if (!whole || (row == kRefusedPoint && point >= v0 && point < v0 + 32 * kStep)) {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i)
+      if (v + i * 32 >= end || (row == kRefusedPoint && v + i * 32 == point)) a[i] = 0.0f;
+  }
+  if (row == kRefused) {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      // max(p - q, 0): the rounding keeps the order, so p <= q gives 0
+      const bool more = a[i] > b[i];
+      const Digits x = digits(more ? a[i] : 0.0f), y = digits(more ? b[i] : 0.0f);
+      w[i] = {x.a - y.a, x.b - y.b, x.c - y.c};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) w[i] = digits(a[i]);
+  }
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -104,6 +132,7 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
+// More CTAs than 1024 threads to an SM would not run at once.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(Params p) {
   constexpr int kWarps = THREADS / 32;
@@ -178,10 +207,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(P
     uint64_t sum = 0, record = 0, upper = 0;
     int v0 = begin;
     for (int i = 0; v0 < end; ++i, v0 += kTokens) {
-      uint64_t w[kStep], x = 0;
+      Digits w[kStep], d = {0, 0, 0};
       step_weights(prow, qrow, row, point, v0, end, w, &err);
 #pragma unroll
-      for (int k = 0; k < kStep; ++k) x += w[k];
+      for (int k = 0; k < kStep; ++k) {
+        d.a += w[k].a;
+        d.b += w[k].b;
+        d.c += w[k].c;
+      }
+      uint64_t x = value(d);
       upper += x >> 32;
       x = warp_sum(x);
       sum += x;
@@ -231,12 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(P
     while (run + s_step[warp][i] <= at) run += s_step[warp][i++];  // ends: run + mine > at
     int ignored = 0;
     for (int v0 = begin + i * each * kTokens;; v0 += kTokens) {
-      uint64_t w[kStep];
+      Digits w[kStep];
       step_weights(prow, qrow, row, point, v0, end, w, &ignored);
       int token = -1;
 #pragma unroll
       for (int k = 0; k < kStep; ++k) {
-        uint64_t x = w[k];
+        uint64_t x = value(w[k]);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -294,8 +328,8 @@ extern "C" int draft_verify(const float* target, int64_t target_req, int64_t tar
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return VERIFY_ERR_CUDA;
   // CTAs per request: up to 8 while they all run at once (1024 threads to an SM) and a warp has
-  // a step to sum. Few requests take CTAs of 512 threads, more of them smaller ones, which
-  // spread evenly: 64 requests of 100K tokens 256 x 512 threads MEASURED, 512 x 256 MEASURED.
+  // a step to sum. Few requests take CTAs of 512 threads, so that one request has 4096; more of
+  // them take CTAs of 256, eight to a request still, which spread more evenly over the SMs.
   const int threads = (int64_t)reqs * 8 <= 2 * sms ? 512 : 256;
   int c = 8;
   while (c > 1 && ((int64_t)reqs * c * threads > (int64_t)1024 * sms ||
