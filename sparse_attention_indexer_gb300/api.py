@@ -132,6 +132,11 @@ class Kv8Cache:
         self.page_size, self.block_tokens = int(page_size), int(block_tokens)
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._workspaces = {}
+        self._heads, self._dim = k.shape[1], k.shape[2]
+        # the cache's part of every call, made once
+        self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                      k.shape[0])
+        self._lib = B.lib()
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, dim: int,
@@ -154,15 +159,21 @@ class Kv8Cache:
     def store(self, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
               token_table: torch.Tensor, block_table: torch.Tensor, stream=None) -> None:
         """Quantises k, v [tokens, kv_heads, dim] (bf16 or fp16) into the cache."""
+        tokens = k.shape[0]
         if k.shape != v.shape or k.dtype != v.dtype or k.shape[1:] != self.k.shape[1:]:
             raise ValueError("k and v are [tokens, kv_heads, dim] of one type")
         _rows(k, "k")
         _rows(v, "v")
-        _int32(positions, (k.shape[0],), "positions")
-        _int32(token_table, (k.shape[0],), "token_table")
+        _int32(positions, (tokens,), "positions")
+        _int32(token_table, (tokens,), "token_table")
         _table(block_table)
-        B.kv8_store(k, v, positions, token_table, block_table, self.page_size, self.block_tokens,
-                    self.k, self.v, self.k_scale, self.v_scale, self.status, stream)
+        code = self._lib.kv8_store(
+            k.data_ptr(), B._ld(k), v.data_ptr(), B._ld(v), B._KV8_TYPES[k.dtype], tokens,
+            self._heads, self._dim, positions.data_ptr(), token_table.data_ptr(),
+            block_table.data_ptr(), block_table.shape[0], block_table.shape[1], self.page_size,
+            self.block_tokens, *self._args, self.status.data_ptr(), B._stream(stream))
+        if code < 0:
+            raise B.Kv8Error(code, "kv8_store")
 
     def attention(self, q: torch.Tensor, lens: torch.Tensor, max_len: int,
                   block_table: torch.Tensor, sm_scale: float, group_rows: int = 1,
@@ -172,17 +183,23 @@ class Kv8Cache:
         """Row t of q [rows, q_heads, dim] attends to positions [0, lens[t]) of its
         group's block-table row. Returns (out, lse)."""
         _rows(q, "q")
-        _int32(lens, (q.shape[0],), "lens")
+        rows, heads, dim = q.shape
+        _int32(lens, (rows,), "lens")
         _table(block_table)
-        groups = -(-q.shape[0] // max(1, group_rows))
         if group_table is not None:
-            _int32(group_table, (groups,), "group_table")
-        with _on(stream):
-            out, lse = self._outputs(q, out, lse)
-        B.kv8_attention(q, sm_scale, lens, max_len, group_rows, group_table, block_table,
-                        self.page_size, self.block_tokens, self.k, self.v, self.k_scale,
-                        self.v_scale, out, lse, self._workspace(q, group_rows, stream),
-                        self.status, stream)
+            _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table")
+        handle = B._stream(stream)
+        out, lse = self._outputs(q, out, lse, stream)
+        ws, ws_bytes = self._workspace(heads, group_rows, handle, stream)
+        code = self._lib.kv8_attention(
+            q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim, sm_scale,
+            lens.data_ptr(), max_len, group_rows,
+            None if group_table is None else group_table.data_ptr(), block_table.data_ptr(),
+            block_table.shape[0], block_table.shape[1], self.page_size, self.block_tokens,
+            *self._args, out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes,
+            self.status.data_ptr(), handle)
+        if code < 0:
+            raise B.Kv8Error(code, "kv8_attention")
         return out, lse
 
     def attention_selected(self, q: torch.Tensor, slots: torch.Tensor, sm_scale: float,
@@ -192,42 +209,51 @@ class Kv8Cache:
         """Row t of q attends to the slots of slots[t] (int32 [rows, k], negative ones
         skipped): what PagedTopK.select returns. Returns (out, lse)."""
         _rows(q, "q")
-        if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != q.shape[0]
-                or not _last_contiguous(slots)):
-            raise ValueError("slots is int32 [rows, k]")
-        with _on(stream):
-            out, lse = self._outputs(q, out, lse)
-        B.kv8_attention_selected(q, sm_scale, slots, self.block_tokens, self.k, self.v,
-                                 self.k_scale, self.v_scale, out, lse,
-                                 self._workspace(q, 1, stream), self.status, stream)
-        return out, lse
-
-    def _outputs(self, q, out, lse):
-        if q.shape[2] != self.k.shape[2]:
-            raise ValueError("q and the cache differ in dim")
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out has q's shape and type")
-        else:
-            _rows(out, "out")
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        elif lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse is contiguous float32 [rows, q_heads]")
-        return out, lse
-
-    def _workspace(self, q, group_rows, stream):
+        rows, heads, dim = q.shape
+        if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != rows
+                or not slots.is_cuda or not _last_contiguous(slots)):
+            raise ValueError("slots is CUDA int32 [rows, k]")
         handle = B._stream(stream)
-        key = (handle, q.shape[1], group_rows)
+        out, lse = self._outputs(q, out, lse, stream)
+        ws, ws_bytes = self._workspace(heads, 1, handle, stream)
+        code = self._lib.kv8_attention_selected(
+            q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim, sm_scale,
+            slots.data_ptr(), slots.shape[1], B._ld(slots), self.block_tokens, *self._args,
+            out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes, self.status.data_ptr(),
+            handle)
+        if code < 0:
+            raise B.Kv8Error(code, "kv8_attention_selected")
+        return out, lse
+
+    def _outputs(self, q, out, lse, stream):
+        if q.shape[2] != self._dim:
+            raise ValueError("q and the cache differ in dim")
+        if out is None or lse is None:
+            with _on(stream):
+                made = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out,
+                        torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+                        if lse is None else lse)
+        else:
+            made = (out, lse)
+        if out is not None:
+            if out.shape != q.shape or out.dtype != q.dtype:
+                raise ValueError("out has q's shape and type")
+            _rows(out, "out")
+        if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
+                                or not lse.is_cuda or not lse.is_contiguous()):
+            raise ValueError("lse is contiguous CUDA float32 [rows, q_heads]")
+        return made
+
+    def _workspace(self, heads, group_rows, handle, stream):
+        """(pointer, bytes) of the workspace of this stream and these heads."""
+        key = (handle, heads, group_rows)
         ws = self._workspaces.get(key)
         if ws is None:
-            n = B.kv8_attention_workspace_bytes(q.shape[1], self.k.shape[1], q.shape[2],
-                                                group_rows)
+            n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)
             with _on(stream):
-                ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-            self._workspaces[key] = ws
-        return ws
+                ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+            self._workspaces[key] = ws = (ws.data_ptr(), n, ws)
+        return ws[:2]
 
 
 class KvPages:
@@ -242,8 +268,6 @@ class KvPages:
     def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
                  planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
         _table(block_table)
-        if not block_table.is_cuda:
-            raise ValueError("block_table is a CUDA tensor")
         _int32(refs, (refs.numel(),), "refs")
         self.block_table, self.refs, self.page_size = block_table, refs, int(page_size)
         self.num_pages = refs.shape[0]
@@ -256,6 +280,13 @@ class KvPages:
         self.new_ids = torch.empty(self.num_pages, dtype=torch.int32, device=dev)
         self.counts = torch.zeros(2, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        # the state's part of the calls, made once
+        self._table_args = (block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
+        self._pool_args = (refs.data_ptr(), self.num_pages)
+        self._plane_args = (self._planes, len(self.tensors))
+        self._ws_args = (self.workspace.data_ptr(), self.workspace.numel())
+        self._status = self.status.data_ptr()
+        self._lib = B.lib()
 
     def reserve(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
                 stream=None) -> None:
@@ -265,8 +296,10 @@ class KvPages:
             _int32(t, (n,), name)
         if n > self.max_rows:
             raise ValueError(f"more than max_rows = {self.max_rows} rows")
-        B.kvpages_reserve(rows, old_lens, new_lens, self.block_table, self.page_size, self.refs,
-                          self._planes, len(self.tensors), self.workspace, self.status, stream)
+        B._kvp(self._lib.kvpages_reserve(
+            rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
+            self.page_size, *self._pool_args, *self._plane_args, *self._ws_args, self._status,
+            B._stream(stream)), "kvpages_reserve")
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
              stream=None) -> None:
@@ -274,8 +307,9 @@ class KvPages:
         n = parents.shape[0]
         for t, name in ((parents, "parents"), (children, "children"), (lens, "lens")):
             _int32(t, (n,), name)
-        B.kvpages_fork(parents, children, lens, self.block_table, self.page_size, self.refs,
-                       self.status, stream)
+        B._kvp(self._lib.kvpages_fork(
+            parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, *self._table_args,
+            self.page_size, *self._pool_args, self._status, B._stream(stream)), "kvpages_fork")
 
     def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
              stream=None) -> None:
@@ -283,15 +317,19 @@ class KvPages:
         _int32(rows, (rows.shape[0],), "rows")
         if keep_lens is not None:
             _int32(keep_lens, (rows.shape[0],), "keep_lens")
-        B.kvpages_free(rows, keep_lens, self.block_table, self.page_size, self.refs, self.status,
-                       stream)
+        B._kvp(self._lib.kvpages_free(
+            rows.data_ptr(), None if keep_lens is None else keep_lens.data_ptr(), rows.shape[0],
+            *self._table_args, self.page_size, *self._pool_args, self._status,
+            B._stream(stream)), "kvpages_free")
 
     def compact(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Moves the live pages into the lowest ids. Returns (new_ids, counts): the new id
         of each page (-1 of a free one) and {live pages, pages moved}; both are this
         instance's buffers, overwritten by the next call."""
-        B.kvpages_compact(self.block_table, self.refs, self._planes, len(self.tensors),
-                          self.new_ids, self.counts, self.workspace, self.status, stream)
+        B._kvp(self._lib.kvpages_compact(
+            *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
+            self.counts.data_ptr(), *self._ws_args, self._status, B._stream(stream)),
+            "kvpages_compact")
         return self.new_ids, self.counts
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -299,8 +337,9 @@ class KvPages:
         n = src.shape[0]
         _int32(src, (n,), "src")
         _int32(dst, (n,), "dst")
-        B.kvpages_copy(src, dst, self.num_pages, self._planes, len(self.tensors), self.status,
-                       stream)
+        B._kvp(self._lib.kvpages_copy(
+            src.data_ptr(), dst.data_ptr(), n, self.num_pages, *self._plane_args, self._status,
+            B._stream(stream)), "kvpages_copy")
 
 
 def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor,
@@ -311,31 +350,47 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
     drafts + 1, vocab], draft float32 [reqs, drafts, vocab] or None (point masses), tokens
     int32 [reqs, drafts], uniforms float32 [reqs, drafts + 1]. Returns (out_tokens [reqs,
     drafts + 1], kept [reqs]): the kept drafts, one drawn token, then -1."""
-    _int32(tokens, tuple(tokens.shape), "tokens")
+    if tokens.dim() != 2:
+        raise ValueError("tokens is int32 [reqs, drafts]")
     reqs, drafts = tokens.shape
-    if (target.dtype != torch.float32 or target.dim() != 3
-            or tuple(target.shape[:2]) != (reqs, drafts + 1) or not _last_contiguous(target)):
-        raise ValueError("target is float32 [reqs, drafts + 1, vocab]")
-    if draft is not None and (draft.dtype != torch.float32
-                              or tuple(draft.shape) != (reqs, drafts, target.shape[2])
-                              or not _last_contiguous(draft)):
-        raise ValueError("draft is float32 [reqs, drafts, vocab]")
-    if (uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (reqs, drafts + 1)
-            or not uniforms.is_contiguous()):
-        raise ValueError("uniforms is contiguous float32 [reqs, drafts + 1]")
+    _int32(tokens, (reqs, drafts), "tokens")
+    if (target.dtype != torch.float32 or target.dim() != 3 or not target.is_cuda
+            or target.shape[0] != reqs or target.shape[1] != drafts + 1
+            or not _last_contiguous(target)):
+        raise ValueError("target is CUDA float32 [reqs, drafts + 1, vocab]")
+    vocab = target.shape[2]
+    if draft is not None and (draft.dtype != torch.float32 or draft.shape != (reqs, drafts, vocab)
+                              or not draft.is_cuda or not _last_contiguous(draft)):
+        raise ValueError("draft is CUDA float32 [reqs, drafts, vocab]")
+    if (uniforms.dtype != torch.float32 or uniforms.shape != (reqs, drafts + 1)
+            or not uniforms.is_cuda or not uniforms.is_contiguous()):
+        raise ValueError("uniforms is contiguous CUDA float32 [reqs, drafts + 1]")
     if n_drafts is not None:
         _int32(n_drafts, (reqs,), "n_drafts")
+    if status is not None:
+        _int32(status, (1,), "status")
     with _on(stream):
         out = torch.empty((reqs, drafts + 1), dtype=torch.int32, device=tokens.device)
-        kept = torch.empty(reqs, dtype=torch.int32, device=tokens.device)
-    B.draft_verify(target, draft, tokens, uniforms, out, kept, n_drafts, status, stream)
+        kept = torch.empty((reqs,), dtype=torch.int32, device=tokens.device)
+    code = B.lib().draft_verify(
+        target.data_ptr(), target.stride(0), target.stride(1) if drafts else vocab,
+        None if draft is None else draft.data_ptr(), 0 if draft is None else draft.stride(0),
+        vocab if draft is None or drafts <= 1 else draft.stride(1), tokens.data_ptr(),
+        None if n_drafts is None else n_drafts.data_ptr(), uniforms.data_ptr(), reqs, drafts,
+        vocab, out.data_ptr(), kept.data_ptr(), None if status is None else status.data_ptr(),
+        B._stream(stream))
+    if code < 0:
+        raise B.VerifyError(code)
     return out, kept
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """Memory for work on `stream` comes from that stream's pool."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not isinstance(stream, torch.cuda.Stream):
         if not int(stream):
             return torch.cuda.stream(torch.cuda.default_stream())
@@ -344,22 +399,22 @@ def _on(stream):
 
 
 def _int32(t: torch.Tensor, shape, name: str) -> None:
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} is contiguous int32 {list(shape)}")
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} is contiguous CUDA int32 {list(shape)}")
 
 
 def _rows(t: torch.Tensor, name: str) -> None:
     """[rows, heads, dim] of bf16 / fp16 whose rows may be strided."""
-    if t.dtype not in (torch.bfloat16, torch.float16) or t.dim() != 3:
-        raise ValueError(f"{name} is bf16 or fp16 [rows, heads, dim]")
+    if t.dtype not in B._KV8_TYPES or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} is CUDA bf16 or fp16 [rows, heads, dim]")
     if t.numel() and (not _last_contiguous(t) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
         raise ValueError(f"{name}: a row's heads are contiguous")
 
 
 def _table(t: torch.Tensor) -> None:
     # table_ld is a row's width as well as its stride
-    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous():
-        raise ValueError("block_table is contiguous int32 [n_tables, table_ld]")
+    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("block_table is contiguous CUDA int32 [n_tables, table_ld]")
 
 
 def _last_contiguous(t: torch.Tensor) -> bool:

@@ -9,6 +9,7 @@ is missing this module raises; there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -161,6 +162,8 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(s) -> Optional[int]:
     if s is None:
+        if torch.cuda.is_initialized():  # the current stream without a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
         return torch.cuda.current_stream().cuda_stream or None
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream or None
@@ -397,7 +400,7 @@ def _kv8(code: int, what: str) -> int:
 
 def _ld(t) -> int:
     """Stride of the first dimension; a lone row's may be anything, so its length."""
-    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else t.stride(0)
+    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])
 
 
 def kv8_store(k, v, positions, token_table, block_table, page_size: int, block_tokens: int,

@@ -37,6 +37,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -968,12 +969,23 @@ int check_common(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, 
   return KV8_OK;
 }
 
-// SMs of the current device, or < 0.
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
+constexpr int kMaxDevices = 64;
+
+// The current device, or < 0.
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices ? dev : -1;
+}
+
+// SMs of a device, or < 0; asked for once.
+int sm_count(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  if (dev < 0) return -1;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
   return sms;
 }
 
@@ -990,18 +1002,24 @@ int shift_of(int x) {
 }
 
 template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
-int launch(const Params& p, int sms, cudaStream_t s) {
+int launch(const Params& p, int dev, cudaStream_t s) {
   using L = Smem<DIM, NT, WM>;
   const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, NT, WM>;
   const auto join = kv8_join_kernel<DIM, FP16, L::kRows>;
-  // both with the largest share of shared memory: a change of it between them would cost time
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-          cudaSuccess)
-    return KV8_ERR_CUDA;
+  // once on a device; both with the largest share of shared memory: a change of it between
+  // them would cost time
+  static std::atomic<uint64_t> ready;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+            cudaSuccess)
+      return KV8_ERR_CUDA;
+    ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  const int sms = sm_count(dev);
   // a tile for each warp group of a CTA, where there is that little work
   const int64_t groups = ((int64_t)p.rows + p.group_rows - 1) / p.group_rows;
   const int64_t units = groups * p.kv_heads;
@@ -1030,17 +1048,17 @@ int launch(const Params& p, int sms, cudaStream_t s) {
 }
 
 template <int DIM, bool FP16, bool SELECTED>
-int launch_rows(const Params& p, int live, int sms, cudaStream_t s) {
+int launch_rows(const Params& p, int live, int dev, cudaStream_t s) {
   if constexpr (SELECTED) {  // at most 16 rows to a unit
-    return live <= 8 ? launch<DIM, FP16, true, 1, 1>(p, sms, s)
-                     : launch<DIM, FP16, true, 2, 1>(p, sms, s);
+    return live <= 8 ? launch<DIM, FP16, true, 1, 1>(p, dev, s)
+                     : launch<DIM, FP16, true, 2, 1>(p, dev, s);
   } else {
     switch (padded_rows(live)) {
-      case 8: return launch<DIM, FP16, false, 1, 1>(p, sms, s);
-      case 16: return launch<DIM, FP16, false, 2, 1>(p, sms, s);
-      case 32: return launch<DIM, FP16, false, 4, 1>(p, sms, s);
-      case 64: return launch<DIM, FP16, false, 4, 2>(p, sms, s);
-      default: return launch<DIM, FP16, false, 4, 4>(p, sms, s);
+      case 8: return launch<DIM, FP16, false, 1, 1>(p, dev, s);
+      case 16: return launch<DIM, FP16, false, 2, 1>(p, dev, s);
+      case 32: return launch<DIM, FP16, false, 4, 1>(p, dev, s);
+      case 64: return launch<DIM, FP16, false, 4, 2>(p, dev, s);
+      default: return launch<DIM, FP16, false, 4, 4>(p, dev, s);
     }
   }
 }
@@ -1077,17 +1095,17 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
       kv8_attention_workspace_bytes(p.q_heads, p.kv_heads, dim, SELECTED ? 1 : p.group_rows);
   if (need < 0) return (int)need;
   if (ws_bytes < need) return KV8_ERR_WORKSPACE;
-  const int sms = sm_count();
-  if (sms < 0) return KV8_ERR_CUDA;
+  const int dev = current_device();
+  if (sm_count(dev) < 0) return KV8_ERR_CUDA;
   p.shared = reinterpret_cast<Shared*>(workspace);
   p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
                                      kMaxCtas * sizeof(Shared));
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
   if (dim == 128)
-    return dtype == KV8_FP16 ? launch_rows<128, true, SELECTED>(p, live, sms, s)
-                             : launch_rows<128, false, SELECTED>(p, live, sms, s);
-  return dtype == KV8_FP16 ? launch_rows<64, true, SELECTED>(p, live, sms, s)
-                           : launch_rows<64, false, SELECTED>(p, live, sms, s);
+    return dtype == KV8_FP16 ? launch_rows<128, true, SELECTED>(p, live, dev, s)
+                             : launch_rows<128, false, SELECTED>(p, live, dev, s);
+  return dtype == KV8_FP16 ? launch_rows<64, true, SELECTED>(p, live, dev, s)
+                           : launch_rows<64, false, SELECTED>(p, live, dev, s);
 }
 
 }  // namespace
@@ -1095,7 +1113,7 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
 extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
                                                  int group_rows) {
   if (!heads_ok(q_heads, kv_heads, dim, group_rows)) return KV8_ERR_SHAPE;
-  const int sms = sm_count();
+  const int sms = sm_count(current_device());
   if (sms < 0) return KV8_ERR_CUDA;
   const int rows = padded_rows(group_rows * (q_heads / kv_heads));
   const int64_t ctas = sms * 3 < kMaxCtas ? sms * 3 : kMaxCtas;  // most of any variant
