@@ -49,6 +49,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 32;   // keys of a tile
+constexpr float kNone = -3e38f;  // maximum of a row that has no key yet: finite, so that no difference
+                                 // of two of them is NaN
+constexpr float kSlack = 4.0f;   // log2 by which a row may pass its maximum before that is raised
 constexpr int kMaxCtas = 2048;
 
 // A unit whose parts CTAs first .. last have; last < 0: none, or one CTA has it whole. Kept by
@@ -172,8 +175,9 @@ template <int DIM, int NT, int WM>
 struct Smem {
   static constexpr int kGroups = kWarps / WM;
   static constexpr int kRows = 8 * NT * WM;
-  static constexpr int kStages = NT <= 2 ? 2 : 3;  // tiles in flight per warp group
-  static constexpr int kCtas = NT <= 2 ? 3 : 2;    // CTAs per SM
+  // tiles in flight per warp group, CTAs per SM
+  static constexpr int kStages = WM == 1 ? 2 : WM == 2 ? 3 : 6;
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;
   static constexpr int kTile = kKeys * DIM;        // bytes of the K (or V) codes of a tile
   static constexpr int kRing = kGroups * kStages * 2 * kTile;
   static constexpr int kLd = DIM + 4;  // floats between the rows of the warps' sums
@@ -504,9 +508,12 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         for (int st = 0; st < kSteps / 2; ++st) qf[i][st] = lds128(q_at + (i * (kSteps / 2) + st) * 512);
     }
     float o[NT][kPieces][4];
-    // m: running maximum of x; o is relative to 2^(m + d), sum to 2^m
+    // m: a maximum of x, not more than kSlack below the running one; o is relative to
+    // 2^(m + d), sum to 2^m
     float m[NT][2], d[NT][2], sum[NT][2];
     uint32_t sv_top = 0, sv_low = 255;  // exponents of the value scales so far
+    float d_all = 0.0f;                 // d, while all rows have the same
+    bool d_own = false;                 // they have not
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -515,7 +522,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        m[i][b] = -INFINITY;
+        m[i][b] = kNone;
         d[i][b] = sum[i][b] = 0.0f;
       }
     }
@@ -579,6 +586,8 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       const uint32_t in = masks[stage];
       const float* sc = reinterpret_cast<const float*>(smem + L::kScale) +
                         (kg * kStages + stage) * 2 * kKeys;
+      const float ks0 = sc[0], vs0 = sc[kKeys];
+      bool same;  // one key scale and one value scale
       {
         // exponents of the scales of the values (zeros weigh nothing and do not count)
         const float v = sc[kKeys + lane];
@@ -586,92 +595,96 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         const uint32_t e = __float_as_uint(v) >> 23;
         sv_top = max(sv_top, __reduce_max_sync(0xffffffffu, some ? e : 0u));
         sv_low = min(sv_low, __reduce_min_sync(0xffffffffu, some ? e : 255u));
+        same = !SELECTED && __all_sync(0xffffffffu, sc[lane] == ks0 && v == vs0);
       }
       const bool near = sv_top <= sv_low + 8 || sv_low == 255;
       // some row of the unit ends inside this tile or before it
       const bool ragged = (int64_t)(tile + 1) * kKeys > least;
-      float vs[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float ks = sc[j * 16 + c * 8 + quad];
-          vs[j][c] = sc[kKeys + j * 16 + c * 8 + quad];
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) s[i][j][2 * c + b] *= mul[i][b] * ks;
-        }
       const bool masked = ragged || in != 0xffffffffu;
-      if (masked) {
+      // the plain tile: the scales come out of the sums, and x is not needed to find its maximum
+      const bool plain = same && !masked && near && vs0 > 0.0f && ks0 >= 0.0f && p.scale >= 0.0f;
+      // d: 2^8 below the largest scale while all of them lie within 2^8, so that the row's
+      // largest weight * scale is 2^d times a number in [1, 2^9) (2^kSlack more between two
+      // updates); 2^d and its reciprocal stay in range
+      const float d_near = sv_low == 255 ? 0.0f : (float)max((int)sv_top - 127 - 8, -120);
+      float vs[2][2];
+      float tm[NT][2];
+      if (plain) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int end = s_len[row0 + i * 8 + 2 * t + b];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int at = j * 16 + c * 8 + quad;
-                if (!((in >> at) & 1) || (int64_t)tile * kKeys + at >= end)
-                  s[i][j][2 * c + b] = -INFINITY;
-              }
-          }
-      }
-      uint32_t pb[NT][2][2];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float keep[2], w2[2][2][2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float tm = fmaxf(fmaxf(s[i][0][b], s[i][0][2 + b]),
-                           fmaxf(s[i][1][b], s[i][1][2 + b]));  // NaN is no maximum
-#pragma unroll
-          for (int x = 4; x <= 16; x <<= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
-          tm = fmaxf(tm, m[i][b]);
-          // a row that has no key yet keeps -inf; 0 stands in for it in the differences
-          const float um = tm == -INFINITY ? 0.0f : tm;
-          // d: 2^8 below the largest scale while all of them lie within 2^8, so that the row's
-          // largest weight * scale is 2^d times a number in [1, 2^9); else what makes it 1.
-          // 2^d and its reciprocal stay in range.
-          float dn = sv_low == 255 ? 0.0f : (float)max((int)sv_top - 127 - 8, -120);
-          if (!near) {
-            float tv = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                tv = fmaxf(tv, s[i][j][2 * c + b] + log2_fast(vs[j][c]));
-#pragma unroll
-            for (int x = 4; x <= 16; x <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
-            // what there is already is at most 2^9 above 2^(m + d)
-            dn = fmaxf(tv, m[i][b] + d[i][b]) - um;
-            dn = dn > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : 0.0f;
-          }
-          const float drop = exp2_fast(m[i][b] - um);
-          sum[i][b] *= drop;
-          keep[b] = dn == d[i][b] ? drop : exp2_fast(m[i][b] + d[i][b] - um - dn);
-          m[i][b] = tm;
-          d[i][b] = dn;
-          const float f = exp2_fast(-dn);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float e = exp2_fast(s[i][j][2 * c + b] - um);
-              sum[i][b] += e;
-              w2[j][c][b] = e * vs[j][c] * f;  // in this order: f may be large where e is 0
-              // a key outside the row weighs 0, whatever the scale of its block is
-              if (masked && s[i][j][2 * c + b] == -INFINITY) w2[j][c][b] = 0.0f;
-            }
-        }
+          for (int b = 0; b < 2; ++b)
+            tm[i][b] = fmaxf(fmaxf(s[i][0][b], s[i][0][2 + b]), fmaxf(s[i][1][b], s[i][1][2 + b])) *
+                       (mul[i][b] * ks0);
+      } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            pb[i][j][c] = transpose8(pack_half(w2[j][c][0], w2[j][c][1]));
-        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+          for (int c = 0; c < 2; ++c) {
+            const float ks = sc[j * 16 + c * 8 + quad];
+            vs[j][c] = sc[kKeys + j * 16 + c * 8 + quad];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) s[i][j][2 * c + b] *= mul[i][b] * ks;
+          }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int end = s_len[row0 + i * 8 + 2 * t + b];
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const int at = j * 16 + c * 8 + quad;
+                  if (!((in >> at) & 1) || (int64_t)tile * kKeys + at >= end)
+                    s[i][j][2 * c + b] = -INFINITY;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)  // NaN is no maximum
+            tm[i][b] = fmaxf(fmaxf(s[i][0][b], s[i][0][2 + b]), fmaxf(s[i][1][b], s[i][1][2 + b]));
+      }
+      bool update = !near || d_own || d_near != d_all;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) update |= tm[i][b] > m[i][b] + kSlack;
+      if (__any_sync(0xffffffffu, update)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          float keep[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float top = tm[i][b], dn = d_near;
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top = fmaxf(top, m[i][b]);
+            if (!near) {  // what makes the row's largest weight * scale 1
+              float tv = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  tv = fmaxf(tv, s[i][j][2 * c + b] + log2_fast(vs[j][c]));
+#pragma unroll
+              for (int x = 4; x <= 16; x <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
+              // what there is already lies around 2^(m + d)
+              if (m[i][b] > kNone) tv = fmaxf(tv, m[i][b] + d[i][b]);
+              dn = tv - top;
+              dn = tv > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : 0.0f;
+            }
+            const float drop = exp2_fast(m[i][b] - top);
+            sum[i][b] *= drop;
+            keep[b] = dn == d[i][b] ? drop : exp2_fast((m[i][b] - top) + (d[i][b] - dn));
+            m[i][b] = top;
+            d[i][b] = dn;
+          }
 #pragma unroll
           for (int j = 0; j < kPieces; ++j) {
             o[i][j][0] *= keep[0];
@@ -679,6 +692,55 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
             o[i][j][2] *= keep[0];
             o[i][j][3] *= keep[1];
           }
+        }
+        d_all = d_near;
+        d_own = !near;
+      }
+      uint32_t pb[NT][2][2];
+      if (plain) {
+        // w' = 2^(x - m + log2(vs 2^-d)) at once; the sum of the weights is that of the w' / (vs 2^-d)
+        const float f = vs0 * exp2_fast(-d_all), lf = log2_fast(f), back = 1.0f / f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float c0 = mul[i][0] * ks0, c1 = mul[i][1] * ks0;
+          const float z0 = lf - m[i][0], z1 = lf - m[i][1];
+          float add0 = 0.0f, add1 = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float w0 = exp2_fast(fmaf(s[i][j][2 * c], c0, z0));
+              const float w1 = exp2_fast(fmaf(s[i][j][2 * c + 1], c1, z1));
+              add0 += w0;
+              add1 += w1;
+              pb[i][j][c] = transpose8(pack_half(w0, w1));
+            }
+          sum[i][0] = fmaf(add0, back, sum[i][0]);
+          sum[i][1] = fmaf(add1, back, sum[i][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          float w2[2][2][2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float f = exp2_fast(-d[i][b]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float e = exp2_fast(s[i][j][2 * c + b] - m[i][b]);
+                sum[i][b] += e;
+                w2[j][c][b] = e * vs[j][c] * f;  // in this order: f may be large where e is 0
+                // a key outside the row weighs 0, whatever the scale of its block is
+                if (masked && s[i][j][2 * c + b] == -INFINITY) w2[j][c][b] = 0.0f;
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              pb[i][j][c] = transpose8(pack_half(w2[j][c][0], w2[j][c][1]));
         }
       }
 
@@ -1056,8 +1118,8 @@ int launch_rows(const Params& p, int live, int dev, cudaStream_t s) {
     switch (padded_rows(live)) {
       case 8: return launch<DIM, FP16, false, 1, 1>(p, dev, s);
       case 16: return launch<DIM, FP16, false, 2, 1>(p, dev, s);
-      case 32: return launch<DIM, FP16, false, 4, 1>(p, dev, s);
-      case 64: return launch<DIM, FP16, false, 4, 2>(p, dev, s);
+      case 32: return launch<DIM, FP16, false, 2, 2>(p, dev, s);
+      case 64: return launch<DIM, FP16, false, 2, 4>(p, dev, s);
       default: return launch<DIM, FP16, false, 4, 4>(p, dev, s);
     }
   }

@@ -16,15 +16,18 @@
 namespace {
 
 constexpr int kCopyThreads = 256;
-constexpr int kItemBytes = 16384;  // one CTA's unit of copy work
+constexpr int kItemBytes = 32768;  // one CTA's unit of copy work
+constexpr int kSmallBytes = 2048;  // planes up to this size a page share one unit, a warp each
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 
+// The planes above kSmallBytes first.
 struct Planes {
-  int n;
+  int n, large;
   char* base[KVPAGES_MAX_PLANES];
   int64_t bytes[KVPAGES_MAX_PLANES];
-  int32_t first[KVPAGES_MAX_PLANES + 1];  // items of a page before each plane
+  int32_t first[KVPAGES_MAX_PLANES + 1];  // items of a page before each large plane
+  int items;                              // of a page: the small planes are the last one
 };
 
 // Workspace: counts[16] | need[n] | offset[n] | pair_src[m] | pair_dst[m] | free[P] |
@@ -57,10 +60,30 @@ __device__ __forceinline__ void report(int32_t* status, int bit) {
 }
 
 // ------------------------------------------------------------------ copy
-// Items are handed out round-robin: item = pair * items_per_page + j, j running over the
-// planes' pieces of kItemBytes. *count (device) or n bounds the pairs.
+// Items are handed out round-robin: item = pair * p.items + j, j running over the planes' pieces
+// of kItemBytes.
+__device__ __forceinline__ bool by_16(const void* base, int64_t bytes) {
+  return ((reinterpret_cast<uintptr_t>(base) | (uintptr_t)bytes) & 15) == 0;
+}
+
 __device__ __forceinline__ void copy_item(const Planes& p, int64_t src, int64_t dst, int j) {
-  int lo = 0, hi = p.n;  // the plane whose items hold j
+  if (j == p.first[p.large]) {  // the small planes
+    const int lane = threadIdx.x & 31;
+    for (int i = p.large + (threadIdx.x >> 5); i < p.n; i += kCopyThreads / 32) {
+      const int n = (int)p.bytes[i];
+      const char* s = p.base[i] + src * n;
+      char* d = p.base[i] + dst * n;
+      if (by_16(p.base[i], n)) {
+        for (int o = lane * 16; o < n; o += 512)
+          *reinterpret_cast<uint4*>(d + o) = *reinterpret_cast<const uint4*>(s + o);
+      } else {
+        for (int o = lane * 4; o < n; o += 128)
+          *reinterpret_cast<uint32_t*>(d + o) = *reinterpret_cast<const uint32_t*>(s + o);
+      }
+    }
+    return;
+  }
+  int lo = 0, hi = p.large;  // the plane whose items hold j
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (p.first[mid] <= j) lo = mid;
@@ -71,18 +94,18 @@ __device__ __forceinline__ void copy_item(const Planes& p, int64_t src, int64_t 
   const int n = (int)(bytes - at < kItemBytes ? bytes - at : kItemBytes);
   const char* s = p.base[lo] + src * bytes + at;
   char* d = p.base[lo] + dst * bytes + at;
-  if (((reinterpret_cast<uintptr_t>(p.base[lo]) | (uintptr_t)bytes) & 15) == 0) {
+  if (by_16(p.base[lo], bytes)) {
     constexpr int kVec = kItemBytes / 16 / kCopyThreads;
     uint4 v[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int o = (i * kCopyThreads + threadIdx.x) * 16;
-      if (o < n) v[i] = *reinterpret_cast<const uint4*>(s + o);
+      if (o < n) v[i] = __ldcs(reinterpret_cast<const uint4*>(s + o));
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int o = (i * kCopyThreads + threadIdx.x) * 16;
-      if (o < n) *reinterpret_cast<uint4*>(d + o) = v[i];
+      if (o < n) __stcs(reinterpret_cast<uint4*>(d + o), v[i]);
     }
   } else {
     for (int o = threadIdx.x * 4; o < n; o += kCopyThreads * 4)
@@ -92,10 +115,10 @@ __device__ __forceinline__ void copy_item(const Planes& p, int64_t src, int64_t 
 
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pairs_kernel(const __grid_constant__ Planes p, const int32_t* src, const int32_t* dst, int n,
-                  const int32_t* count, int num_pages, int32_t* status) {
-  const int64_t per = p.first[p.n];
-  const int64_t pairs = count ? min(*count, n) : n;
-  for (int64_t item = blockIdx.x; item < pairs * per; item += gridDim.x) {
+                  int num_pages, int32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan, where there is one
+  const int64_t per = p.items;
+  for (int64_t item = blockIdx.x; item < n * per; item += gridDim.x) {
     const int64_t i = item / per;
     const int j = (int)(item - i * per);
     const int32_t a = src[i], b = dst[i];
@@ -197,24 +220,65 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
   return before + x - v;
 }
 
-constexpr int kPer = 16;  // counts a thread looks at per round of a scan
+// A round of a scan over the pages: warp w looks at 512 of them, its lanes at 4 consecutive
+// ones of each quarter k, so that loads and stores of 16 bytes to a lane are contiguous.
+constexpr int kQuarters = 4;
+constexpr int kRound = kPlanThreads * 4 * kQuarters;
 
-// The counts of pages [first, first + kPer), -1 past the end.
-__device__ __forceinline__ void load_counts(const int32_t* refs, int64_t first, int num_pages,
-                                            int32_t* r) {
-  if (first + kPer <= num_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+__device__ __forceinline__ int64_t first_of(int64_t round, int k) {
+  return round + (threadIdx.x >> 5) * (128 * kQuarters) + k * 128 + (threadIdx.x & 31) * 4;
+}
+
+// The counts of pages [first, first + 4), -1 past the end.
+__device__ __forceinline__ int4 load_counts(const int32_t* refs, int64_t first, int num_pages) {
+  if (first + 4 <= num_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0)
+    return *reinterpret_cast<const int4*>(refs + first);
+  int4 v = make_int4(-1, -1, -1, -1);
+  if (first < num_pages) v.x = refs[first];
+  if (first + 1 < num_pages) v.y = refs[first + 1];
+  if (first + 2 < num_pages) v.z = refs[first + 2];
+  if (first + 3 < num_pages) v.w = refs[first + 3];
+  return v;
+}
+
+// Of the flagged pages of a round (flags[k]: 4 bits), how many come before this lane's of each
+// quarter; *total gets their number. The quarters' counts are scanned together, a byte each
+// (at most 128 to a warp).
+__device__ __forceinline__ void ranks(const uint32_t (&flags)[kQuarters], int (&before)[kQuarters],
+                                      int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPer / 4; ++i) {
-      const int4 v = *reinterpret_cast<const int4*>(refs + first + 4 * i);
-      r[4 * i] = v.x;
-      r[4 * i + 1] = v.y;
-      r[4 * i + 2] = v.z;
-      r[4 * i + 3] = v.w;
-    }
-  } else {
+  for (int k = 0; k < kQuarters; ++k) mine |= (uint32_t)__popc(flags[k]) << (8 * k);
+  uint32_t x = mine;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r[i] = first + i < num_pages ? refs[first + i] : -1;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  const uint32_t all = __shfl_sync(0xffffffffu, x, 31);
+  x -= mine;
+  int sum = 0;
+#pragma unroll
+  for (int k = 0; k < kQuarters; ++k) {
+    before[k] = sum + (int)((x >> (8 * k)) & 0xFF);
+    sum += (int)((all >> (8 * k)) & 0xFF);
+  }
+  __syncthreads();
+  if (lane == 0) s_warp[warp] = sum;
+  __syncthreads();
+  // every warp sums the warps before it
+  const int w = s_warp[lane];
+  int upto = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  *total = __shfl_sync(0xffffffffu, upto, 31);
+  const int base = __shfl_sync(0xffffffffu, upto - w, warp);
+#pragma unroll
+  for (int k = 0; k < kQuarters; ++k) before[k] += base;
 }
 
 // Pages of [old, new) that row `row` needs, lane by lane in order. `page(c, rank)` is
@@ -244,6 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t* new_lens, int n,
                     int32_t* table, int n_tables, int64_t ld, int page_size, int32_t* refs,
                     int num_pages, Work w, int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int64_t s_warp64[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -283,18 +348,22 @@ reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t*
   }
   // 3: the lowest free ids, until there are enough
   int found = 0;
-  for (int64_t p0 = 0; p0 < num_pages && found < total; p0 += (int64_t)kPlanThreads * kPer) {
-    int32_t r[kPer];
-    const int64_t first = p0 + (int64_t)tid * kPer;
-    load_counts(refs, first, num_pages, r);
-    int mine = 0;
+  for (int64_t p0 = 0; p0 < num_pages && found < total; p0 += kRound) {
+    uint32_t flags[kQuarters];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += r[i] == 0;
-    int sum;
-    int at = found + block_scan(mine, s_warp, &sum);
+    for (int k = 0; k < kQuarters; ++k) {
+      const int4 r = load_counts(refs, first_of(p0, k), num_pages);
+      flags[k] = (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
+    }
+    int before[kQuarters], sum;
+    ranks(flags, before, s_warp, &sum);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (r[i] == 0) w.free[at++] = (int32_t)(first + i);
+    for (int k = 0; k < kQuarters; ++k) {
+      int at = found + before[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (flags[k] >> i & 1) w.free[at++] = (int32_t)(first_of(p0, k) + i);
+    }
     found += sum;
   }
   __syncthreads();
@@ -347,45 +416,65 @@ reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t*
 
 __global__ void __launch_bounds__(kPlanThreads)
 compact_plan_kernel(int32_t* refs, int num_pages, Work w, int32_t* new_ids, int32_t* counts) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int s_warp[kPlanThreads / 32];
   const int tid = threadIdx.x;
   int mine = 0;
-  for (int64_t first = (int64_t)tid * kPer; first < num_pages;
-       first += (int64_t)kPlanThreads * kPer) {
-    int32_t r[kPer];
-    load_counts(refs, first, num_pages, r);
+  for (int64_t p0 = 0; p0 < num_pages; p0 += kRound)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += r[i] > 0;
-  }
+    for (int k = 0; k < kQuarters; ++k) {
+      const int4 r = load_counts(refs, first_of(p0, k), num_pages);
+      mine += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+    }
   int live;
   block_scan(mine, s_warp, &live);
   int holes = 0, movers = 0;
-  for (int64_t p0 = 0; p0 < num_pages; p0 += (int64_t)kPlanThreads * kPer) {
-    int32_t r[kPer];
-    const int64_t first = p0 + (int64_t)tid * kPer;
-    load_counts(refs, first, num_pages, r);
-    int h = 0, m = 0;
+  for (int64_t p0 = 0; p0 < num_pages; p0 += kRound) {
+    uint32_t hole[kQuarters], mover[kQuarters];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const bool in = first + i < num_pages;
-      h += in && r[i] <= 0 && first + i < live;
-      m += r[i] > 0 && first + i >= live;
-    }
-    int sum_h, sum_m;
-    int at_h = holes + block_scan(h, s_warp, &sum_h);
-    int at_m = movers + block_scan(m, s_warp, &sum_m);
+    for (int k = 0; k < kQuarters; ++k) {
+      const int64_t first = first_of(p0, k);
+      const int4 v = load_counts(refs, first, num_pages);
+      const int32_t r[4] = {v.x, v.y, v.z, v.w};
+      int32_t id[4];
+      hole[k] = mover[k] = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t id = first + i;
-      if (id >= num_pages) break;
-      if (r[i] > 0 && id >= live) w.src[at_m++] = (int32_t)id;
-      else if (r[i] <= 0 && id < live) w.dst[at_h++] = (int32_t)id;
-      new_ids[id] = r[i] > 0 ? (int32_t)id : -1;
+      for (int i = 0; i < 4; ++i) {
+        const bool in = first + i < num_pages, used = r[i] > 0;
+        id[i] = used ? (int32_t)(first + i) : -1;
+        if (in && used && first + i >= live) mover[k] |= 1u << i;
+        if (in && !used && first + i < live) hole[k] |= 1u << i;
+      }
+      if (first + 4 <= num_pages && (reinterpret_cast<uintptr_t>(new_ids) & 15) == 0) {
+        *reinterpret_cast<int4*>(new_ids + first) = make_int4(id[0], id[1], id[2], id[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (first + i < num_pages) new_ids[first + i] = id[i];
+      }
     }
-    holes += sum_h;
-    movers += sum_m;
+    int before[kQuarters], sum;
+    ranks(hole, before, s_warp, &sum);
+#pragma unroll
+    for (int k = 0; k < kQuarters; ++k) {
+      int at = holes + before[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (hole[k] >> i & 1) w.dst[at++] = (int32_t)(first_of(p0, k) + i);
+    }
+    holes += sum;
+    ranks(mover, before, s_warp, &sum);
+#pragma unroll
+    for (int k = 0; k < kQuarters; ++k) {
+      int at = movers + before[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (mover[k] >> i & 1) w.src[at++] = (int32_t)(first_of(p0, k) + i);
+    }
+    movers += sum;
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = tid; i < movers; i += kPlanThreads) {  // as many holes as movers
     const int a = w.src[i], b = w.dst[i];
     new_ids[a] = b;
@@ -405,7 +494,8 @@ compact_plan_kernel(int32_t* refs, int num_pages, Work w, int32_t* new_ids, int3
 __global__ void __launch_bounds__(kCopyThreads)
 compact_move_kernel(const __grid_constant__ Planes p, Work w, int num_pages, int32_t* table,
                     int64_t entries, const int32_t* new_ids, int32_t* status) {
-  const int64_t per = p.first[p.n];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
+  const int64_t per = p.items;
   const int64_t items = (int64_t)w.counts[0] * per;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t i = item / per;
@@ -440,25 +530,53 @@ int copy_grid(int64_t items) {
 int make_planes(const kvpages_plane* planes, int n, Planes* p) {
   if (n < 0 || n > KVPAGES_MAX_PLANES) return KVPAGES_ERR_SHAPE;
   if (n > 0 && !planes) return KVPAGES_ERR_NULL;
-  p->n = n;
-  int64_t items = 0;
   for (int i = 0; i < n; ++i) {
     if (planes[i].page_bytes < 4 || (planes[i].page_bytes & 3)) return KVPAGES_ERR_SHAPE;
     if (!planes[i].base) return KVPAGES_ERR_NULL;
     if (!aligned(planes[i].base, 4)) return KVPAGES_ERR_ALIGN;
-    p->base[i] = reinterpret_cast<char*>(planes[i].base);
-    p->bytes[i] = planes[i].page_bytes;
-    p->first[i] = (int32_t)items;
-    items += (planes[i].page_bytes + kItemBytes - 1) / kItemBytes;
-    if (items > (int64_t(1) << 30)) return KVPAGES_ERR_SHAPE;
   }
-  p->first[n] = (int32_t)items;
+  p->n = n;
+  int64_t items = 0;
+  int at = 0;
+  for (int small = 0; small < 2; ++small) {
+    for (int i = 0; i < n; ++i) {
+      if ((planes[i].page_bytes <= kSmallBytes) != (small == 1)) continue;
+      p->base[at] = reinterpret_cast<char*>(planes[i].base);
+      p->bytes[at] = planes[i].page_bytes;
+      p->first[at] = (int32_t)items;
+      ++at;
+      if (!small) items += (planes[i].page_bytes + kItemBytes - 1) / kItemBytes;
+      if (items > (int64_t(1) << 30)) return KVPAGES_ERR_SHAPE;
+    }
+    if (!small) {
+      p->large = at;
+      p->first[at] = (int32_t)items;
+    }
+  }
+  p->first[p->large] = (int32_t)items;
+  p->items = (int)items + (p->large < n);
   return KVPAGES_OK;
 }
 
 bool table_ok(int n, int n_tables, int64_t ld, int page_size, int num_pages) {
   return n >= 0 && n_tables >= 1 && ld >= 1 && ld < (int64_t(1) << 31) && page_size >= 1 &&
          num_pages >= 0;
+}
+
+// A launch that may be set up while the plan before it still runs; the kernel waits for its end.
+template <typename... Args, typename... Given>
+int launch_after(void (*kernel)(Args...), int grid, cudaStream_t s, Given... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(args)...);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KVPAGES_OK : KVPAGES_ERR_CUDA;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? KVPAGES_OK : KVPAGES_ERR_CUDA; }
@@ -492,7 +610,7 @@ extern "C" int kvpages_reserve(const int32_t* rows, const int32_t* old_lens,
   if (ws_bytes < kvpages_workspace_bytes(n, num_pages)) return KVPAGES_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   const Work w = layout(workspace, n, num_pages);
-  const int64_t items = (int64_t)n * p.first[p.n];
+  const int64_t items = (int64_t)n * p.items;
   const int grid = copy_grid(items);
   if (grid < 0) return KVPAGES_ERR_CUDA;
   reserve_plan_kernel<<<1, kPlanThreads, 0, s>>>(rows, old_lens, new_lens, n, block_table,
@@ -500,9 +618,7 @@ extern "C" int kvpages_reserve(const int32_t* rows, const int32_t* old_lens,
                                                  w, status);
   const int code = launched();
   if (code || items == 0) return code;
-  copy_pairs_kernel<<<grid, kCopyThreads, 0, s>>>(p, w.src, w.dst, n, nullptr, num_pages,
-                                                  nullptr);
-  return launched();
+  return launch_after(copy_pairs_kernel, grid, s, p, w.src, w.dst, n, num_pages, nullptr);
 }
 
 extern "C" int kvpages_fork(const int32_t* parents, const int32_t* children, const int32_t* lens,
@@ -554,15 +670,14 @@ extern "C" int kvpages_compact(int32_t* block_table, int n_tables, int64_t table
   cudaStream_t s = (cudaStream_t)stream;
   const Work w = layout(workspace, 0, num_pages);
   const int64_t entries = (int64_t)n_tables * table_ld;
-  const int64_t items = (int64_t)(num_pages / 2 + 1) * p.first[p.n];
+  const int64_t items = (int64_t)(num_pages / 2 + 1) * p.items;
   const int grid = copy_grid(items > entries / kCopyThreads ? items : entries / kCopyThreads);
   if (grid < 0) return KVPAGES_ERR_CUDA;
   compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(refs, num_pages, w, new_ids, counts);
   const int code = launched();
   if (code) return code;
-  compact_move_kernel<<<grid, kCopyThreads, 0, s>>>(p, w, num_pages, block_table, entries,
-                                                    new_ids, status);
-  return launched();
+  return launch_after(compact_move_kernel, grid, s, p, w, num_pages, block_table, entries, new_ids,
+                      status);
 }
 
 extern "C" int kvpages_copy(const int32_t* src, const int32_t* dst, int n, int num_pages,
@@ -572,13 +687,13 @@ extern "C" int kvpages_copy(const int32_t* src, const int32_t* dst, int n, int n
   Planes p;
   const int err = make_planes(planes, n_planes, &p);
   if (err) return err;
-  const int64_t items = (int64_t)n * p.first[p.n];
+  const int64_t items = (int64_t)n * p.items;
   if (items == 0) return KVPAGES_OK;
   if (!src || !dst) return KVPAGES_ERR_NULL;
   if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(status, 4)) return KVPAGES_ERR_ALIGN;
   const int grid = copy_grid(items);
   if (grid < 0) return KVPAGES_ERR_CUDA;
-  copy_pairs_kernel<<<grid, kCopyThreads, 0, (cudaStream_t)stream>>>(p, src, dst, n, nullptr,
-                                                                     num_pages, status);
+  copy_pairs_kernel<<<grid, kCopyThreads, 0, (cudaStream_t)stream>>>(p, src, dst, n, num_pages,
+                                                                     status);
   return launched();
 }
