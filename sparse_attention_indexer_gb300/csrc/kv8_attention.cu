@@ -176,7 +176,7 @@ struct Smem {
   static constexpr int kGroups = kWarps / WM;
   static constexpr int kRows = 8 * NT * WM;
   // tiles in flight per warp group, CTAs per SM
-  static constexpr int kStages = WM == 1 ? 2 : WM == 2 ? 3 : 6;
+  static constexpr int kStages = NT <= 2 ? (WM == 1 ? 2 : WM == 2 ? 3 : 6) : WM == 4 ? 6 : 3;
   static constexpr int kCtas = NT <= 2 ? 3 : 2;
   static constexpr int kTile = kKeys * DIM;        // bytes of the K (or V) codes of a tile
   static constexpr int kRing = kGroups * kStages * 2 * kTile;
@@ -1118,8 +1118,8 @@ int launch_rows(const Params& p, int live, int dev, cudaStream_t s) {
     switch (padded_rows(live)) {
       case 8: return launch<DIM, FP16, false, 1, 1>(p, dev, s);
       case 16: return launch<DIM, FP16, false, 2, 1>(p, dev, s);
-      case 32: return launch<DIM, FP16, false, 2, 2>(p, dev, s);
-      case 64: return launch<DIM, FP16, false, 2, 4>(p, dev, s);
+      case 32: return launch<DIM, FP16, false, 4, 1>(p, dev, s);
+      case 64: return launch<DIM, FP16, false, 4, 2>(p, dev, s);
       default: return launch<DIM, FP16, false, 4, 4>(p, dev, s);
     }
   }
