@@ -266,6 +266,86 @@ def test_heads_and_groups(hq, hk, group):
     Dense(hq * 10 + group, lens, group, hq, hk, 128 if hq % 2 else 64, 64, 32, "bf16").check()
 
 
+# More than 32 query rows to a key head, 128 channels: (query heads, key heads, group)
+WIDE = [(16, 1, 3), (56, 8, 7), (16, 1, 4), (40, 5, 8), (16, 2, 5), (16, 1, 5), (15, 1, 7), (32, 2, 8)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hk,group", WIDE)
+def test_wide_groups(hq, hk, group, dtype):
+    lens = []
+    for n in (group + 70, group, 130 + group, 513):
+        lens += [n - group + 1 + i for i in range(group)]
+    Dense(hq * 10 + group, lens[:-1], group, hq, hk, 128, 64, 32, dtype).check()
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (48, 48), (128, 16), (256, 256)])
+def test_wide_lengths(page, block):
+    """Rows of a group of any lengths, none among them, around the tiles of 128 keys."""
+    for lens in ([0, 1, 127, 128, 129, 2, 0], [0] * 7, [255, 256, 257, 300, 31, 32, 33],
+                 [1, 0, 0, 0, 0, 0, 0]):
+        Dense(page + len(lens), lens, 7, 8, 1, 128, page, block, "bf16").check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_wide_split_over_the_grid(dtype):
+    Dense(50, [20000 + i for i in range(7)], 7, 8, 1, 128, 64, 64, dtype).check(rows={0, 3, 6})
+    Dense(51, [3000, 2999, 1, 0, 700, 650, 600, 601] * 3, 4, 16, 1, 128, 64, 16, dtype).check()
+
+
+def test_wide_many_groups():
+    rng = np.random.default_rng(52)
+    lens = rng.integers(0, 200, 4 * 650).tolist()
+    Dense(53, lens, 4, 20, 2, 128, 16, 16, "bf16").check(rows=set(range(0, 2600, 37)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_wide_scales_and_peaks(dtype):
+    Dense(54, [500, 64, 100, 900], 4, 16, 1, 128, 64, 16, dtype, wide=True).check()
+    Dense(55, [400, 300, 20, 1], 4, 16, 1, 128, 64, 64, dtype, q_gain=40.0).check()
+    Dense(56, [400, 300, 20, 1], 4, 16, 1, 128, 64, 64, dtype, q_gain=0.0).check()
+
+
+def test_wide_zero_scales_and_queries():
+    d = Dense(57, [200, 40, 300, 290], 4, 16, 1, 128, 64, 16, "bf16")
+    d.cache[2][:] = 0.0
+    d.cache[3][::3] = 0.0
+    d.check()
+    d.cache[3][:] = 0.0
+    d.check()
+    for gain in (1e-30, 1e30):
+        d = Dense(58, [90, 33, 200, 1], 4, 16, 1, 128, 16, 16, "bf16", q_gain=gain)
+        d.scale = 0.125 / gain
+        d.check()
+
+
+def test_wide_refused_and_streams():
+    d = Dense(59, [300] * 8, 4, 16, 1, 128, 16, 16, "bf16", poison=False)
+    d.lens[0], d.lens[1] = -1, 301
+    d.table[1, 2], d.table[1, 6] = -1, 10 ** 6
+    assert d.check(max_len=300)[2] == K8.LEN | K8.TABLE_ENTRY | K8.SLOT
+    d = Dense(60, [5000, 77, 0, 1300], 4, 16, 2, 128, 64, 64, "bf16")
+    h, a = d.handle(), d.args()
+    ref = h.attention(*a)
+    for _ in range(3):
+        got = h.attention(*a)
+        assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+    with torch.cuda.stream(s):
+        h.attention(*a, out=out, lse=lse)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        h.attention(*a, out=out, lse=lse)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ref[0], out) and torch.equal(ref[1], lse)
+
+
 def test_rows_of_a_group_differ_freely():
     Dense(3, [0, 100, 17, 64, 0, 1, 333], 7, 16, 2, 128, 64, 64, "fp16").check()
     Dense(4, [0] * 7, 7, 16, 2, 128, 64, 64, "bf16").check()
@@ -305,11 +385,12 @@ def test_zero_scales():
     d.check()
 
 
-@pytest.mark.parametrize("dim", [64, 128])
-def test_nan_seen_by_the_later_rows_alone(dim):
+@pytest.mark.parametrize("dim,hq", [(64, 8), (128, 8), (128, 32)])
+def test_nan_seen_by_the_later_rows_alone(dim, hq):
     """NaN codes and scales in the last draft's key and value: the rows before it are as
     without them, the rows that see them are NaN where the definition says so."""
-    d = Dense(24, [97, 98, 99, 100], 4, 8, 2, dim, 64, 16, "bf16", poison=False)
+    n = hq // 2  # query heads of a key head
+    d = Dense(24, [97, 98, 99, 100], 4, hq, 2, dim, 64, 16, "bf16", poison=False)
     slot = K8.row_slots(d.table, 0, 100, 100, 64, d.cache[0].shape[0])[0]
     d.cache[1][slot[99], 1, 5] = 0x7F       # a value: channel 5 of the last row, key head 1
     d.cache[1][slot[98], 0, 40] = 0xFF      # rows 2 and 3, key head 0
@@ -319,12 +400,12 @@ def test_nan_seen_by_the_later_rows_alone(dim):
     o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
     for r in (0, 1):
         close(o[r], l[r], d.ref(r)[0], "bf16", f"row {r}")
-    nan = np.zeros((4, 8, dim), bool)
-    nan[2, :4, 40] = True
-    nan[3, :4] = True
-    nan[3, 4:, 5] = True
+    nan = np.zeros((4, hq, dim), bool)
+    nan[2, :n, 40] = True
+    nan[3, :n] = True
+    nan[3, n:, 5] = True
     assert np.array_equal(np.isnan(o), nan)
-    assert np.isnan(l[3, :4]).all() and not np.isnan(l[:3]).any() and not np.isnan(l[3, 4:]).any()
+    assert np.isnan(l[3, :n]).all() and not np.isnan(l[:3]).any() and not np.isnan(l[3, n:]).any()
     d.cache[3][slot[96] // 16] = np.nan     # the scale of a block that starts at position 96
     h = d.handle()
     d.lens[:] = [96, 96, 97, 100]
