@@ -8,16 +8,16 @@
 // the bytes take 24. Here nothing is widened: a tile of 128 keys goes from HBM to shared memory
 // in the 128-byte swizzle and is an operand of both products.
 //   - S[key, row] = K[128 keys, 128] . Q[rows, 128]^T, keys on the 128 lanes of tensor
-//     memory. Q is e4m3 too, in pieces stacked along N: q = q0 + q1 / 16 (+ q2 / 256 for fp16),
+//     memory. Q is e4m3 too, in pieces stacked along N: q = q0 + q1 / 32 (+ q2 / 1024 for fp16),
 //     each piece the rounding to 4 significant bits of what the one before left. The row's
 //     largest magnitude lies in [2^7, 2^8), so two pieces hold a bf16, and three an fp16, to
-//     2^-21 of it.
+//     2^-22 of it.
 //   - O^T[channel, row] = V^T[128, keys] . W[keys, rows]: V in its own order is the transposed
-//     operand. The weights w' are split into three pieces the same way (12 significant bits, as an
-//     fp16 has 11), stacked along N with an accumulator each: O = O0 + O1 / 16 + O2 / 256.
+//     operand. The weights w' are rounded to fp16 and split into three pieces the same way,
+//     stacked along N with an accumulator each: O = O0 + O1 / 32 + O2 / 1024.
 //   - w' = 2^(x + log2 sv - B), the value scale folded in, B a reference per row raised (and O
 //     and the sums rescaled) only when a w' would pass 2^8; the largest w' of a row then
-//     lies in [2^6, 2^8], and what lies below 2^-18 of 1 is lost. The sum of weights is kept in
+//     lies in [2^4, 2^8], and what lies below 2^-20 of 1 is lost. The sum of weights is kept in
 //     fp32, unrounded: sum of w' / sv. A thread of the weights is a key, so its scales and
 //     its mask are its own, and no row needs a reduction until the end of a unit.
 //
@@ -39,14 +39,14 @@ constexpr int kRing = 4;       // tiles in shared memory
 constexpr int kDepth = 3;      // tiles on their way
 constexpr int kSoftThreads = 256;
 constexpr int kLoadThreads = 128;
-constexpr int kWideThreads = kSoftThreads + kLoadThreads + 32;
+constexpr int kWideThreads = 512;  // 16 warps, the last three idle: registers move by warpgroups
 constexpr int kTileBytes = kTileKeys * kDim;  // codes of K or V: 16 KB
 constexpr int kPieceBytes = kTileKeys * kRows;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 192;  // scores in columns [0, 192), sums in [192, 384)
 constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
-constexpr float kPass = 8.0f;  // log2 of the weight that raises the reference
-constexpr float kHead = 6.0f;  // log2 of a row's largest weight after that
+constexpr float kPass = 256.0f;  // a weight above this raises the reference
+constexpr float kHead = 4.0f;    // log2 of a row's largest weight after that
 
 // shared memory, base aligned to 1024 bytes
 constexpr int kQOff = kRing * 2 * kTileBytes;
@@ -201,14 +201,32 @@ __device__ __forceinline__ float2 from_e4m3(uint32_t c) {
   return __half22float2(__half2(h));
 }
 
-// a, b as codes of the pieces: x = p0 + p1 / 16 + p2 / 256.
+// a, b (at most 256 in magnitude) as codes of the pieces: x = p0 + p1 / 32 + p2 / 1024.
 __device__ __forceinline__ void pieces(float a, float b, uint32_t (&p)[3]) {
   p[0] = to_e4m3(a, b);
   const float2 f = from_e4m3(p[0]);
-  const float a1 = a - f.x, b1 = b - f.y;  // exact
-  p[1] = to_e4m3(a1 * 16.0f, b1 * 16.0f);
+  const float a1 = (a - f.x) * 32.0f, b1 = (b - f.y) * 32.0f;  // exact
+  p[1] = to_e4m3(a1, b1);
   const float2 g = from_e4m3(p[1]);
-  p[2] = to_e4m3(fmaf(g.x, -16.0f, a1 * 256.0f), fmaf(g.y, -16.0f, b1 * 256.0f));
+  p[2] = to_e4m3((a1 - g.x) * 32.0f, (b1 - g.y) * 32.0f);
+}
+
+// The same of two fp16 (non-negative, at most 256): the differences are exact in fp16 too, two at
+// an operation.
+__device__ __forceinline__ uint32_t half_to_e4m3(__half2 x) {
+  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE,
+                                              __NV_E4M3);
+}
+__device__ __forceinline__ __half2 half_from_e4m3(uint32_t c) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3));
+}
+__device__ __forceinline__ void pieces(__half2 x, uint32_t (&p)[3]) {
+  const __half2 up = __float2half2_rn(32.0f);
+  p[0] = half_to_e4m3(x);
+  const __half2 x1 = __hmul2(__hsub2(x, half_from_e4m3(p[0])), up);
+  p[1] = half_to_e4m3(x1);
+  const __half2 x2 = __hmul2(__hsub2(x1, half_from_e4m3(p[1])), up);
+  p[2] = half_to_e4m3(x2);
 }
 
 // The next segment of a CTA's range: tiles [tile0, tile1) of a unit of `tiles`.
@@ -298,7 +316,9 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
   const int64_t units = (int64_t)groups * subs;
   Shared mine = {0, 0, 0, -1};
 
+  // 512 threads of 128 registers: 256 of 184 and 256 of 72
   if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------------------------------------------------------- copies
     const int lw = warp - 8;
     int it = 0, done = 0;
@@ -362,9 +382,10 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
     copy_wait<0>();
     fence_async();
     for (; done < it; ++done) bar_arrive(b_full + 8 * (done % kRing));
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t kScores = idesc(kRows * kQPieces, false);
       constexpr uint32_t kValues = idesc(kRows * 3, true);
       int it = 0, seg = 0;
@@ -408,6 +429,7 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---------------------------------------------------------------- weights
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -498,24 +520,6 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
         bar_wait(b_full + 8 * stage, (it / kRing) & 1, expired);
         __syncwarp();
         tc_fence_after();
-        float x[32];
-        {
-          uint32_t a[32], b[32];
-          tmem_load(lanes + c0, a);
-          tmem_load(lanes + kRows + c0, b);
-          tmem_load_wait();
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            x[c] = fmaf(__uint_as_float(b[c]), 1.0f / 16, __uint_as_float(a[c]));
-          if (FP16) {
-            tmem_load(lanes + 2 * kRows + c0, a);
-            tmem_load_wait();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = fmaf(__uint_as_float(a[c]), 1.0f / 256, x[c]);
-          }
-        }
-        tc_fence_before();
-        bar_arrive(b_read);
         const uint32_t in = reinterpret_cast<const uint32_t*>(sm + kMaskOff)[stage * 4 + quarter];
         const float* sc = reinterpret_cast<const float*>(sm + kScaleOff) + stage * 2 * kTileKeys;
         const float ks = sc[key], sv = sc[kTileKeys + key];
@@ -524,84 +528,113 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
         const bool zero = sv == 0.0f;
         const float lv = zero ? -60.0f : log2_fast(sv);
         const float back = zero ? 0x1p60f : sv > 0.0f && sv < INFINITY ? 1.0f / sv : 1.0f;
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(s_mul + c0 + c);
-          x[c] = fmaf(x[c] * ks, m.x, lv);
-          x[c + 1] = fmaf(x[c + 1] * ks, m.y, lv);
-          x[c + 2] = fmaf(x[c + 2] * ks, m.z, lv);
-          x[c + 3] = fmaf(x[c + 3] * ks, m.w, lv);
-        }
         const bool ragged = (int64_t)(tile + 1) * kTileKeys > least;
-        if (ragged || in != 0xffffffffu) {
-          const int64_t pos = (int64_t)tile * kTileKeys + key;
+        // x, the log2 of the weights (with the value scale, without the reference)
+        auto scores = [&](float (&x)[32]) {
+          uint32_t a[32];
+          tmem_load(lanes + c0, a);
+          tmem_load(lanes + kRows + c0, reinterpret_cast<uint32_t(&)[32]>(x));
+          tmem_load_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], 1.0f / 32, __uint_as_float(a[c]));
+          if (FP16) {
+            tmem_load(lanes + 2 * kRows + c0, a);
+            tmem_load_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = fmaf(__uint_as_float(a[c]), 1.0f / 1024, x[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(s_mul + c0 + c);
+            x[c] = fmaf(x[c] * ks, m.x, lv);
+            x[c + 1] = fmaf(x[c + 1] * ks, m.y, lv);
+            x[c + 2] = fmaf(x[c + 2] * ks, m.z, lv);
+            x[c + 3] = fmaf(x[c + 3] * ks, m.w, lv);
+          }
+          if (ragged || in != 0xffffffffu) {
+            const int64_t pos = (int64_t)tile * kTileKeys + key;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!valid || pos >= s_len[c0 + c]) x[c] = -INFINITY;
+          }
+        };
+        bool freed = tile == sg.tile0;  // the product before has read its weights
+        float w[32];
+        // Once in most tiles. Where a weight would pass kPass, a second time with new references for
+        // the rows where one does (the scores are read again, which costs no registers meanwhile).
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          scores(w);
+          if (pass == 1) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int bits = __float_as_int(w[c]);
+              const int top = __reduce_max_sync(0xffffffffu, bits ^ ((bits >> 31) & 0x7fffffff));
+              if (lane == c)
+                s_max[quarter * kRows + c0 + c] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+            }
+            soft_sync();
+            if (tid < kRows) {
+              const float top = fmaxf(fmaxf(s_max[tid], s_max[kRows + tid]),
+                                      fmaxf(s_max[2 * kRows + tid], s_max[3 * kRows + tid]));
+              const float b = s_b[tid], to = exp2_fast(top - b) > kPass ? top - kHead : b;
+              s_keep[tid] = exp2_fast(b - to);
+              s_b[tid] = to;
+            }
+            soft_sync();
+            if (!freed) {
+              bar_wait(b_values, (it - 1) & 1, expired);
+              __syncwarp();
+              freed = true;
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < 3; ++k) {
+                const uint32_t at = lanes + kOCol + k * kRows + c0;
+                uint32_t v[32];
+                tmem_load(at, v);
+                tmem_load_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  v[c] = __float_as_uint(__uint_as_float(v[c]) * s_keep[c0 + c]);
+                tmem_store(at, v);
+              }
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sum[c] *= s_keep[c0 + c];
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(s_b + c0 + c);
+            w[c] = exp2_fast(w[c] - b.x);
+            w[c + 1] = exp2_fast(w[c + 1] - b.y);
+            w[c + 2] = exp2_fast(w[c + 2] - b.z);
+            w[c + 3] = exp2_fast(w[c + 3] - b.w);
+          }
+          if (pass == 1) break;
+          float most = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) most = fmaxf(most, w[c]);
+          if (!soft_any(most > kPass)) break;
+        }
+        tc_fence_before();
+        bar_arrive(b_read);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) sum[c] = fmaf(w[c], back, sum[c]);
+        if (__any_sync(0xffffffffu, zero)) {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (!valid || pos >= s_len[c0 + c]) x[c] = -INFINITY;
+            if (zero) w[c] = 0.0f;
         }
-        float past = -INFINITY;
+        // ---- the weights' pieces: 16 rows are 16 bytes of a piece
+        uint32_t code[3][8];
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(s_b + c0 + c);
-          past = fmaxf(past, fmaxf(fmaxf(x[c] - b.x, x[c + 1] - b.y),
-                                   fmaxf(x[c + 2] - b.z, x[c + 3] - b.w)));
-        }
-        bool freed = tile == sg.tile0;  // the product before has read its weights
-        if (soft_any(past > kPass)) {
-          // ---- a weight would pass 2^8: new references for the rows where one does
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int bits = __float_as_int(x[c]);
-            const int top = __reduce_max_sync(0xffffffffu, bits ^ ((bits >> 31) & 0x7fffffff));
-            if (lane == c) s_max[quarter * kRows + c0 + c] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-          }
-          soft_sync();
-          if (tid < kRows) {
-            const float top = fmaxf(fmaxf(s_max[tid], s_max[kRows + tid]),
-                                    fmaxf(s_max[2 * kRows + tid], s_max[3 * kRows + tid]));
-            const float b = s_b[tid], to = top - b > kPass ? top - kHead : b;
-            s_keep[tid] = exp2_fast(b - to);
-            s_b[tid] = to;
-          }
-          soft_sync();
-          if (!freed) {
-            bar_wait(b_values, (it - 1) & 1, expired);
-            __syncwarp();
-            freed = true;
-            tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < 3; ++k) {
-              const uint32_t at = lanes + kOCol + k * kRows + c0;
-              uint32_t v[32];
-              tmem_load(at, v);
-              tmem_load_wait();
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                v[c] = __float_as_uint(__uint_as_float(v[c]) * s_keep[c0 + c]);
-              tmem_store(at, v);
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          }
-#pragma unroll
-          for (int c = 0; c < 32; ++c) sum[c] *= s_keep[c0 + c];
-        }
-        // ---- weights, and their pieces: 16 rows are 16 bytes of a piece
-        uint32_t w[3][8];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(s_b + c0 + c);
-          float y[4] = {exp2_fast(x[c] - b.x), exp2_fast(x[c + 1] - b.y),
-                        exp2_fast(x[c + 2] - b.z), exp2_fast(x[c + 3] - b.w)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum[c + i] = fmaf(y[i], back, sum[c + i]);
-            if (zero) y[i] = 0.0f;
-          }
           uint32_t lo[3], hi[3];
-          pieces(y[0], y[1], lo);
-          pieces(y[2], y[3], hi);
+          pieces(__floats2half2_rn(w[c], w[c + 1]), lo);
+          pieces(__floats2half2_rn(w[c + 2], w[c + 3]), hi);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) w[k][c >> 2] = lo[k] | (hi[k] << 16);
+          for (int k = 0; k < 3; ++k) code[k][c >> 2] = __byte_perm(lo[k], hi[k], 0x5410);
         }
         if (!freed) {
           bar_wait(b_values, (it - 1) & 1, expired);
@@ -614,7 +647,7 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             *reinterpret_cast<uint4*>(at + k * kPieceBytes + (((half * 2 + i) ^ turn) << 4)) =
-                make_uint4(w[k][4 * i], w[k][4 * i + 1], w[k][4 * i + 2], w[k][4 * i + 3]);
+                make_uint4(code[k][4 * i], code[k][4 * i + 1], code[k][4 * i + 2], code[k][4 * i + 3]);
         // ---- a NaN code must not reach the rows that end before it (0 * NaN is NaN in a
         // product): where a row ends, the rows that see one are marked, and it becomes 0
         if (ragged && half == 0 && valid) {
@@ -658,11 +691,11 @@ kv8_wide_kernel(const __grid_constant__ Params p) {
         tmem_load_wait();
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          o[c] = fmaf(__uint_as_float(b[c]), 1.0f / 16, __uint_as_float(a[c]));
+          o[c] = fmaf(__uint_as_float(b[c]), 1.0f / 32, __uint_as_float(a[c]));
         tmem_load(lanes + kOCol + 2 * kRows + c0, a);
         tmem_load_wait();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = fmaf(__uint_as_float(a[c]), 1.0f / 256, o[c]);
+        for (int c = 0; c < 32; ++c) o[c] = fmaf(__uint_as_float(a[c]), 1.0f / 1024, o[c]);
       }
       tc_fence_before();
       bar_arrive(b_sums);
