@@ -74,9 +74,7 @@ enum {
   KV8_STATUS_SLOT = 8,         /* slot >= num_slots: position skipped / not stored */
   KV8_STATUS_TABLE_ROW = 16,   /* table row outside [0, n_tables): rows attend to nothing /
                                   token not stored */
-  KV8_STATUS_POSITION = 32,    /* kv8_store: a negative position: token not stored */
-  KV8_STATUS_TIMEOUT = 64      /* a bounded wait inside an attention kernel expired: the
-                                  results of this call are unreliable */
+  KV8_STATUS_POSITION = 32     /* kv8_store: a negative position: token not stored */
 };
 
 /* Quantises `tokens` tokens into the cache. One launch.

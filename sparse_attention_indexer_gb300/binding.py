@@ -382,7 +382,6 @@ KV8_STATUS_TABLE_ENTRY = 4
 KV8_STATUS_SLOT = 8
 KV8_STATUS_TABLE_ROW = 16
 KV8_STATUS_POSITION = 32
-KV8_STATUS_TIMEOUT = 64
 
 _KV8_TYPES = {torch.bfloat16: KV8_BF16, torch.float16: KV8_FP16}
 

@@ -18,9 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtopk_paged.so")
 SOURCES = ["select.cu", "short.cu", "medium.cu", "rowcluster.cu", "plan.cu", "abi.cu", "noalloc.cu",
            "prologue.cu", "resolver.cu", "logits.cu", "kv8_store.cu", "kv8_attention.cu",
-           "kv8_wide.cu",
            "kv_pages.cu", "draft_verify.cu"]
-HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh", "kv8_common.cuh"]
+HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -32,15 +32,143 @@
 //     far lie within 2^8 of each other, one d for all rows keeps the row's largest w' in
 //     [1, 2^9), and fp16 holds what is 2^-24 of it; else d is chosen per row so that the
 //     largest w' is about 1.
-#include "kv8_common.cuh"
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
 
-namespace kv8 {
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "kv8_attention.h"
+
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 32;   // keys of a tile
+constexpr float kNone = -3e38f;  // maximum of a row that has no key yet: finite, so that no difference
+                                 // of two of them is NaN
 constexpr float kSlack = 4.0f;   // log2 by which a row may pass its maximum before that is raised
+constexpr int kMaxCtas = 2048;
+
+// A unit whose parts CTAs first .. last have; last < 0: none, or one CTA has it whole. Kept by
+// unit where there are at most kMaxCtas units, else by the unit's first CTA.
+struct __align__(16) Shared {
+  int32_t g, h, first, last;
+};
+
+struct Params {
+  const uint16_t* q;
+  int64_t q_ld;
+  int q_heads, kv_heads;
+  float scale;  // sm_scale * log2(e)
+  int rows;
+  const int32_t* lens;
+  int max_len;
+  int group_rows;
+  const int32_t* group_table;
+  const int32_t* block_table;
+  int n_tables;
+  int64_t table_ld;
+  int page_size;
+  int page_shift;  // log2 where a power of two, else -1
+  const int32_t* slots;  // the selected form: slots[row * slots_ld + i], i < max_len
+  int64_t slots_ld;
+  int block;
+  int block_shift;
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  int64_t num_slots;
+  uint16_t* out;
+  int64_t out_ld;
+  float* lse;
+  int32_t* status;
+  Shared* shared;  // workspace: the shared unit that starts in each CTA
+  float* parts;    // workspace: two partial results per CTA
+};
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 / 4 bytes to shared memory, zeros where !in (the source is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ldmatrix_trans(uint32_t a) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Four e4m3 codes as fp16, exactly: lo the two lower, hi the two upper.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of fp16 (lane 4 r + c: row r, columns 2 c, 2 c + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ------------------------------------------------------------------ layout in shared memory
 template <int DIM, int NT, int WM>
@@ -71,6 +199,81 @@ __device__ __forceinline__ int piece_at(int key, int piece) {
   return (key >> 1) * 128 + ((((key & 1) * 4 + piece) ^ ((key >> 1) & 3)) << 4);
 }
 
+// ------------------------------------------------------------------ lengths
+// Keys that group g attends to at most: the largest length of its rows that pass the checks;
+// len_of(row) is 0 for one that does not. `err` collects what is wrong.
+__device__ __forceinline__ int row_len(const Params& p, int row, int table, int* err) {
+  const int len = __ldg(p.lens + row);
+  if (len < 0 || len > p.max_len) {
+    *err |= KV8_STATUS_LEN;
+    return 0;
+  }
+  if (table < 0 || table >= p.n_tables) {
+    *err |= KV8_STATUS_TABLE_ROW;
+    return 0;
+  }
+  if ((int64_t)len > p.table_ld * p.page_size) {
+    *err |= KV8_STATUS_TABLE_WIDTH;
+    return 0;
+  }
+  return len;
+}
+
+__device__ __forceinline__ int group_len(const Params& p, int g, int* err) {
+  const int table = p.group_table ? __ldg(p.group_table + g) : g;
+  int len = 0;
+  const int64_t r0 = (int64_t)g * p.group_rows;
+  for (int i = 0; i < p.group_rows && r0 + i < p.rows; ++i)
+    len = max(len, row_len(p, (int)(r0 + i), table, err));
+  return len;
+}
+
+// A unit has at least one tile, so that rows without keys are written too.
+__device__ __forceinline__ int tiles_of(int len) {
+  return max(1, (int)(((uint32_t)len + kKeys - 1) / kKeys));
+}
+
+// 0xFF in each byte that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
+  return __vcmpeq4(c & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// A part of a unit in the workspace: ROWS x DIM sums, then {m, m + d, sum} per row.
+template <int DIM, int ROWS>
+struct Part {
+  static constexpr int kStat = ROWS * DIM;
+  static constexpr int kFloats = ROWS * (DIM + 4);
+};
+
+// Channels [N * c, N * c + N) of row r of unit (g, h): v relative to 2^topv over l relative to
+// 2^top, and with c == 0 the row's lse.
+template <int DIM, bool FP16, int N>
+__device__ __forceinline__ void write_row(const Params& p, int g, int h, int r, int c,
+                                          const float* v, float top, float topv, float l) {
+  const int ratio = p.q_heads / p.kv_heads;
+  const int64_t row = (int64_t)g * p.group_rows + r / ratio;
+  if (row >= p.rows) return;
+  const int head = h * ratio + r % ratio;
+  const bool none = l == 0.0f;  // no key: one that counts adds 1 to l, a NaN makes it NaN
+  const float f = none ? 0.0f : exp2f(topv - top) / l;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float x = none ? 0.0f : v[2 * i] * f, y = none ? 0.0f : v[2 * i + 1] * f;
+    if (FP16) {
+      w[i] = pack_half(x, y);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  uint16_t* dst = p.out + row * p.out_ld + (int64_t)head * DIM + c * N;
+  if (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[N / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (c == 0 && p.lse)
+    p.lse[row * p.q_heads + head] = none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+}
+
 // ------------------------------------------------------------------ kernel
 template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
 __global__ void __launch_bounds__(kThreads, Smem<DIM, NT, WM>::kCtas)
@@ -81,6 +284,9 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   constexpr int kSteps = DIM / 16;    // mma steps of q . k
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");  // the join, which waits for this launch
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_first;
+  __shared__ int s_group;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kg = warp / WM, wm = warp % WM;
@@ -100,7 +306,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   const int64_t units = (int64_t)groups * p.kv_heads;
   const int64_t me = blockIdx.x;
   if (SELECTED) {
-    const int64_t tiles = tiles_of<kKeys>(len);
+    const int64_t tiles = tiles_of(len);
     all = tiles * groups * p.kv_heads;
     n = min(n, max(units, (all + kGroups - 1) / kGroups));
     w0 = me * all / n;
@@ -110,15 +316,52 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     h = (int)(u % p.kv_heads);
     first_tile = u * tiles;
   } else {
-    const Range r = locate<kKeys>(p, groups, p.kv_heads, kGroups, &err);
-    all = r.all;
-    n = r.n;
-    w0 = r.w0;
-    w1 = r.w1;
-    g = r.g;
-    h = r.s;
-    len = r.len;
-    first_tile = r.first;
+    const int per = (groups + kThreads - 1) / kThreads;
+    const int64_t g0 = min((int64_t)groups, (int64_t)tid * per);
+    const int64_t g1 = min((int64_t)groups, g0 + per);
+    int64_t mine = 0;
+    for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len(p, (int)i, &err));
+    if (me) err = 0;  // CTA 0 reports for all
+    int64_t before = mine, total = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) s_sum[warp] = before;
+    __syncthreads();
+    before -= mine;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t x = s_sum[i];
+      if (i < warp) before += x;
+      total += x;
+    }
+    all = total * p.kv_heads;
+    n = min(n, max(units, (all + kGroups - 1) / kGroups));
+    w0 = me * all / n;
+    w1 = me < n ? (me + 1) * all / n : w0;
+    if (w0 < w1 && w0 >= before * p.kv_heads && w0 < (before + mine) * p.kv_heads) {
+      int ignored = 0;
+      int64_t i = g0, at = before * p.kv_heads;
+      for (;; ++i) {
+        const int64_t here = (int64_t)tiles_of(group_len(p, (int)i, &ignored)) * p.kv_heads;
+        if (w0 < at + here) break;
+        at += here;
+      }
+      s_group = (int)i;
+      s_first = at;
+    }
+    __syncthreads();
+    if (w0 < w1) {
+      int ignored = 0;
+      g = s_group;
+      first_tile = s_first;
+      len = group_len(p, g, &ignored);
+      const int tiles = tiles_of(len);
+      h = (int)((w0 - first_tile) / tiles);
+      first_tile += (int64_t)h * tiles;
+    }
   }
 
   const uint32_t ring = smem_u32(smem) + kg * kStages * 2 * L::kTile;
@@ -131,7 +374,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   Shared mine = {0, 0, 0, -1};
   int64_t w = w0;
   while (w < w1) {
-    const int tiles = tiles_of<kKeys>(len);
+    const int tiles = tiles_of(len);
     const int tile0 = (int)(w - first_tile);
     const int tile1 = (int)min((int64_t)tiles, w1 - first_tile);
     const int table = SELECTED ? 0 : p.group_table ? __ldg(p.group_table + g) : g;
@@ -653,6 +896,111 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   if (err && p.status) atomicOr(p.status, err);
 }
 
+// Joins the parts of the shared units: CTA (i, y) the rows y, y + gridDim.y, .. of entry i. The
+// warps take a row's parts in turn, each lane 16th .. of its channels, and meet in shared memory in
+// the order of the warps.
+constexpr int kJoinWarps = 8;
+
+template <int DIM, bool FP16, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+kv8_join_kernel(const __grid_constant__ Params p) {
+  using Q = Part<DIM, ROWS>;
+  constexpr int kVec = DIM / 32;  // channels of a lane
+  __shared__ float s_v[kJoinWarps][DIM];
+  __shared__ float s_st[kJoinWarps][3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Shared u = p.shared[blockIdx.x];
+  if (u.last < 0) return;
+  const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  const int parts = u.last - u.first + 1;
+  // the first CTA's part is its second one, the others' are their first
+  auto part = [&](int c) {
+    return p.parts + (2 * (int64_t)(u.first + c) + (c == 0)) * Q::kFloats;
+  };
+  for (int r = blockIdx.y; r < live; r += gridDim.y) {
+    float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
+    for (int c0 = warp; c0 < parts; c0 += 4 * kJoinWarps) {
+      float4 st[4];
+      float y[4][kVec];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + k * kJoinWarps;
+        if (c < parts) {
+          const float* q = part(c);
+          st[k] = __ldcg(reinterpret_cast<const float4*>(q + Q::kStat + r * 4));
+          const float* src = q + r * DIM + lane * kVec;
+          if (kVec == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            y[k][0] = x.x;
+            y[k][1] = x.y;
+            y[k][kVec - 2] = x.z;
+            y[k][kVec - 1] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            y[k][0] = x.x;
+            y[k][1] = x.y;
+          }
+        } else {
+          st[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) y[k][i] = 0.0f;
+        }
+      }
+      float nt = top, nv = topv;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        nt = fmaxf(nt, st[k].x);
+        nv = fmaxf(nv, st[k].y);
+      }
+      const float ut = nt == -INFINITY ? 0.0f : nt, uv = nv == -INFINITY ? 0.0f : nv;
+      l *= exp2_fast(top - ut);
+      const float keep = exp2_fast(topv - uv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] *= keep;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l += st[k].z * exp2_fast(st[k].x - ut);
+        const float f = exp2_fast(st[k].y - uv);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] += y[k][i] * f;
+      }
+      top = nt;
+      topv = nv;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) s_v[warp][lane * kVec + i] = v[i];
+    if (lane == 0) {
+      s_st[warp][0] = top;
+      s_st[warp][1] = topv;
+      s_st[warp][2] = l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) {
+        top = fmaxf(top, s_st[w][0]);
+        topv = fmaxf(topv, s_st[w][1]);
+      }
+      const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
+      l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        l += s_st[w][2] * exp2_fast(s_st[w][0] - ut);
+        const float f = exp2_fast(s_st[w][1] - uv);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] += s_v[w][lane * kVec + i] * f;
+      }
+      write_row<DIM, FP16, kVec>(p, u.g, u.h, r, lane, v, top, topv, l);
+    }
+    __syncthreads();
+  }
+}
+
 bool aligned(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) % a) == 0; }
 
 bool heads_ok(int q_heads, int kv_heads, int dim, int group_rows) {
@@ -681,6 +1029,26 @@ int check_common(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, 
       !aligned(lse, 4) || !aligned(status, 4))
     return KV8_ERR_ALIGN;
   return KV8_OK;
+}
+
+constexpr int kMaxDevices = 64;
+
+// The current device, or < 0.
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices ? dev : -1;
+}
+
+// SMs of a device, or < 0; asked for once.
+int sm_count(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  if (dev < 0) return -1;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
 }
 
 // Rows that the variant for a unit of `live` rows pads to.
@@ -725,7 +1093,20 @@ int launch(const Params& p, int dev, cudaStream_t s) {
   kernel<<<(unsigned)grid, kThreads, L::kTotal, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return KV8_ERR_CUDA;
   // the join is launched while the first kernel runs and waits for its end
-  return launch_join<DIM, FP16, L::kRows>(p, units, grid, s);
+  const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  const int entries = units > kMaxCtas ? grid : (int)units;
+  const int rows = 4096 / entries < 1 ? 1 : 4096 / entries;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)entries, (unsigned)(live < rows ? live : rows));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
 }
 
 template <int DIM, bool FP16, bool SELECTED>
@@ -778,12 +1159,10 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
   if (ws_bytes < need) return KV8_ERR_WORKSPACE;
   const int dev = current_device();
   if (sm_count(dev) < 0) return KV8_ERR_CUDA;
-  p.halves = 1;
   p.shared = reinterpret_cast<Shared*>(workspace);
   p.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
                                      kMaxCtas * sizeof(Shared));
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
-  if (!SELECTED && dim == 128 && live > 32) return launch_wide(p, dtype == KV8_FP16, dev, s);
   if (dim == 128)
     return dtype == KV8_FP16 ? launch_rows<128, true, SELECTED>(p, live, dev, s)
                              : launch_rows<128, false, SELECTED>(p, live, dev, s);
@@ -792,9 +1171,6 @@ int run(Params& p, int dim, int dtype, void* workspace, int64_t ws_bytes, cudaSt
 }
 
 }  // namespace
-}  // namespace kv8
-
-using namespace kv8;
 
 extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
                                                  int group_rows) {
