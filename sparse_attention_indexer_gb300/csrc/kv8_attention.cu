@@ -896,16 +896,71 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   if (err && p.status) atomicOr(p.status, err);
 }
 
-// Joins the parts of the shared units: CTA (i, y) the rows y, y + gridDim.y, .. of entry i. The
-// warps take a row's parts in turn, each lane 16th .. of its channels, and meet in shared memory in
-// the order of the warps.
+// Joins the parts of the shared units: CTA (i, y) a share of the rows of entry i. A unit of few
+// parts gives a row to a warp, which sums all of them; of many, the warps take a row's
+// parts in turn and meet in shared memory, in the order of the warps.
 constexpr int kJoinWarps = 8;
+
+// Adds parts c0, c0 + step, .. (< parts) of row r to (top, topv, l, v); `part` gives their address.
+template <int DIM, int ROWS, typename F>
+__device__ __forceinline__ void add_parts(F&& part, int c0, int step, int parts, int r, float& top,
+                                          float& topv, float& l, float (&v)[DIM / 32]) {
+  constexpr int kVec = DIM / 32;  // channels of a lane
+  const int lane = threadIdx.x & 31;
+  for (; c0 < parts; c0 += 4 * step) {
+    float4 st[4];
+    float y[4][kVec];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k * step;
+      if (c < parts) {
+        const float* q = part(c);
+        st[k] = __ldcg(reinterpret_cast<const float4*>(q + Part<DIM, ROWS>::kStat + r * 4));
+        const float* src = q + r * DIM + lane * kVec;
+        if (kVec == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          y[k][0] = x.x;
+          y[k][1] = x.y;
+          y[k][kVec - 2] = x.z;
+          y[k][kVec - 1] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          y[k][0] = x.x;
+          y[k][1] = x.y;
+        }
+      } else {
+        st[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[k][i] = 0.0f;
+      }
+    }
+    float nt = top, nv = topv;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      nt = fmaxf(nt, st[k].x);
+      nv = fmaxf(nv, st[k].y);
+    }
+    l *= exp2_fast(top - nt);  // the first part makes both finite
+    const float keep = exp2_fast(topv - nv);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l += st[k].z * exp2_fast(st[k].x - nt);
+      const float f = exp2_fast(st[k].y - nv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] += y[k][i] * f;
+    }
+    top = nt;
+    topv = nv;
+  }
+}
 
 template <int DIM, bool FP16, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 kv8_join_kernel(const __grid_constant__ Params p) {
   using Q = Part<DIM, ROWS>;
-  constexpr int kVec = DIM / 32;  // channels of a lane
+  constexpr int kVec = DIM / 32;
   __shared__ float s_v[kJoinWarps][DIM];
   __shared__ float s_st[kJoinWarps][3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -913,63 +968,24 @@ kv8_join_kernel(const __grid_constant__ Params p) {
   const Shared u = p.shared[blockIdx.x];
   if (u.last < 0) return;
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
+  const int share = (live + gridDim.y - 1) / gridDim.y;
+  const int r0 = blockIdx.y * share, r1 = min(live, r0 + share);
   const int parts = u.last - u.first + 1;
   // the first CTA's part is its second one, the others' are their first
   auto part = [&](int c) {
     return p.parts + (2 * (int64_t)(u.first + c) + (c == 0)) * Q::kFloats;
   };
-  for (int r = blockIdx.y; r < live; r += gridDim.y) {
-    float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
-    for (int c0 = warp; c0 < parts; c0 += 4 * kJoinWarps) {
-      float4 st[4];
-      float y[4][kVec];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = c0 + k * kJoinWarps;
-        if (c < parts) {
-          const float* q = part(c);
-          st[k] = __ldcg(reinterpret_cast<const float4*>(q + Q::kStat + r * 4));
-          const float* src = q + r * DIM + lane * kVec;
-          if (kVec == 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-            y[k][0] = x.x;
-            y[k][1] = x.y;
-            y[k][kVec - 2] = x.z;
-            y[k][kVec - 1] = x.w;
-          } else {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-            y[k][0] = x.x;
-            y[k][1] = x.y;
-          }
-        } else {
-          st[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) y[k][i] = 0.0f;
-        }
-      }
-      float nt = top, nv = topv;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        nt = fmaxf(nt, st[k].x);
-        nv = fmaxf(nv, st[k].y);
-      }
-      const float ut = nt == -INFINITY ? 0.0f : nt, uv = nv == -INFINITY ? 0.0f : nv;
-      l *= exp2_fast(top - ut);
-      const float keep = exp2_fast(topv - uv);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] *= keep;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        l += st[k].z * exp2_fast(st[k].x - ut);
-        const float f = exp2_fast(st[k].y - uv);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] += y[k][i] * f;
-      }
-      top = nt;
-      topv = nv;
+  if (share > 1 && parts <= 2 * kJoinWarps) {
+    for (int r = r0 + warp; r < r1; r += kJoinWarps) {
+      float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec] = {};
+      add_parts<DIM, ROWS>(part, 0, 1, parts, r, top, topv, l, v);
+      write_row<DIM, FP16, kVec>(p, u.g, u.h, r, lane, v, top, topv, l);
     }
+    return;
+  }
+  for (int r = r0; r < r1; ++r) {
+    float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec] = {};
+    add_parts<DIM, ROWS>(part, warp, kJoinWarps, parts, r, top, topv, l, v);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) s_v[warp][lane * kVec + i] = v[i];
     if (lane == 0) {
@@ -978,20 +994,19 @@ kv8_join_kernel(const __grid_constant__ Params p) {
       s_st[warp][2] = l;
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0) {  // has a part, so its maxima are finite
 #pragma unroll
       for (int w = 1; w < kJoinWarps; ++w) {
         top = fmaxf(top, s_st[w][0]);
         topv = fmaxf(topv, s_st[w][1]);
       }
-      const float ut = top == -INFINITY ? 0.0f : top, uv = topv == -INFINITY ? 0.0f : topv;
       l = 0.0f;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) v[i] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) {
-        l += s_st[w][2] * exp2_fast(s_st[w][0] - ut);
-        const float f = exp2_fast(s_st[w][1] - uv);
+        l += s_st[w][2] * exp2_fast(s_st[w][0] - top);
+        const float f = exp2_fast(s_st[w][1] - topv);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] += s_v[w][lane * kVec + i] * f;
       }
@@ -1095,9 +1110,13 @@ int launch(const Params& p, int dev, cudaStream_t s) {
   // the join is launched while the first kernel runs and waits for its end
   const int live = p.group_rows * (p.q_heads / p.kv_heads);
   const int entries = units > kMaxCtas ? grid : (int)units;
-  const int rows = 4096 / entries < 1 ? 1 : 4096 / entries;
+  // a CTA per row where that launches few or a unit has many parts on average, else one for each
+  // 8 rows: 448 rows of 8 parts 20.9 against 22.5 us (7 x 2048 slots), 2048 rows of 1-2
+  // parts 79 against 75.6 us (64 x 2048 slots)
+  const bool each = (int64_t)entries * live <= 1024 || grid / entries > 2 * kJoinWarps;
+  const int rows = each ? live : (live + kJoinWarps - 1) / kJoinWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)entries, (unsigned)(live < rows ? live : rows));
+  cfg.gridDim = dim3((unsigned)entries, (unsigned)rows);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
