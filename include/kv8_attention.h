@@ -23,8 +23,8 @@
  *   lse(t, i) = log sum_p exp(x(p)),  out(t, i) = sum_p exp(x(p) - lse) * v(p, h).
  * kv8_attention takes p over positions [0, lens[t]) through a block table, for decode
  * steps and for verify steps of up to 8 query rows per request; kv8_attention_selected
- * takes p over a list of slots per query row (the out_slots of topk_select_paged, or
- * the out_rows of hisparse_resolve), skipping negative ones. A row that attends to
+ * takes p over a list of slots per query row (the out_slots of topk_select_paged),
+ * skipping negative ones. A row that attends to
  * nothing gives out 0 and lse -infinity. What lies at positions that a row does not
  * attend to, NaN codes and scales among it, never reaches its result. Scales must be
  * >= 0. Scores, softmax statistics and sums are fp32; the weights exp(..) are rounded

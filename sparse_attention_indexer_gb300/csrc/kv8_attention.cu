@@ -28,10 +28,12 @@
 //     are rows g and g + 8 of a product of 16 channels. The weights turn from keys x rows
 //     into rows x keys by movmatrix.
 //   - the value scale of a block is folded into its weights before these are rounded to
-//     fp16: w' = 2^(x - m) * sv * 2^-d, m the row's running maximum. While the scales met so
-//     far lie within 2^8 of each other, one d for all rows keeps the row's largest w' in
-//     [1, 2^9), and fp16 holds what is 2^-24 of it; else d is chosen per row so that the
-//     largest w' is about 1.
+//     fp16: w' = 2^(x - m) * sv * 2^-d, m the row's maximum, which is raised only when an x
+//     passes it by 4 (in most tiles none does, and no lane asks another). While the scales
+//     met so far lie within 2^8 of each other, one d for all rows keeps the row's largest w'
+//     in [1, 2^13), and fp16 holds what is 2^-24 of it; else d is chosen per row so that
+//     the largest w' is about 1. Where a tile has one key and one value scale, they come
+//     out of the sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -40,7 +42,6 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "kv8_attention.h"
 
@@ -200,8 +201,7 @@ __device__ __forceinline__ int piece_at(int key, int piece) {
 }
 
 // ------------------------------------------------------------------ lengths
-// Keys that group g attends to at most: the largest length of its rows that pass the checks;
-// len_of(row) is 0 for one that does not. `err` collects what is wrong.
+// The length of a row, 0 where it does not pass the checks; `err` collects what is wrong.
 __device__ __forceinline__ int row_len(const Params& p, int row, int table, int* err) {
   const int len = __ldg(p.lens + row);
   if (len < 0 || len > p.max_len) {
@@ -219,6 +219,7 @@ __device__ __forceinline__ int row_len(const Params& p, int row, int table, int*
   return len;
 }
 
+// Keys that group g attends to at most: its rows' largest length.
 __device__ __forceinline__ int group_len(const Params& p, int g, int* err) {
   const int table = p.group_table ? __ldg(p.group_table + g) : g;
   int len = 0;
@@ -344,7 +345,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     if (w0 < w1 && w0 >= before * p.kv_heads && w0 < (before + mine) * p.kv_heads) {
       int ignored = 0;
       int64_t i = g0, at = before * p.kv_heads;
-      for (;; ++i) {
+      for (; i + 1 < g1; ++i) {
         const int64_t here = (int64_t)tiles_of(group_len(p, (int)i, &ignored)) * p.kv_heads;
         if (w0 < at + here) break;
         at += here;
@@ -443,7 +444,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     // ---- queries: row r of the unit is row r / ratio of the group, head r % ratio of h's
     for (int x = tid; x < kRows * kPieces; x += kThreads) {
       const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
-      const int row = g * (SELECTED ? 1 : p.group_rows) + r / ratio;
+      const int64_t row = (int64_t)g * (SELECTED ? 1 : p.group_rows) + r / ratio;
       const bool in = r < live && row < p.rows;
       uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
       if (in) {
@@ -482,7 +483,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
         int ignored = 0;
         s_mul[r] = mul;
         // only rows that end before the unit's keys do need the comparison with their length
-        s_len[r] = !in || SELECTED ? INT32_MAX : row_len(p, row, table, &ignored);
+        s_len[r] = !in || SELECTED ? INT32_MAX : row_len(p, (int)row, table, &ignored);
       }
     }
     __syncthreads();

@@ -376,6 +376,15 @@ def test_peaked_and_flat_rows():
     Dense(15, [400, 300], 1, 8, 2, 128, 64, 64, "fp16", q_gain=0.0).check()
 
 
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 5.0])
+@pytest.mark.parametrize("group", [1, 5])
+def test_score_scales(scale, group):
+    """Negative and zero softmax scales take the general tile."""
+    d = Dense(16, [200, 40, 129, 64, 90], group, 16, 2, 128, 64, 64, "bf16")
+    d.scale = scale
+    d.check()
+
+
 def test_zero_scales():
     d = Dense(16, [200, 40], 1, 8, 2, 128, 64, 16, "bf16")
     d.cache[2][:] = 0.0
