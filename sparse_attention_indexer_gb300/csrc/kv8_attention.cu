@@ -17,7 +17,11 @@
 // score set to -inf, so what lies there never enters). Products run on mma.sync m16n8k16
 // fp16 with fp32 accumulators, keys and channels on its 16 rows and query rows on its 8
 // columns: the 8 query heads of a key head fill it, where query rows on the 16 would leave
-// half of the products, the weights and the registers of the sums idle.
+// half of the products, the weights and the registers of the sums idle (52 against 40 us for
+// one row of 64 heads over 80000 keys on 8 key heads, 4.1 TB/s; 32 ragged rows of 857K keys in
+// all 429 against 387 us, 5.7 TB/s). Up to 16 rows three CTAs of two stages fit an SM, which
+// beats two of three stages by 6 %; from there on the products and the weights bound the kernel
+// (56 rows: 98 us, 40 % of the tensor pipe).
 //   - q . k: an fp16 times an e4m3 (widened, exact) product is exact. Rows of bf16 q are
 //     brought to [2^14, 2^15) by a power of two, which fp16 then holds exactly but for
 //     channels 2^-38 below the row's largest. The channels may be summed in any order, so
