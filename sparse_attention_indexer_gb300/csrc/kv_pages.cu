@@ -313,6 +313,7 @@ reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t*
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int64_t s_warp64[kPlanThreads / 32];
+  __shared__ int32_t s_free[2 * kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // the pages of row i's span; [0, 0) where there is none
@@ -328,6 +329,86 @@ reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t*
     }
     return 0;
   };
+  // The lowest free ids in order, `store(k, id)` for the k-th, until `total` are found.
+  auto find_free = [&](int64_t total, auto&& store) {
+    int found = 0;
+    for (int64_t p0 = 0; p0 < num_pages && found < total; p0 += kRound) {
+      uint32_t flags[kQuarters];
+#pragma unroll
+      for (int k = 0; k < kQuarters; ++k) {
+        const int4 r = load_counts(refs, first_of(p0, k), num_pages);
+        flags[k] = (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
+      }
+      int before[kQuarters], sum;
+      ranks(flags, before, s_warp, &sum);
+#pragma unroll
+      for (int k = 0; k < kQuarters; ++k) {
+        int at = found + before[k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (flags[k] >> i & 1) store(at++, (int32_t)(first_of(p0, k) + i));
+      }
+      found += sum;
+    }
+    __syncthreads();
+    return found;
+  };
+
+  // Decode and verify steps: a row to a thread, two pages to a row at most. What a row needs stays
+  // in its thread's registers and the free ids in shared memory, so that tables and counts
+  // are read once (free, fork and reserve of 8 rows: 18.9 us, 21.5 us by the way below).
+  if (n <= kPlanThreads) {
+    int64_t first = 0, last = 0;
+    int bad = 0;
+    if (tid < n) bad = span(tid, &first, &last);
+    if (__syncthreads_and(last - first <= 2)) {
+      if (bad) report(status, bad);
+      int32_t* const a = table + (first < last ? rows[tid] * ld : 0);
+      const int64_t old = tid < n ? old_lens[tid] : 0;
+      int32_t was[2];
+      bool need[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        need[k] = false;
+        if (first + k < last) {
+          was[k] = a[first + k];
+          if (was[k] >= num_pages) report(status, KVPAGES_STATUS_PAGE);
+          else need[k] = was[k] < 0 || refs[was[k]] > 1;
+        }
+      }
+      const int mine = need[0] + need[1];
+      int total;
+      int at = block_scan(mine, s_warp, &total);
+      const int found = find_free(total, [&](int k, int32_t id) {
+        if (k < 2 * kPlanThreads) s_free[k] = id;
+      });
+      int32_t from = -1, to = -1;
+      if (mine && at + mine > found) {
+        report(status, KVPAGES_STATUS_NO_PAGE);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!need[k]) continue;
+          const int32_t id = s_free[at++];
+          if (was[k] >= 0) {
+            atomicSub(refs + was[k], 1);
+            if ((first + k) * page_size < old) {  // only the page of position old - 1
+              from = was[k];
+              to = id;
+            }
+          }
+          a[first + k] = id;
+          refs[id] = 1;
+        }
+      }
+      if (tid < n) {
+        w.src[tid] = from;
+        w.dst[tid] = to;
+      }
+      return;
+    }
+  }
+
   // 1: how many pages each row needs
   for (int i = warp; i < n; i += kPlanThreads / 32) {
     int64_t first, last;
@@ -349,26 +430,7 @@ reserve_plan_kernel(const int32_t* rows, const int32_t* old_lens, const int32_t*
     total += sum;
   }
   // 3: the lowest free ids, until there are enough
-  int found = 0;
-  for (int64_t p0 = 0; p0 < num_pages && found < total; p0 += kRound) {
-    uint32_t flags[kQuarters];
-#pragma unroll
-    for (int k = 0; k < kQuarters; ++k) {
-      const int4 r = load_counts(refs, first_of(p0, k), num_pages);
-      flags[k] = (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
-    }
-    int before[kQuarters], sum;
-    ranks(flags, before, s_warp, &sum);
-#pragma unroll
-    for (int k = 0; k < kQuarters; ++k) {
-      int at = found + before[k];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (flags[k] >> i & 1) w.free[at++] = (int32_t)(first_of(p0, k) + i);
-    }
-    found += sum;
-  }
-  __syncthreads();
+  const int found = find_free(total, [&](int k, int32_t id) { w.free[k] = id; });
   // 4: the list of needed pages of the rows that can be served (nothing is changed yet: the
   // needs of one row read counts that serving another changes)
   for (int i = warp; i < n; i += kPlanThreads / 32) {

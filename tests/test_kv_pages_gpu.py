@@ -189,6 +189,30 @@ def test_more_rows_than_one_round_of_the_plan():
     b.reserve(rows.tolist(), [0] * 2500, b.rng.integers(0, 13, 2500).tolist())
 
 
+@pytest.mark.parametrize("n", [1, 32, 1023, 1024, 1025])
+@pytest.mark.parametrize("free", [0, 700, 5000])
+def test_appends_of_one_or_two_pages(n, free):
+    """Decode and verify steps of up to and over a CTA's rows, with pages enough and not, some of
+    them shared, some rows refused."""
+    b = Both(12, n + 3, 4, 6000, 8, row_bytes=(16, 8))
+    rows = b.rng.permutation(n).astype(int)
+    old = b.rng.integers(0, 17, n)
+    new = np.minimum(old + b.rng.integers(0, 9, n), 32)
+    own = b.rng.permutation(6000)
+    at = 0
+    for r, o in zip(rows, old):
+        for c in range(-(-int(o) // 8)):
+            b.table[r, c] = own[at % 900]       # shared by several rows once more than 900 are out
+            at += 1
+    b.refs[:] = np.bincount(b.table[b.table >= 0], minlength=6000)
+    spare = np.nonzero(b.refs == 0)[0]
+    b.refs[b.rng.permutation(spare)[:max(0, len(spare) - free)]] = 1
+    if n > 40:
+        old[5], new[6], rows[7] = -1, 40, n + 3
+    b.up(max_rows=2000)
+    b.reserve(rows.tolist(), old.tolist(), new.tolist())
+
+
 def test_copy_planes_and_padding():
     b = Both(8, 1, 1, 300, 4, row_bytes=(16, 20, 16384, 16388, 50000))
     b.up()
