@@ -11,8 +11,8 @@
 // in the order of the CTAs. (The last CTA to arrive joining its unit alone took 250 of 334 us
 // for 56 rows to a unit of 80K keys: 38 parts of 28 KB through one SM.)
 //
-// A tile. The four warps of a CTA form KW groups that take a segment's tiles in turn, WM warps
-// to a group, each with NT * 8 of the M rows. A group keeps kStages tiles of codes and scales
+// A tile. The W warps of a CTA (four, or one) form groups that take a segment's tiles in turn, WM
+// warps to a group, each with NT * 8 of the M rows. A group keeps kStages tiles of codes and scales
 // in flight with cp.async (a key that is masked or missing is filled with zeros and its
 // score set to -inf, so what lies there never enters). Products run on mma.sync m16n8k16
 // fp16 with fp32 accumulators, keys and channels on its 16 rows and query rows on its 8
@@ -51,8 +51,6 @@
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 32;   // keys of a tile
 constexpr float kNone = -3e38f;  // maximum of a row that has no key yet: finite, so that no difference
                                  // of two of them is NaN
@@ -176,13 +174,13 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // ------------------------------------------------------------------ layout in shared memory
-template <int DIM, int NT, int WM>
+template <int DIM, int NT, int WM, int W>
 struct Smem {
-  static constexpr int kGroups = kWarps / WM;
+  static constexpr int kGroups = W / WM;
   static constexpr int kRows = 8 * NT * WM;
   // tiles in flight per warp group, CTAs per SM
-  static constexpr int kStages = NT <= 2 ? (WM == 1 ? 2 : WM == 2 ? 3 : 6) : WM == 4 ? 6 : 3;
-  static constexpr int kCtas = NT <= 2 ? 3 : 2;
+  static constexpr int kStages = WM == 4 ? 6 : NT <= 2 ? 2 : 3;
+  static constexpr int kCtas = W == 1 ? (DIM == 64 ? 12 : NT == 1 ? 11 : 10) : NT <= 2 ? 3 : 2;
   static constexpr int kTile = kKeys * DIM;        // bytes of the K (or V) codes of a tile
   static constexpr int kRing = kGroups * kStages * 2 * kTile;
   static constexpr int kLd = DIM + 4;  // floats between the rows of the warps' sums
@@ -280,10 +278,11 @@ __device__ __forceinline__ void write_row(const Params& p, int g, int h, int r, 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
-__global__ void __launch_bounds__(kThreads, Smem<DIM, NT, WM>::kCtas)
+template <int DIM, bool FP16, bool SELECTED, int NT, int WM, int W>
+__global__ void __launch_bounds__(W * 32, Smem<DIM, NT, WM, W>::kCtas)
 kv8_attention_kernel(const __grid_constant__ Params p) {
-  using L = Smem<DIM, NT, WM>;
+  using L = Smem<DIM, NT, WM, W>;
+  constexpr int kWarps = W, kThreads = W * 32;
   constexpr int kGroups = L::kGroups, kRows = L::kRows, kStages = L::kStages;
   constexpr int kPieces = DIM / 16;   // 16-byte pieces of a row of codes
   constexpr int kSteps = DIM / 16;    // mma steps of q . k
@@ -325,7 +324,15 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     const int64_t g0 = min((int64_t)groups, (int64_t)tid * per);
     const int64_t g1 = min((int64_t)groups, g0 + per);
     int64_t mine = 0;
-    for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len(p, (int)i, &err));
+    if (p.group_rows == 1) {  // all loads of eight rows on their way at once
+#pragma unroll 8
+      for (int64_t i = g0; i < g1; ++i)
+        mine += tiles_of(
+            row_len(p, (int)i, p.group_table ? __ldg(p.group_table + i) : (int)i, &err));
+    } else {
+#pragma unroll 2
+      for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len(p, (int)i, &err));
+    }
     if (me) err = 0;  // CTA 0 reports for all
     int64_t before = mine, total = 0;
 #pragma unroll
@@ -1083,10 +1090,11 @@ int shift_of(int x) {
   return s;
 }
 
-template <int DIM, bool FP16, bool SELECTED, int NT, int WM>
+template <int DIM, bool FP16, bool SELECTED, int NT, int WM, int W>
 int launch(const Params& p, int dev, cudaStream_t s) {
-  using L = Smem<DIM, NT, WM>;
-  const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, NT, WM>;
+  using L = Smem<DIM, NT, WM, W>;
+  constexpr int kThreads = W * 32;
+  const auto kernel = kv8_attention_kernel<DIM, FP16, SELECTED, NT, WM, W>;
   const auto join = kv8_join_kernel<DIM, FP16, L::kRows>;
   // once on a device; both with the largest share of shared memory: a change of it between
   // them would cost time
@@ -1133,20 +1141,28 @@ int launch(const Params& p, int dev, cudaStream_t s) {
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
 }
 
+// Up to 16 rows to a unit: four warps to a CTA, or, where there is a unit for every warp of the
+// device, one. Then a warp passes from unit to unit without waiting for three others: 2048 rows
+// of 200-400 keys and 8 key heads 345 against 299 us, 8192 of 20-40 keys 819 against 590 us.
+template <int DIM, bool FP16, bool SELECTED, int NT>
+int launch_few(const Params& p, int dev, cudaStream_t s) {
+  const int64_t groups = ((int64_t)p.rows + p.group_rows - 1) / p.group_rows;
+  if (groups * p.kv_heads >= (int64_t)sm_count(dev) * Smem<DIM, NT, 1, 1>::kCtas)
+    return launch<DIM, FP16, SELECTED, NT, 1, 1>(p, dev, s);
+  return launch<DIM, FP16, SELECTED, NT, 1, 4>(p, dev, s);
+}
+
 template <int DIM, bool FP16, bool SELECTED>
 int launch_rows(const Params& p, int live, int dev, cudaStream_t s) {
-  if constexpr (SELECTED) {  // at most 16 rows to a unit
-    return live <= 8 ? launch<DIM, FP16, true, 1, 1>(p, dev, s)
-                     : launch<DIM, FP16, true, 2, 1>(p, dev, s);
-  } else {
-    switch (padded_rows(live)) {
-      case 8: return launch<DIM, FP16, false, 1, 1>(p, dev, s);
-      case 16: return launch<DIM, FP16, false, 2, 1>(p, dev, s);
-      case 32: return launch<DIM, FP16, false, 4, 1>(p, dev, s);
-      case 64: return launch<DIM, FP16, false, 4, 2>(p, dev, s);
-      default: return launch<DIM, FP16, false, 4, 4>(p, dev, s);
-    }
+  const int rows = padded_rows(live);
+  if (rows == 8) return launch_few<DIM, FP16, SELECTED, 1>(p, dev, s);
+  if (rows == 16) return launch_few<DIM, FP16, SELECTED, 2>(p, dev, s);
+  if constexpr (!SELECTED) {  // the selected form has at most 16 rows to a unit
+    if (rows == 32) return launch<DIM, FP16, false, 4, 1, 4>(p, dev, s);
+    if (rows == 64) return launch<DIM, FP16, false, 4, 2, 4>(p, dev, s);
+    return launch<DIM, FP16, false, 4, 4, 4>(p, dev, s);
   }
+  return KV8_ERR_SHAPE;
 }
 
 Params common(const void* q, int64_t q_ld, int rows, int q_heads, int kv_heads, float sm_scale,
@@ -1202,7 +1218,8 @@ extern "C" int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int 
   const int sms = sm_count(current_device());
   if (sms < 0) return KV8_ERR_CUDA;
   const int rows = padded_rows(group_rows * (q_heads / kv_heads));
-  const int64_t ctas = sms * 3 < kMaxCtas ? sms * 3 : kMaxCtas;  // most of any variant
+  const int64_t most = (int64_t)sms * (rows <= 16 ? 12 : 2);  // CTAs of any variant for these rows
+  const int64_t ctas = most < kMaxCtas ? most : kMaxCtas;
   return kMaxCtas * (int64_t)sizeof(Shared) + ctas * 2 * rows * (dim + 4) * 4;
 }
 

@@ -365,6 +365,18 @@ def test_many_short_rows():
         rows=set(range(0, 1201, 11)))
 
 
+@pytest.mark.parametrize("hq,dim,group,dtype", [(6, 64, 1, "bf16"), (16, 128, 1, "fp16"),
+                                                (30, 128, 1, "bf16"), (8, 64, 4, "fp16")])
+def test_a_unit_for_every_warp(hq, dim, group, dtype):
+    """More units than the device has warps for them: a warp to a CTA, long rows split over
+    several, empty ones among them."""
+    rng = np.random.default_rng(dim + hq)
+    lens = rng.integers(0, 70, 950 * group)
+    lens[rng.permutation(950 * group)[:6]] = [3000, 700, 0, 1, 32, 2111]
+    Dense(40 + hq, lens.tolist(), group, hq, 2, dim, 32, 16, dtype).check(
+        rows=set(np.argsort(lens)[-8:].tolist()) | set(range(0, 950 * group, 41 * group)))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_scales_far_apart(dtype):
     """Block scales over 24 octaves: a heavily weighted block next to one of large values."""
@@ -605,6 +617,11 @@ def test_selected_nothing_and_strides():
 
 def test_selected_rows_many():
     check_selected(*selected_case(34, 300, 33, 4, 1, 64, 32, "fp16"), "fp16")
+
+
+@pytest.mark.parametrize("hq,dim", [(2, 128), (24, 64)])
+def test_selected_a_unit_for_every_warp(hq, dim):
+    check_selected(*selected_case(36, 950, 70, hq, 2, dim, 16, "bf16"), "bf16")
 
 
 def test_selected_equals_dense():
