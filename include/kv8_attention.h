@@ -58,7 +58,7 @@ enum {
                              multiple of page_size (of block_tokens for the selected form),
                              n_tables < 1, table_ld < 1, a row stride below the row or not
                              a multiple of 8, slots_ld < k, sm_scale not finite, or more
-                             than 2^31 - 1 pairs of work */
+                             than 2^33 pairs of a group and a key head */
   KV8_ERR_ALIGN = -3,     /* q, out, k, v, caches or workspace not 16-byte aligned, or
                              another array not 4-byte aligned */
   KV8_ERR_CUDA = -4,      /* a launch or a device query failed */
