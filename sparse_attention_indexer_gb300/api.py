@@ -262,6 +262,7 @@ class KvPages:
     block_table  int32 [n_tables, table_ld]: -1 where a sequence has no page
     refs         int32 [num_pages]: owners of each page, 0 of a free one
     planes       the tensors that hold the pages' data, each [num_pages, ...]
+    max_rows     the most rows that one reserve names
     All stay the caller's and are changed in place. One instance serves one stream at a
     time. `status` collects the device status bits of all calls."""
 
