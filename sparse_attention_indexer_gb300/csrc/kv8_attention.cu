@@ -523,7 +523,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     // m: a maximum of x, not more than kSlack below the running one; o is relative to
     // 2^(m + d), sum to 2^m
     float m[NT][2], d[NT][2], sum[NT][2];
-    uint32_t sv_top = 0, sv_low = 255;  // exponents of the value scales so far
+    uint32_t sv_top = 0, sv_low = 255;  // largest and least exponent of the value scales so far
     float d_all = 0.0f;                 // d, while all rows have the same
     bool d_own = false;                 // they have not
 #pragma unroll
@@ -601,10 +601,11 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       const float ks0 = sc[0], vs0 = sc[kKeys];
       bool same;  // one key scale and one value scale
       {
-        // exponents of the scales of the values (zeros weigh nothing and do not count)
+        // exponents of the scales of the values; a 0 counts as the least: where the heaviest key's
+        // scale is 0, the row's largest weight * scale may lie any distance below the maximum
         const float v = sc[kKeys + lane];
-        const bool some = ((in >> lane) & 1) && v != 0.0f;
-        const uint32_t e = __float_as_uint(v) >> 23;
+        const bool some = (in >> lane) & 1;
+        const uint32_t e = (__float_as_uint(v) & 0x7FFFFFFFu) >> 23;
         sv_top = max(sv_top, __reduce_max_sync(0xffffffffu, some ? e : 0u));
         sv_low = min(sv_low, __reduce_min_sync(0xffffffffu, some ? e : 255u));
         same = !SELECTED && __all_sync(0xffffffffu, sc[lane] == ks0 && v == vs0);
@@ -689,7 +690,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
               // what there is already lies around 2^(m + d)
               if (m[i][b] > kNone) tv = fmaxf(tv, m[i][b] + d[i][b]);
               dn = tv - top;
-              dn = tv > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : 0.0f;
+              dn = tv > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : -120.0f;
             }
             const float drop = exp2_fast(m[i][b] - top);
             sum[i][b] *= drop;

@@ -406,6 +406,70 @@ def test_zero_scales():
     d.check()
 
 
+def far_scales(d, rng, exponents, zero):
+    """Value scales 2^e, e alternating between two exponents from block to block (a tile has
+    both), and a tile's blocks zero with probability `zero`."""
+    sv = d.cache[3]
+    blocks = np.arange(len(sv))
+    sv[:] = np.exp2(np.asarray(exponents, np.float64)[blocks % 2])[:, None]
+    sv[np.repeat(rng.random(len(sv) // 2 + 1) < zero, 2)[:len(sv)]] = 0.0
+
+
+def one_table(seed, rows, length, group, hq, hk, dim, block=16):
+    """Rows of one length over one table row, with value scales far apart, for launches in
+    which a warp takes many tiles of a row."""
+    d = Dense(seed, [length] * group, group, hq, hk, dim, 64, block, "bf16", poison=False)
+    d.table[0] = np.arange(d.table.shape[1])  # consecutive pages: tiles take blocks in order
+    q = torch.from_numpy(d.rng.standard_normal((rows, hq, dim)).astype(np.float32))
+    d.q = q.to(torch.bfloat16).to(DEV)
+    d.lens = np.full(rows, length, np.int32)
+    d.group_table = np.zeros(-(-rows // group), np.int32)
+    return d
+
+
+def check_rows(d, rows):
+    """Dense.check without the references of the other rows."""
+    h = d.handle()
+    out, lse = h.attention(*d.args())
+    for r in rows:
+        ref, st = d.ref(r)
+        assert st == 0
+        close(out[r].double().cpu().numpy(), lse[r].double().cpu().numpy(), ref, d.dtype, f"row {r}")
+    assert int(h.status.item()) == 0
+
+
+# (rows, keys, group, query heads, key heads, dim) that give a warp about 100 tiles of a row: a warp
+# to a CTA, four to a CTA, and units of 32, 64 and 128 rows
+MANY_TILES = [(1900, 3200, 1, 1, 1, 128), (1900, 3200, 1, 16, 1, 64), (300, 12800, 1, 8, 1, 128),
+              (2400, 12800, 8, 4, 1, 128), (2400, 12800, 8, 8, 1, 64), (2400, 12800, 8, 16, 1, 128)]
+
+
+@pytest.mark.parametrize("rows,length,group,hq,hk,dim", MANY_TILES)
+def test_keys_of_zero_scale_before_small_scales(rows, length, group, hq, hk, dim):
+    """Tiles whose values have scale 0 set no reference for the tiles of 2^-28 and 2^-40 after
+    them."""
+    d = one_table(60 + group, rows, length, group, hq, hk, dim)
+    far_scales(d, d.rng, (-28, -40), 0.5)
+    check_rows(d, (0, rows // 2, rows - 1))
+
+
+@pytest.mark.parametrize("group", [1, 4])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_heaviest_key_of_zero_scale(dim, group):
+    """The block of the heaviest key has value scale 0: what is left are keys of 2^-20 to 2^-90 of
+    its weight, and the output is theirs."""
+    lens = [32] * (6 * group)
+    d = Dense(80 + dim, lens, group, 4, 4, dim, 32, 16, "bf16", poison=False, q_gain=25.0)
+    for g in range(6):
+        d.q[g * group:(g + 1) * group] = d.q[g * group]   # the rows of a group agree on the key
+        slots = K8.row_slots(d.table, g, 32, 32, 32, d.cache[0].shape[0])[0]
+        q = K8.values(bits(d.q[g * group]), "bf16")
+        for h in range(4):
+            kk = K8.e4m3_value(d.cache[0][slots, h]) * d.cache[2][slots // 16, h][:, None]
+            d.cache[3][slots[np.argmax(kk @ q[h])] // 16, h] = 0.0
+    d.check()
+
+
 @pytest.mark.parametrize("dim,hq", [(64, 8), (128, 8), (128, 32)])
 def test_nan_seen_by_the_later_rows_alone(dim, hq):
     """NaN codes and scales in the last draft's key and value: the rows before it are as
