@@ -687,10 +687,11 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
                   tv = fmaxf(tv, s[i][j][2 * c + b] + log2_fast(vs[j][c]));
 #pragma unroll
               for (int x = 4; x <= 16; x <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, x));
-              // what there is already lies around 2^(m + d)
-              if (m[i][b] > kNone) tv = fmaxf(tv, m[i][b] + d[i][b]);
-              dn = tv - top;
-              dn = tv > -INFINITY ? fminf(fmaxf(ceilf(dn), -120.0f), 126.0f) : -120.0f;
+              // 2^(m + d) is the largest so far (the first time a bound below it): d is no whole
+              // number, as one would let m + d rise with every rise of m
+              const float was = m[i][b] > kNone ? m[i][b] + d[i][b] : -INFINITY;
+              dn = tv <= was && top == m[i][b] ? d[i][b] : fmaxf(tv, was) - top;
+              dn = fminf(fmaxf(dn, -120.0f), 126.0f);
             }
             const float drop = exp2_fast(m[i][b] - top);
             sum[i][b] *= drop;

@@ -453,6 +453,22 @@ def test_keys_of_zero_scale_before_small_scales(rows, length, group, hq, hk, dim
     check_rows(d, (0, rows // 2, rows - 1))
 
 
+@pytest.mark.parametrize("rows,length,group,hq,hk,dim", MANY_TILES)
+def test_scores_that_rise_while_value_scales_fall(rows, length, group, hq, hk, dim):
+    """weight * value scale is about the same in all tiles: the reference of the weights' rounding
+    does not rise with the row's maximum."""
+    d = one_table(70 + group, rows, length, group, hq, hk, dim)
+    blocks = np.arange(len(d.cache[2]))
+    # 60 octaves over the row, in steps of a tile
+    octave = 60.0 * (blocks // 2) / (len(blocks) // 2)
+    # log2 of a weight: log2(e) / sqrt(dim) * q . k, with q . k = dim * key scale
+    d.cache[0][:] = 0x38                    # 1.0
+    d.q.fill_(1.0)
+    d.cache[2][:] = (octave * math.log(2) / math.sqrt(dim))[:, None]
+    d.cache[3][:] = np.exp2(-octave - 12.0 * (blocks % 2))[:, None]
+    check_rows(d, (0, rows // 2, rows - 1))
+
+
 @pytest.mark.parametrize("group", [1, 4])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_heaviest_key_of_zero_scale(dim, group):
