@@ -89,7 +89,7 @@ def verify(target, draft, tokens, uniforms, n_drafts=None, mutant=0):
             if total >= 15 * ONE:
                 status |= w.status
                 continue
-            at = total * int(Fraction(r) * (1 << 64)) >> 64
+            at = math.floor(Fraction(r) * total)
             run = 0
             for v, x in enumerate(weights):
                 run += x

@@ -76,6 +76,16 @@ __device__ __forceinline__ uint64_t value(const Digits& d) {
   return ((uint64_t)(int64_t)d.a << 40) + ((uint64_t)(int64_t)d.b << 20) + (uint64_t)(int64_t)d.c;
 }
 
+// floor(r * total) for r in [0, 1): the significand times total, 88 bits, moved down by the exponent.
+__device__ __forceinline__ uint64_t drawn_point(float r, uint64_t total) {
+  const uint32_t b = __float_as_uint(r), e = b >> 23;
+  const uint64_t m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);  // r = m * 2^-down
+  const int down = 150 - (int)max(e, 1u);                     // 24 .. 149
+  const uint64_t low = m * total, high = __umul64hi(m, total);
+  if (down >= 88) return 0;
+  return down >= 64 ? high >> (down - 64) : (high << (64 - down)) | (low >> down);
+}
+
 enum Row { kBonus, kRefused, kRefusedPoint };
 
 // The weights of tokens v0 + 32 i + lane, i < kStep, in digits; 0 past `end`. Loads past it
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(P
   }
 
   const float r = checked_uniform(__ldg(uni + p.drafts), &err);
-  const uint64_t at = __umul64hi(total, __float2ull_rz(r * 0x1p64f));  // floor(r * total)
+  const uint64_t at = drawn_point(r, total);
   const bool lost = high >= uint64_t(15) << 28;
   if (lost || total > (uint64_t(1) << 63)) err |= VERIFY_STATUS_PROB;
   for (int w = 0; w < warp; ++w) before += s_sum[w];

@@ -82,6 +82,30 @@ def test_draws_over_the_whole_row(seed):
     check(p, q, tok, u)
 
 
+def above(x):
+    """The least float32 that is not below x."""
+    f = np.float32(x)
+    return f if f >= x else np.nextafter(f, np.float32(np.inf))
+
+
+@pytest.mark.parametrize("ones", [0, 9])
+def test_uniforms_with_bits_below_2_to_the_64th(ones):
+    """Tokens of 2^-60 each before those that have the rest: the drawn token is floor(r * sum),
+    for the least r at which it is a given one, whose last bits lie below 2^-64."""
+    rng = np.random.default_rng(ones)
+    want = np.unique(np.concatenate([2 ** np.arange(13), rng.integers(1, 5900, 50)]))
+    vocab, reqs = 6000, len(want) + 2
+    p = np.full((reqs, 1, vocab), 2.0 ** -60, np.float32)
+    p[:, 0, -1] = rng.uniform(0.5, 1, reqs)
+    p[:, 0, vocab - 1 - ones:vocab - 1] = 0.75
+    total = p[:, 0].astype(np.float64).sum(-1)
+    u = np.zeros((reqs, 1), np.float32)
+    u[:-2, 0] = [above(k * 2.0 ** -60 / t) for k, t in zip(want, total)]
+    u[-2], u[-1] = 2.0 ** -149, 2.0 ** -62
+    o, k, s = check(p, None, np.zeros((reqs, 0), np.int32), u)
+    assert s == 0 and o[:-2, 0].tolist() == want.tolist()
+
+
 def test_ties_of_the_test_and_of_the_draw():
     """u q equal to p refuses; a running sum equal to the point does not stop the draw."""
     p = np.full((4, 2, 8), 0.125, np.float32)

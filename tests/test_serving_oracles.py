@@ -1,6 +1,7 @@
 """Pins of the oracles of the 8-bit cache, the page operations and the drafts' verification:
 hand-worked values, invariants, distributions, and planted mistakes that must show."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -204,3 +205,21 @@ def test_verify_keeps_the_targets_distribution(point):
     o, k, s = DV.verify(np.tile(p, (n, 1, 1)), None if point else np.tile(q, (n, 1, 1)), tok, u)
     freq = np.bincount(o[:, 0], minlength=v) / n
     assert s == 0 and np.all(np.abs(freq - p[0]) < 5 * np.sqrt(p[0] / n))
+
+
+def test_verify_draws_at_the_floor():
+    """The drawn token is the least whose running sum passes floor(r * sum), for the least r that
+    draws a given one (its last bits lie far below the sums' unit)."""
+    rng = np.random.default_rng(200)
+    vocab, n = 5000, 40
+    p = np.full((n, 1, vocab), 2.0 ** -60, np.float32)
+    p[:, 0, -1] = rng.uniform(0.5, 1, n)
+    want = rng.integers(1, vocab - 1, n)
+    u = np.zeros((n, 1), np.float32)
+    for j in range(n):
+        total = vocab - 1 + int(float(p[j, 0, -1]) * 2.0 ** 60)
+        u[j] = np.float32(int(want[j]) / total)
+        while Fraction(float(u[j, 0])) * total < int(want[j]):
+            u[j] = np.nextafter(u[j], np.float32(1))
+    o, k, s = DV.verify(p, None, np.zeros((n, 0), np.int32), u)
+    assert s == 0 and o[:, 0].tolist() == want.tolist()
