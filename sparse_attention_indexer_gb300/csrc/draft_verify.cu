@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(P
   const int begin = (int)min(begin64, (int64_t)p.vocab);
   const int end = (int)min(begin64 + (int64_t)steps * kTokens, (int64_t)p.vocab);
 
-  // A row that sums to 16 or more would wrap the sums: the upper halves tell
+  // A row that sums to 16 or more wraps the sums: the upper halves tell
   uint64_t total = 0, before = 0, high = 0;
   for (int round = 0; round < 2; ++round) {
     uint64_t sum = 0, record = 0, upper = 0;
@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) draft_verify_kernel(P
 
   const float r = checked_uniform(__ldg(uni + p.drafts), &err);
   const uint64_t at = drawn_point(r, total);
-  const bool lost = high >= uint64_t(15) << 28;
+  // 15 or more: a sum below 16 is in `total` as it is; of one above, the upper halves of at most
+  // 2^27 partial sums, each less than one too low, leave more than 15 * 2^28
+  const bool lost = high >= uint64_t(15) << 28 || total >= uint64_t(15) << 60;
   if (lost || total > (uint64_t(1) << 63)) err |= VERIFY_STATUS_PROB;
   for (int w = 0; w < warp; ++w) before += s_sum[w];
   const uint64_t mine = s_sum[warp];

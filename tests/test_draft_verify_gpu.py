@@ -158,6 +158,20 @@ def test_rows_that_would_wrap_the_sums():
     assert s == DV.PROB and o[0, 0] == -1 and o[1, 0] == 2000
 
 
+@pytest.mark.parametrize("vocab", [300, 70000])
+def test_rows_that_sum_to_fifteen(vocab):
+    """No token from a sum of 15, wherever the tokens lie; one from the least sum below."""
+    rng = np.random.default_rng(vocab)
+    w = [1.0] * 14 + [2.0 ** -i for i in range(1, 29)]
+    p = np.zeros((24, 1, vocab), np.float32)
+    for j in range(24):
+        at = rng.permutation(vocab)[:len(w) + 2]
+        p[j, 0, at] = w + ([2.0 ** -29, 2.0 ** -29] if j < 12 else [2.0 ** -29, 2.0 ** -30])
+    u = rng.random((24, 1)).astype(np.float32)
+    o, k, s = check(p, None, np.zeros((24, 0), np.int32), u)
+    assert (o[:12] == -1).all() and (o[12:] >= 0).all() and s == DV.PROB
+
+
 @pytest.mark.parametrize("vocab", [255, 256, 257, 4095, 16384, 32768, 32769, 65537, 1100000])
 def test_slices_and_steps(vocab):
     """One token's weight at a step's, a slice's and the row's ends."""
