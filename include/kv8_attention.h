@@ -113,7 +113,8 @@ int64_t kv8_attention_workspace_bytes(int q_heads, int kv_heads, int dim, int gr
  *   out          device, q's type [rows, out_ld], 16-byte aligned; may not overlap q
  *   lse          device float32 [rows, q_heads] or NULL
  *   workspace    device, 16-byte aligned; what it holds before and after is of no account.
- *                One workspace serves one stream at a time. */
+ *                One workspace serves one stream at a time, and its two launches belong
+ *                together: host threads that share one enqueue their calls one after another. */
 int kv8_attention(const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads,
                   int dim, float sm_scale, const int32_t* lens, int max_len, int group_rows,
                   const int32_t* group_table, const int32_t* block_table, int n_tables,

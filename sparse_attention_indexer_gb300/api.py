@@ -6,6 +6,7 @@ allocates device memory through torch and passes pointers, sizes and the stream.
 from __future__ import annotations
 
 import contextlib
+import threading
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -113,8 +114,8 @@ class Kv8Cache:
     k_scale, v_scale  float32 [num_slots / block_tokens, kv_heads]
     The tensors stay the caller's; several layers are several caches. The workspace is made
     when a call first needs it, one for each stream the cache is used on (make the first call
-    of a shape before a stream capture). `status` collects the device status bits of all
-    calls."""
+    of a shape before a stream capture). Several host threads may call one cache, on one stream
+    too. `status` collects the device status bits of all calls."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor, page_size: int, block_tokens: int):
@@ -132,6 +133,8 @@ class Kv8Cache:
         self.page_size, self.block_tokens = int(page_size), int(block_tokens)
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._workspaces = {}
+        # held over an attention call: its two launches use the stream's workspace together
+        self._lock = threading.Lock()
         self._heads, self._dim = k.shape[1], k.shape[2]
         # the cache's part of every call, made once
         self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -190,14 +193,15 @@ class Kv8Cache:
             _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table")
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
-        ws, ws_bytes = self._workspace(heads, group_rows, handle, stream)
-        code = self._lib.kv8_attention(
-            q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim, sm_scale,
-            lens.data_ptr(), max_len, group_rows,
-            None if group_table is None else group_table.data_ptr(), block_table.data_ptr(),
-            block_table.shape[0], block_table.shape[1], self.page_size, self.block_tokens,
-            *self._args, out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes,
-            self.status.data_ptr(), handle)
+        with self._lock:
+            ws, ws_bytes = self._workspace(heads, group_rows, handle, stream)
+            code = self._lib.kv8_attention(
+                q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim,
+                sm_scale, lens.data_ptr(), max_len, group_rows,
+                None if group_table is None else group_table.data_ptr(), block_table.data_ptr(),
+                block_table.shape[0], block_table.shape[1], self.page_size, self.block_tokens,
+                *self._args, out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes,
+                self.status.data_ptr(), handle)
         if code < 0:
             raise B.Kv8Error(code, "kv8_attention")
         return out, lse
@@ -215,12 +219,13 @@ class Kv8Cache:
             raise ValueError("slots is CUDA int32 [rows, k]")
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
-        ws, ws_bytes = self._workspace(heads, 1, handle, stream)
-        code = self._lib.kv8_attention_selected(
-            q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim, sm_scale,
-            slots.data_ptr(), slots.shape[1], B._ld(slots), self.block_tokens, *self._args,
-            out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes, self.status.data_ptr(),
-            handle)
+        with self._lock:
+            ws, ws_bytes = self._workspace(heads, 1, handle, stream)
+            code = self._lib.kv8_attention_selected(
+                q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim,
+                sm_scale, slots.data_ptr(), slots.shape[1], B._ld(slots), self.block_tokens,
+                *self._args, out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes,
+                self.status.data_ptr(), handle)
         if code < 0:
             raise B.Kv8Error(code, "kv8_attention_selected")
         return out, lse

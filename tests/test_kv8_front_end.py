@@ -1,0 +1,118 @@
+"""What the tensor-level front end of the 8-bit cache and the pages does around the library's
+calls, on the CPU: the library is a stand-in that records how it is called, and CPU tensors
+that say they are on a GPU stand for device memory."""
+import threading
+import time
+
+import pytest
+
+torch = pytest.importorskip("torch")
+S = pytest.importorskip("sparse_attention_indexer_gb300")
+from sparse_attention_indexer_gb300 import api  # noqa: E402
+
+
+class Device(torch.Tensor):
+    """A CPU tensor that says it is on a GPU."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+
+def dev(t):
+    return t.as_subclass(Device)
+
+
+class Torch:
+    """torch for the front end: what it makes is on the CPU and says it is on a GPU."""
+
+    def __init__(self):
+        self.cuda = self.Cuda()
+
+    class Cuda:
+        def __getattr__(self, name):
+            return getattr(torch.cuda, name)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    def empty(self, shape, dtype=None, device=None):
+        return dev(torch.empty(shape, dtype=dtype))
+
+    def zeros(self, shape, dtype=None, device=None):
+        return dev(torch.zeros(shape, dtype=dtype))
+
+
+class Library:
+    """Records its calls; a call of two launches takes a while between them."""
+
+    def __init__(self):
+        self.launches = []
+        self.calls = []
+
+    def kvpages_workspace_bytes(self, n, pages):
+        return 1024
+
+    def kv8_attention_workspace_bytes(self, *a):
+        return 512
+
+    def __getattr__(self, name):
+        def call(*a):
+            me = (name, threading.get_ident(), len(self.calls))
+            self.calls.append((name, a))
+            self.launches.append(me)
+            if name in ("kv8_attention", "kv8_attention_selected", "kvpages_reserve",
+                        "kvpages_compact"):
+                time.sleep(0.002)
+                self.launches.append(me)
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(api.B, "lib", lambda: lib)
+    monkeypatch.setattr(api.B, "_stream", lambda s: 7)
+    monkeypatch.setattr(api, "torch", Torch())
+    return lib
+
+
+def cache():
+    codes = lambda: dev(torch.zeros((64, 2, 64), dtype=torch.uint8))  # noqa: E731
+    return S.Kv8Cache(codes(), codes(), dev(torch.ones(4, 2)), dev(torch.ones(4, 2)), 32, 16)
+
+
+def attention_args(rows=2):
+    return (dev(torch.zeros((rows, 4, 64), dtype=torch.bfloat16)),
+            dev(torch.zeros(rows, dtype=torch.int32)), 32,
+            dev(torch.zeros((rows, 1), dtype=torch.int32)), 0.1)
+
+
+def in_pairs(launches):
+    """Both launches of a call follow one another."""
+    return len(launches) % 2 == 0 and all(a == b for a, b in zip(launches[::2], launches[1::2]))
+
+
+def on_threads(*calls):
+    failed = []
+
+    def repeat(call):
+        try:
+            for _ in range(8):
+                call()
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=repeat, args=(c,)) for c in calls]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed
+
+
+def test_attention_of_two_threads(library):
+    """A call's two launches share a workspace with the next call's on the stream: no thread
+    comes between them."""
+    c, a = cache(), attention_args()
+    q, slots = a[0], dev(torch.zeros((2, 3), dtype=torch.int32))
+    on_threads(lambda: c.attention(*a), lambda: c.attention(*a),
+               lambda: c.attention_selected(q, slots, 0.1))
+    assert len(library.launches) == 48 and in_pairs(library.launches)
