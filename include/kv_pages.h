@@ -18,9 +18,11 @@
  * order of the rows named and of their pages, so every result is determined by the
  * arguments. Nothing here waits on the host or allocates.
  *
- * Each call is enqueued on `stream`. A row id may be named once per call; rows,
- * parents and children that break this, or a contract below, race on the table and
- * the counts, but every access stays inside the arrays. */
+ * Each call is enqueued on `stream`. The two launches of a reserve or a compact use the
+ * workspace together: host threads that share one enqueue their calls one after another.
+ * A row id may be named once per call; rows, parents and children that break this, or a
+ * contract below, race on the table and the counts, but every access stays inside the
+ * arrays. */
 #ifndef KV_PAGES_H
 #define KV_PAGES_H
 

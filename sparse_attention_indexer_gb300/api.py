@@ -269,7 +269,8 @@ class KvPages:
     planes       the tensors that hold the pages' data, each [num_pages, ...]
     max_rows     the most rows that one reserve names
     All stay the caller's and are changed in place. One instance serves one stream at a
-    time. `status` collects the device status bits of all calls."""
+    time; several host threads may call it there. `status` collects the device status bits of
+    all calls."""
 
     def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
                  planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
@@ -293,6 +294,8 @@ class KvPages:
         self._ws_args = (self.workspace.data_ptr(), self.workspace.numel())
         self._status = self.status.data_ptr()
         self._lib = B.lib()
+        # held over a call: reserve's and compact's two launches use the workspace together
+        self._lock = threading.Lock()
 
     def reserve(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
                 stream=None) -> None:
@@ -302,10 +305,12 @@ class KvPages:
             _int32(t, (n,), name)
         if n > self.max_rows:
             raise ValueError(f"more than max_rows = {self.max_rows} rows")
-        B._kvp(self._lib.kvpages_reserve(
-            rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
-            self.page_size, *self._pool_args, *self._plane_args, *self._ws_args, self._status,
-            B._stream(stream)), "kvpages_reserve")
+        with self._lock:
+            code = self._lib.kvpages_reserve(
+                rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
+                self.page_size, *self._pool_args, *self._plane_args, *self._ws_args, self._status,
+                B._stream(stream))
+        B._kvp(code, "kvpages_reserve")
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
              stream=None) -> None:
@@ -313,9 +318,11 @@ class KvPages:
         n = parents.shape[0]
         for t, name in ((parents, "parents"), (children, "children"), (lens, "lens")):
             _int32(t, (n,), name)
-        B._kvp(self._lib.kvpages_fork(
-            parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, *self._table_args,
-            self.page_size, *self._pool_args, self._status, B._stream(stream)), "kvpages_fork")
+        with self._lock:
+            code = self._lib.kvpages_fork(
+                parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, *self._table_args,
+                self.page_size, *self._pool_args, self._status, B._stream(stream))
+        B._kvp(code, "kvpages_fork")
 
     def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
              stream=None) -> None:
@@ -323,19 +330,22 @@ class KvPages:
         _int32(rows, (rows.shape[0],), "rows")
         if keep_lens is not None:
             _int32(keep_lens, (rows.shape[0],), "keep_lens")
-        B._kvp(self._lib.kvpages_free(
-            rows.data_ptr(), None if keep_lens is None else keep_lens.data_ptr(), rows.shape[0],
-            *self._table_args, self.page_size, *self._pool_args, self._status,
-            B._stream(stream)), "kvpages_free")
+        with self._lock:
+            code = self._lib.kvpages_free(
+                rows.data_ptr(), None if keep_lens is None else keep_lens.data_ptr(),
+                rows.shape[0], *self._table_args, self.page_size, *self._pool_args, self._status,
+                B._stream(stream))
+        B._kvp(code, "kvpages_free")
 
     def compact(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Moves the live pages into the lowest ids. Returns (new_ids, counts): the new id
         of each page (-1 of a free one) and {live pages, pages moved}; both are this
         instance's buffers, overwritten by the next call."""
-        B._kvp(self._lib.kvpages_compact(
-            *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
-            self.counts.data_ptr(), *self._ws_args, self._status, B._stream(stream)),
-            "kvpages_compact")
+        with self._lock:
+            code = self._lib.kvpages_compact(
+                *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
+                self.counts.data_ptr(), *self._ws_args, self._status, B._stream(stream))
+        B._kvp(code, "kvpages_compact")
         return self.new_ids, self.counts
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -343,9 +353,11 @@ class KvPages:
         n = src.shape[0]
         _int32(src, (n,), "src")
         _int32(dst, (n,), "dst")
-        B._kvp(self._lib.kvpages_copy(
-            src.data_ptr(), dst.data_ptr(), n, self.num_pages, *self._plane_args, self._status,
-            B._stream(stream)), "kvpages_copy")
+        with self._lock:
+            code = self._lib.kvpages_copy(
+                src.data_ptr(), dst.data_ptr(), n, self.num_pages, *self._plane_args, self._status,
+                B._stream(stream))
+        B._kvp(code, "kvpages_copy")
 
 
 def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor,

@@ -116,3 +116,24 @@ def test_attention_of_two_threads(library):
     on_threads(lambda: c.attention(*a), lambda: c.attention(*a),
                lambda: c.attention_selected(q, slots, 0.1))
     assert len(library.launches) == 48 and in_pairs(library.launches)
+
+
+def pages():
+    planes = [dev(torch.zeros((8, 16), dtype=torch.uint8))]
+    return S.KvPages(dev(torch.full((4, 2), -1, dtype=torch.int32)),
+                     dev(torch.zeros(8, dtype=torch.int32)), 16, planes)
+
+
+def test_page_operations_of_two_threads(library):
+    """reserve and compact leave a list of copies for their second launch: no other operation of
+    the pool comes between."""
+    p = pages()
+    i = [dev(torch.zeros(2, dtype=torch.int32)) for _ in range(3)]
+    on_threads(lambda: p.reserve(*i), lambda: p.compact(), lambda: p.reserve(*i))
+    assert len(library.launches) == 48 and in_pairs(library.launches)
+    library.launches.clear()
+    on_threads(lambda: p.reserve(*i), lambda: (p.fork(*i), p.fork(*i)),
+               lambda: (p.free(i[0]), p.free(i[0])), lambda: (p.copy(*i[:2]), p.copy(*i[:2])))
+    two = [x for x in library.launches if x[0] == "kvpages_reserve"]
+    at = [library.launches.index(x) for x in two[::2]]
+    assert all(library.launches[j + 1] == library.launches[j] for j in at)
