@@ -113,9 +113,11 @@ class Kv8Cache:
     k, v      uint8 [num_slots, kv_heads, dim]: e4m3 codes
     k_scale, v_scale  float32 [num_slots / block_tokens, kv_heads]
     The tensors stay the caller's; several layers are several caches. The workspace is made
-    when a call first needs it, one for each stream the cache is used on (make the first call
-    of a shape before a stream capture). Several host threads may call one cache, on one stream
-    too. `status` collects the device status bits of all calls."""
+    when a call first needs it, one for each stream the cache is used on. A call captured by
+    torch.cuda.graph takes it from the graph's pool, so that graphs may be replayed on any
+    streams (a capture made by other means has no such pool: use the binding there, with a
+    workspace for each graph). Several host threads may call one cache, on one stream too.
+    `status` collects the device status bits of all calls."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor, page_size: int, block_tokens: int):
@@ -194,7 +196,7 @@ class Kv8Cache:
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
         with self._lock:
-            ws, ws_bytes = self._workspace(heads, group_rows, handle, stream)
+            ws, ws_bytes, _held = self._workspace(heads, group_rows, handle, stream)
             code = self._lib.kv8_attention(
                 q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim,
                 sm_scale, lens.data_ptr(), max_len, group_rows,
@@ -220,7 +222,7 @@ class Kv8Cache:
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
         with self._lock:
-            ws, ws_bytes = self._workspace(heads, 1, handle, stream)
+            ws, ws_bytes, _held = self._workspace(heads, 1, handle, stream)
             code = self._lib.kv8_attention_selected(
                 q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim,
                 sm_scale, slots.data_ptr(), slots.shape[1], B._ld(slots), self.block_tokens,
@@ -250,15 +252,19 @@ class Kv8Cache:
         return made
 
     def _workspace(self, heads, group_rows, handle, stream):
-        """(pointer, bytes) of the workspace of this stream and these heads."""
+        """(pointer, bytes, tensor) of a workspace for these heads: the stream's, or in a capture
+        one of the graph's own, which the caller holds until the call is enqueued."""
         key = (handle, heads, group_rows)
-        ws = self._workspaces.get(key)
-        if ws is None:
-            n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)
-            with _on(stream):
-                ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
-            self._workspaces[key] = ws = (ws.data_ptr(), n, ws)
-        return ws[:2]
+        with _on(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+            ws = None if capturing else self._workspaces.get(key)
+            if ws is None:
+                n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)
+                t = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+                ws = (t.data_ptr(), n, t)
+                if not capturing:
+                    self._workspaces[key] = ws
+        return ws
 
 
 class KvPages:

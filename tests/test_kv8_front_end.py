@@ -29,6 +29,11 @@ class Torch:
         self.cuda = self.Cuda()
 
     class Cuda:
+        capturing = False
+
+        def is_current_stream_capturing(self):
+            return self.capturing
+
         def __getattr__(self, name):
             return getattr(torch.cuda, name)
 
@@ -137,3 +142,34 @@ def test_page_operations_of_two_threads(library):
     two = [x for x in library.launches if x[0] == "kvpages_reserve"]
     at = [library.launches.index(x) for x in two[::2]]
     assert all(library.launches[j + 1] == library.launches[j] for j in at)
+
+
+def test_a_captured_call_has_a_workspace_of_its_graph(library):
+    """Streams are shared by captures, and graphs are replayed on any: a call in a capture takes
+    memory of the graph's pool, which the call does not keep, and not the stream's workspace."""
+    c, a = cache(), attention_args()
+    q, slots = a[0], dev(torch.zeros((2, 3), dtype=torch.int32))
+
+    def workspace():
+        c.attention(*a)
+        c.attention_selected(q, slots, 0.1)
+        (_, x), (_, y) = library.calls[-2:]
+        return x[-4], y[-4]
+
+    eager = workspace()
+    kept = dict(c._workspaces)
+    api.torch.cuda.capturing = True
+    made = []
+    empty = api.torch.empty
+    api.torch.empty = lambda *x, **k: made.append(empty(*x, **k)) or made[-1]
+    captured = [workspace() for _ in range(2)]
+    assert len({p for pair in captured for p in pair}) == 4  # `made` keeps them apart here
+    assert not {p for pair in captured for p in pair} & set(eager)
+    assert {p for pair in captured for p in pair} <= {t.data_ptr() for t in made}
+    assert c._workspaces == kept
+    api.torch.cuda.capturing = False
+    assert workspace() == eager
+    fresh = cache()
+    api.torch.cuda.capturing = True
+    fresh.attention(*a)  # the first call of a shape
+    assert not fresh._workspaces

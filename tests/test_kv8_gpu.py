@@ -604,6 +604,39 @@ def test_runs_streams_and_graphs_agree():
         assert torch.equal(ref[0], out) and torch.equal(ref[1], lse)
 
 
+def test_graphs_of_one_capture_stream_replayed_on_two():
+    """Two graphs captured on the same stream, with the same heads, share no workspace: replayed
+    side by side and beside eager calls they give what each gives alone."""
+    a, b = (Dense(seed, [30000 + seed], 1, 16, 2, 128, 64, 64, "bf16", poison=False)
+            for seed in (90, 91))
+    h = a.handle()
+    hb = b.handle()
+    args = [(h, a.args()), (hb, b.args())]
+    other = list(a.args())
+    other[0] = other[0].flip(1)
+    args.append((h, other))            # the first cache again, other queries
+    ref = [c.attention(*x) for c, x in args]
+    outs, graphs = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for c, x in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(c.attention(*x))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(50):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = h.attention(*args[0][1])
+        assert torch.equal(eager[0], ref[0][0]) and torch.equal(eager[1], ref[0][1])
+    torch.cuda.synchronize()
+    for got, want in zip(outs, ref):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 code bytes: the pages in use lie at its end."""
     page, hk, dim, block = 64, 8, 128, 64
