@@ -137,7 +137,7 @@ class Kv8Cache:
         self._workspaces = {}
         # held over an attention call: its two launches use the stream's workspace together
         self._lock = threading.Lock()
-        self._heads, self._dim = k.shape[1], k.shape[2]
+        self._heads, self._dim, self._device = k.shape[1], k.shape[2], k.get_device()
         # the cache's part of every call, made once
         self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                       k.shape[0])
@@ -164,14 +164,15 @@ class Kv8Cache:
     def store(self, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
               token_table: torch.Tensor, block_table: torch.Tensor, stream=None) -> None:
         """Quantises k, v [tokens, kv_heads, dim] (bf16 or fp16) into the cache."""
+        _current(self._device)
         tokens = k.shape[0]
         if k.shape != v.shape or k.dtype != v.dtype or k.shape[1:] != self.k.shape[1:]:
             raise ValueError("k and v are [tokens, kv_heads, dim] of one type")
-        _rows(k, "k")
-        _rows(v, "v")
-        _int32(positions, (tokens,), "positions")
-        _int32(token_table, (tokens,), "token_table")
-        _table(block_table)
+        _rows(k, "k", self._device)
+        _rows(v, "v", self._device)
+        _int32(positions, (tokens,), "positions", self._device)
+        _int32(token_table, (tokens,), "token_table", self._device)
+        _table(block_table, self._device)
         code = self._lib.kv8_store(
             k.data_ptr(), B._ld(k), v.data_ptr(), B._ld(v), B._KV8_TYPES[k.dtype], tokens,
             self._heads, self._dim, positions.data_ptr(), token_table.data_ptr(),
@@ -187,12 +188,13 @@ class Kv8Cache:
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Row t of q [rows, q_heads, dim] attends to positions [0, lens[t]) of its
         group's block-table row. Returns (out, lse)."""
-        _rows(q, "q")
+        _current(self._device)
+        _rows(q, "q", self._device)
         rows, heads, dim = q.shape
-        _int32(lens, (rows,), "lens")
-        _table(block_table)
+        _int32(lens, (rows,), "lens", self._device)
+        _table(block_table, self._device)
         if group_table is not None:
-            _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table")
+            _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table", self._device)
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
         with self._lock:
@@ -214,10 +216,11 @@ class Kv8Cache:
                            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Row t of q attends to the slots of slots[t] (int32 [rows, k], negative ones
         skipped): what PagedTopK.select returns. Returns (out, lse)."""
-        _rows(q, "q")
+        _current(self._device)
+        _rows(q, "q", self._device)
         rows, heads, dim = q.shape
         if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != rows
-                or not slots.is_cuda or not _last_contiguous(slots)):
+                or slots.get_device() != self._device or not _last_contiguous(slots)):
             raise ValueError("slots is CUDA int32 [rows, k]")
         handle = B._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
@@ -245,9 +248,9 @@ class Kv8Cache:
         if out is not None:
             if out.shape != q.shape or out.dtype != q.dtype:
                 raise ValueError("out has q's shape and type")
-            _rows(out, "out")
+            _rows(out, "out", self._device)
         if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32
-                                or not lse.is_cuda or not lse.is_contiguous()):
+                                or lse.get_device() != self._device or not lse.is_contiguous()):
             raise ValueError("lse is contiguous CUDA float32 [rows, q_heads]")
         return made
 
@@ -280,11 +283,14 @@ class KvPages:
 
     def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
                  planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
-        _table(block_table)
-        _int32(refs, (refs.numel(),), "refs")
+        self._device = block_table.get_device()
+        _table(block_table, self._device)
+        _int32(refs, (refs.numel(),), "refs", self._device)
         self.block_table, self.refs, self.page_size = block_table, refs, int(page_size)
         self.num_pages = refs.shape[0]
         self.tensors = list(planes)  # keeps the planes' memory alive
+        if any(t.get_device() != self._device for t in self.tensors):
+            raise ValueError("the planes lie on another device than block_table")
         self._planes = B.kvpages_planes(self.tensors, self.num_pages)
         self.max_rows = int(max_rows)
         dev = refs.device
@@ -306,9 +312,10 @@ class KvPages:
     def reserve(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
                 stream=None) -> None:
         """Makes positions [old_lens[i], new_lens[i]) of rows[i] writable."""
+        _current(self._device)
         n = rows.shape[0]
         for t, name in ((rows, "rows"), (old_lens, "old_lens"), (new_lens, "new_lens")):
-            _int32(t, (n,), name)
+            _int32(t, (n,), name, self._device)
         if n > self.max_rows:
             raise ValueError(f"more than max_rows = {self.max_rows} rows")
         with self._lock:
@@ -321,9 +328,10 @@ class KvPages:
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
              stream=None) -> None:
         """children[i] shares the pages of the first lens[i] positions of parents[i]."""
+        _current(self._device)
         n = parents.shape[0]
         for t, name in ((parents, "parents"), (children, "children"), (lens, "lens")):
-            _int32(t, (n,), name)
+            _int32(t, (n,), name, self._device)
         with self._lock:
             code = self._lib.kvpages_fork(
                 parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, *self._table_args,
@@ -333,9 +341,10 @@ class KvPages:
     def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
              stream=None) -> None:
         """rows[i] gives up its pages past the first keep_lens[i] positions (all of them)."""
-        _int32(rows, (rows.shape[0],), "rows")
+        _current(self._device)
+        _int32(rows, (rows.shape[0],), "rows", self._device)
         if keep_lens is not None:
-            _int32(keep_lens, (rows.shape[0],), "keep_lens")
+            _int32(keep_lens, (rows.shape[0],), "keep_lens", self._device)
         with self._lock:
             code = self._lib.kvpages_free(
                 rows.data_ptr(), None if keep_lens is None else keep_lens.data_ptr(),
@@ -347,6 +356,7 @@ class KvPages:
         """Moves the live pages into the lowest ids. Returns (new_ids, counts): the new id
         of each page (-1 of a free one) and {live pages, pages moved}; both are this
         instance's buffers, overwritten by the next call."""
+        _current(self._device)
         with self._lock:
             code = self._lib.kvpages_compact(
                 *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
@@ -356,9 +366,10 @@ class KvPages:
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies page src[i] to page dst[i] in every plane."""
+        _current(self._device)
         n = src.shape[0]
-        _int32(src, (n,), "src")
-        _int32(dst, (n,), "dst")
+        _int32(src, (n,), "src", self._device)
+        _int32(dst, (n,), "dst", self._device)
         with self._lock:
             code = self._lib.kvpages_copy(
                 src.data_ptr(), dst.data_ptr(), n, self.num_pages, *self._plane_args, self._status,
@@ -377,22 +388,24 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
     if tokens.dim() != 2:
         raise ValueError("tokens is int32 [reqs, drafts]")
     reqs, drafts = tokens.shape
-    _int32(tokens, (reqs, drafts), "tokens")
-    if (target.dtype != torch.float32 or target.dim() != 3 or not target.is_cuda
+    device = tokens.get_device()
+    _int32(tokens, (reqs, drafts), "tokens", device)
+    if (target.dtype != torch.float32 or target.dim() != 3 or target.get_device() != device
             or target.shape[0] != reqs or target.shape[1] != drafts + 1
             or not _last_contiguous(target)):
         raise ValueError("target is CUDA float32 [reqs, drafts + 1, vocab]")
     vocab = target.shape[2]
     if draft is not None and (draft.dtype != torch.float32 or draft.shape != (reqs, drafts, vocab)
-                              or not draft.is_cuda or not _last_contiguous(draft)):
+                              or draft.get_device() != device or not _last_contiguous(draft)):
         raise ValueError("draft is CUDA float32 [reqs, drafts, vocab]")
     if (uniforms.dtype != torch.float32 or uniforms.shape != (reqs, drafts + 1)
-            or not uniforms.is_cuda or not uniforms.is_contiguous()):
+            or uniforms.get_device() != device or not uniforms.is_contiguous()):
         raise ValueError("uniforms is contiguous CUDA float32 [reqs, drafts + 1]")
     if n_drafts is not None:
-        _int32(n_drafts, (reqs,), "n_drafts")
+        _int32(n_drafts, (reqs,), "n_drafts", device)
     if status is not None:
-        _int32(status, (1,), "status")
+        _int32(status, (1,), "status", device)
+    _current(device)
     with _on(stream):
         out = torch.empty((reqs, drafts + 1), dtype=torch.int32, device=tokens.device)
         kept = torch.empty((reqs,), dtype=torch.int32, device=tokens.device)
@@ -422,23 +435,32 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-def _int32(t: torch.Tensor, shape, name: str) -> None:
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} is contiguous CUDA int32 {list(shape)}")
+# `device`: the index of the GPU that a handle's (or a call's other) tensors lie on
+def _current(device: int) -> None:
+    if device != torch.cuda.current_device():  # where the library launches
+        raise ValueError(f"the current device is not the tensors' device {device}")
 
 
-def _rows(t: torch.Tensor, name: str) -> None:
+def _int32(t: torch.Tensor, shape, name: str, device: int) -> None:
+    if (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda
+            or t.get_device() != device):
+        raise ValueError(f"{name} is contiguous int32 {list(shape)} on device {device}")
+
+
+def _rows(t: torch.Tensor, name: str, device: int) -> None:
     """[rows, heads, dim] of bf16 / fp16 whose rows may be strided."""
-    if t.dtype not in B._KV8_TYPES or t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} is CUDA bf16 or fp16 [rows, heads, dim]")
+    if t.dtype not in B._KV8_TYPES or t.dim() != 3 or not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} is bf16 or fp16 [rows, heads, dim] on device {device}")
     if t.numel() and (not _last_contiguous(t) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
         raise ValueError(f"{name}: a row's heads are contiguous")
 
 
-def _table(t: torch.Tensor) -> None:
+def _table(t: torch.Tensor, device: int) -> None:
     # table_ld is a row's width as well as its stride
-    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("block_table is contiguous CUDA int32 [n_tables, table_ld]")
+    if (t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda
+            or t.get_device() != device):
+        raise ValueError("block_table is contiguous int32 [n_tables, table_ld] on the handle's "
+                         "device")
 
 
 def _last_contiguous(t: torch.Tensor) -> bool:

@@ -15,11 +15,27 @@ class Device(torch.Tensor):
     """A CPU tensor that says it is on a GPU."""
     __torch_function__ = torch._C._disabled_torch_function_impl
     is_cuda = True
-    device = torch.device("cuda", 0)
+    index = 0
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    def get_device(self):
+        return self.index
+
+
+class Elsewhere(Device):
+    """The same on a second GPU."""
+    index = 1
 
 
 def dev(t):
     return t.as_subclass(Device)
+
+
+def elsewhere(t):
+    return t.as_subclass(Elsewhere)
 
 
 class Torch:
@@ -30,6 +46,10 @@ class Torch:
 
     class Cuda:
         capturing = False
+        index = 0
+
+        def current_device(self):
+            return self.index
 
         def is_current_stream_capturing(self):
             return self.capturing
@@ -173,3 +193,51 @@ def test_a_captured_call_has_a_workspace_of_its_graph(library):
     api.torch.cuda.capturing = True
     fresh.attention(*a)  # the first call of a shape
     assert not fresh._workspaces
+
+
+def each_elsewhere(call, args):
+    """call(*args) is refused with any one tensor of args on another GPU, and works with none."""
+    for i, t in enumerate(args):
+        if isinstance(t, torch.Tensor):
+            with pytest.raises(ValueError):
+                call(*args[:i], elsewhere(t.as_subclass(torch.Tensor)), *args[i + 1:])
+    call(*args)
+
+
+def test_tensors_on_another_device_are_refused(library):
+    c, a = cache(), attention_args()
+    i = lambda *s: dev(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    x = lambda: dev(torch.zeros((3, 2, 64), dtype=torch.bfloat16))  # noqa: E731
+    out, lse = dev(torch.zeros((2, 4, 64), dtype=torch.bfloat16)), dev(torch.zeros(2, 4))
+    each_elsewhere(c.store, (x(), x(), i(3), i(3), i(1, 2)))
+    each_elsewhere(c.attention, (*a, 1, i(2), out, lse))
+    each_elsewhere(c.attention_selected, (a[0], i(2, 5), 0.1, out, lse))
+    codes = lambda: dev(torch.zeros((64, 2, 64), dtype=torch.uint8))  # noqa: E731
+    ones = lambda: dev(torch.ones(4, 2))  # noqa: E731
+    each_elsewhere(S.Kv8Cache, (codes(), codes(), ones(), ones(), 32, 16))
+    p = pages()
+    each_elsewhere(p.reserve, (i(2), i(2), i(2)))
+    each_elsewhere(p.fork, (i(2), i(2), i(2)))
+    each_elsewhere(p.free, (i(2), i(2)))
+    each_elsewhere(p.copy, (i(2), i(2)))
+    each_elsewhere(lambda t, r, x, y: S.KvPages(t, r, 16, [x, y]),
+                   (i(4, 2), i(8), dev(torch.zeros(8, 16)), dev(torch.zeros(8, 4))))
+    f = lambda *s: dev(torch.zeros(s))  # noqa: E731
+    each_elsewhere(S.verify_drafts, (f(2, 3, 10), f(2, 2, 10), i(2, 2), f(2, 3), i(2), i(1)))
+
+
+def test_another_current_device_is_refused(library):
+    """The library launches on the current device."""
+    c, a, p = cache(), attention_args(), pages()
+    i = lambda *s: dev(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    x = dev(torch.zeros((3, 2, 64), dtype=torch.bfloat16))
+    f = lambda *s: dev(torch.zeros(s))  # noqa: E731
+    api.torch.cuda.index = 1
+    for call in (lambda: c.store(x, x, i(3), i(3), i(1, 2)), lambda: c.attention(*a),
+                 lambda: c.attention_selected(a[0], i(2, 5), 0.1),
+                 lambda: p.reserve(i(2), i(2), i(2)), lambda: p.fork(i(2), i(2), i(2)),
+                 lambda: p.free(i(2)), lambda: p.compact(), lambda: p.copy(i(2), i(2)),
+                 lambda: S.verify_drafts(f(2, 3, 10), None, i(2, 2), f(2, 3))):
+        with pytest.raises(ValueError):
+            call()
+    assert not library.calls
