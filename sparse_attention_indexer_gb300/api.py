@@ -107,7 +107,24 @@ class HostPagedTopK:
         return self.out_host
 
 
-class Kv8Cache:
+class _Handle:
+    """The buffers that a handle makes for itself, and the streams that use them."""
+
+    def _own(self, *tensors: torch.Tensor) -> None:
+        self._buffers, self._streams = tensors, {B._stream(None)}
+
+    def _stream(self, stream) -> Optional[int]:
+        """The stream's handle. The buffers come from the pool of the stream they were made on,
+        which must not give them out again while another one still works on them."""
+        handle = B._stream(stream)
+        if handle not in self._streams:
+            for t in self._buffers:
+                t.record_stream(_torch_stream(stream))
+            self._streams.add(handle)
+        return handle
+
+
+class Kv8Cache(_Handle):
     """A paged K/V cache in 8 bits and the attention over it (include/kv8_attention.h).
 
     k, v      uint8 [num_slots, kv_heads, dim]: e4m3 codes
@@ -134,6 +151,7 @@ class Kv8Cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_size, self.block_tokens = int(page_size), int(block_tokens)
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._own(self.status)
         self._workspaces = {}
         # held over an attention call: its two launches use the stream's workspace together
         self._lock = threading.Lock()
@@ -177,7 +195,7 @@ class Kv8Cache:
             k.data_ptr(), B._ld(k), v.data_ptr(), B._ld(v), B._KV8_TYPES[k.dtype], tokens,
             self._heads, self._dim, positions.data_ptr(), token_table.data_ptr(),
             block_table.data_ptr(), block_table.shape[0], block_table.shape[1], self.page_size,
-            self.block_tokens, *self._args, self.status.data_ptr(), B._stream(stream))
+            self.block_tokens, *self._args, self.status.data_ptr(), self._stream(stream))
         if code < 0:
             raise B.Kv8Error(code, "kv8_store")
 
@@ -195,7 +213,7 @@ class Kv8Cache:
         _table(block_table, self._device)
         if group_table is not None:
             _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table", self._device)
-        handle = B._stream(stream)
+        handle = self._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
         with self._lock:
             ws, ws_bytes, _held = self._workspace(heads, group_rows, handle, stream)
@@ -222,7 +240,7 @@ class Kv8Cache:
         if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != rows
                 or slots.get_device() != self._device or not _last_contiguous(slots)):
             raise ValueError("slots is CUDA int32 [rows, k]")
-        handle = B._stream(stream)
+        handle = self._stream(stream)
         out, lse = self._outputs(q, out, lse, stream)
         with self._lock:
             ws, ws_bytes, _held = self._workspace(heads, 1, handle, stream)
@@ -270,7 +288,7 @@ class Kv8Cache:
         return ws
 
 
-class KvPages:
+class KvPages(_Handle):
     """Ownership of the pages of one or more paged tensors (include/kv_pages.h).
 
     block_table  int32 [n_tables, table_ld]: -1 where a sequence has no page
@@ -278,8 +296,8 @@ class KvPages:
     planes       the tensors that hold the pages' data, each [num_pages, ...]
     max_rows     the most rows that one reserve names
     All stay the caller's and are changed in place. One instance serves one stream at a
-    time; several host threads may call it there. `status` collects the device status bits of
-    all calls."""
+    time (the replays of a graph that captured its calls among them); several host threads may
+    call it there. `status` collects the device status bits of all calls."""
 
     def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
                  planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
@@ -299,6 +317,7 @@ class KvPages:
         self.new_ids = torch.empty(self.num_pages, dtype=torch.int32, device=dev)
         self.counts = torch.zeros(2, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._own(self.workspace, self.new_ids, self.counts, self.status)
         # the state's part of the calls, made once
         self._table_args = (block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
         self._pool_args = (refs.data_ptr(), self.num_pages)
@@ -322,7 +341,7 @@ class KvPages:
             code = self._lib.kvpages_reserve(
                 rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
                 self.page_size, *self._pool_args, *self._plane_args, *self._ws_args, self._status,
-                B._stream(stream))
+                self._stream(stream))
         B._kvp(code, "kvpages_reserve")
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
@@ -335,7 +354,7 @@ class KvPages:
         with self._lock:
             code = self._lib.kvpages_fork(
                 parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, *self._table_args,
-                self.page_size, *self._pool_args, self._status, B._stream(stream))
+                self.page_size, *self._pool_args, self._status, self._stream(stream))
         B._kvp(code, "kvpages_fork")
 
     def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
@@ -349,7 +368,7 @@ class KvPages:
             code = self._lib.kvpages_free(
                 rows.data_ptr(), None if keep_lens is None else keep_lens.data_ptr(),
                 rows.shape[0], *self._table_args, self.page_size, *self._pool_args, self._status,
-                B._stream(stream))
+                self._stream(stream))
         B._kvp(code, "kvpages_free")
 
     def compact(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -360,7 +379,7 @@ class KvPages:
         with self._lock:
             code = self._lib.kvpages_compact(
                 *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
-                self.counts.data_ptr(), *self._ws_args, self._status, B._stream(stream))
+                self.counts.data_ptr(), *self._ws_args, self._status, self._stream(stream))
         B._kvp(code, "kvpages_compact")
         return self.new_ids, self.counts
 
@@ -373,7 +392,7 @@ class KvPages:
         with self._lock:
             code = self._lib.kvpages_copy(
                 src.data_ptr(), dst.data_ptr(), n, self.num_pages, *self._plane_args, self._status,
-                B._stream(stream))
+                self._stream(stream))
         B._kvp(code, "kvpages_copy")
 
 
@@ -426,13 +445,16 @@ _HERE = contextlib.nullcontext()
 
 def _on(stream):
     """Memory for work on `stream` comes from that stream's pool."""
+    return _HERE if stream is None else torch.cuda.stream(_torch_stream(stream))
+
+
+def _torch_stream(stream):
+    """The torch stream of a `stream` argument."""
     if stream is None:
-        return _HERE
-    if not isinstance(stream, torch.cuda.Stream):
-        if not int(stream):
-            return torch.cuda.stream(torch.cuda.default_stream())
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+        return torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 # `device`: the index of the GPU that a handle's (or a call's other) tensors lie on

@@ -1,6 +1,7 @@
 """What the tensor-level front end of the 8-bit cache and the pages does around the library's
 calls, on the CPU: the library is a stand-in that records how it is called, and CPU tensors
 that say they are on a GPU stand for device memory."""
+import contextlib
 import threading
 import time
 
@@ -23,6 +24,12 @@ class Device(torch.Tensor):
 
     def get_device(self):
         return self.index
+
+    def record_stream(self, stream):
+        recorded.append((self.data_ptr(), stream))
+
+
+recorded = []
 
 
 class Elsewhere(Device):
@@ -50,6 +57,18 @@ class Torch:
 
         def current_device(self):
             return self.index
+
+        def ExternalStream(self, handle):
+            return handle
+
+        def current_stream(self):
+            return 7
+
+        def default_stream(self):
+            return 0
+
+        def stream(self, stream):
+            return contextlib.nullcontext()
 
         def is_current_stream_capturing(self):
             return self.capturing
@@ -97,7 +116,7 @@ class Library:
 def library(monkeypatch):
     lib = Library()
     monkeypatch.setattr(api.B, "lib", lambda: lib)
-    monkeypatch.setattr(api.B, "_stream", lambda s: 7)
+    monkeypatch.setattr(api.B, "_stream", lambda s: 7 if s is None else s or None)
     monkeypatch.setattr(api, "torch", Torch())
     return lib
 
@@ -241,3 +260,35 @@ def test_another_current_device_is_refused(library):
         with pytest.raises(ValueError):
             call()
     assert not library.calls
+
+
+def test_a_handles_own_buffers_are_recorded_on_the_streams_it_serves(library):
+    """They come from the pool of the stream that the handle was made on, which would give them
+    out again while another stream's work is on its way."""
+    i = lambda *s: dev(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    c, a, p = cache(), attention_args(), pages()
+    x = dev(torch.zeros((3, 2, 64), dtype=torch.bfloat16))
+    buffers = [t.data_ptr() for t in (p.workspace, p.new_ids, p.counts, p.status)]
+    recorded.clear()
+    p.reserve(i(2), i(2), i(2))
+    c.store(x, x, i(3), i(3), i(1, 2))
+    c.attention(*a)
+    assert not recorded
+    for call in (lambda s: p.reserve(i(2), i(2), i(2), stream=s), lambda s: p.compact(stream=s),
+                 lambda s: p.free(i(2), stream=s), lambda s: p.copy(i(2), i(2), stream=s),
+                 lambda s: p.fork(i(2), i(2), i(2), stream=s)):
+        p = pages()
+        buffers = [t.data_ptr() for t in (p.workspace, p.new_ids, p.counts, p.status)]
+        for stream in (9, 9, 0, 7):
+            call(stream)
+        assert sorted(recorded, key=str) == sorted([(b, s) for b in buffers for s in (9, 0)], key=str)
+        recorded.clear()
+    for call in (lambda s: c.store(x, x, i(3), i(3), i(1, 2), stream=s),
+                 lambda s: c.attention(*a, stream=s),
+                 lambda s: c.attention_selected(a[0], i(2, 5), 0.1, stream=s)):
+        c = cache()
+        call(9)
+        call(9)
+        call(7)
+        assert recorded == [(c.status.data_ptr(), 9)]
+        recorded.clear()

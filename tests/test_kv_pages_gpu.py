@@ -255,3 +255,25 @@ def test_captured_in_a_graph():
         KP.fork([0] * 3, [1, 2, 3], [100] * 3, b.table, 16, b.refs)
         KP.reserve([1, 2, 3], [100] * 3, [101] * 3, b.table, 16, b.refs, b.planes)
         b.same(0)
+
+
+def test_a_pool_dropped_while_another_stream_works():
+    """The instance's buffers are not given out again while work of its stream is on its way."""
+    b = Both(13, 6, 8, 64, 16)
+    b.up()
+    api, s = b.api, torch.cuda.Stream()
+    buffers = {(t.numel(), t.dtype, t.data_ptr())
+               for t in (api.workspace, api.new_ids, api.counts, api.status)}
+    table, refs = api.block_table, api.refs
+    rows, old, new = b.i([0, 1]), b.i([0, 0]), b.i([40, 100])
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        api.reserve(rows, old, new)
+    b.api = api = None
+    held = [torch.empty(n, dtype=t, device="cuda") for n, t, _ in buffers for _ in range(3)]
+    working = not s.query()
+    assert not working or not {t.data_ptr() for t in held} & {at for _, _, at in buffers}
+    torch.cuda.synchronize()
+    KP.reserve([0, 1], [0, 0], [40, 100], b.table, 16, b.refs, b.planes)
+    assert np.array_equal(table.cpu().numpy(), b.table) and np.array_equal(refs.cpu().numpy(), b.refs)
