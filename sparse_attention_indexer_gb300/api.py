@@ -108,15 +108,18 @@ class HostPagedTopK:
 
 
 class _Handle:
-    """The buffers that a handle makes for itself, and the streams that use them."""
+    """The buffers that a handle makes for itself, and the device and streams that it serves."""
 
-    def _own(self, *tensors: torch.Tensor) -> None:
-        self._buffers, self._streams = tensors, {B._stream(None)}
+    def _own(self, device: int, *tensors: torch.Tensor) -> None:
+        self._device, self._buffers, self._streams = device, tensors, {B._stream(None)}
 
     def _stream(self, stream) -> Optional[int]:
-        """The stream's handle. The buffers come from the pool of the stream they were made on,
-        which must not give them out again while another one still works on them."""
-        handle = B._stream(stream)
+        """The raw stream of a call. The buffers come from the pool of the stream they were made
+        on, which must not give them out again while another one still works on them."""
+        device = _current_device()
+        if device != self._device:  # the library launches on the current device
+            raise ValueError(f"the current device is not the handle's, {self._device}")
+        handle = B._stream(stream) if stream is not None else _raw_stream(device) or None
         if handle not in self._streams:
             for t in self._buffers:
                 t.record_stream(_torch_stream(stream))
@@ -151,11 +154,11 @@ class Kv8Cache(_Handle):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_size, self.block_tokens = int(page_size), int(block_tokens)
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._own(self.status)
+        self._own(k.get_device(), self.status)
         self._workspaces = {}
         # held over an attention call: its two launches use the stream's workspace together
         self._lock = threading.Lock()
-        self._heads, self._dim, self._device = k.shape[1], k.shape[2], k.get_device()
+        self._heads, self._dim = k.shape[1], k.shape[2]
         # the cache's part of every call, made once
         self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                       k.shape[0])
@@ -182,7 +185,6 @@ class Kv8Cache(_Handle):
     def store(self, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
               token_table: torch.Tensor, block_table: torch.Tensor, stream=None) -> None:
         """Quantises k, v [tokens, kv_heads, dim] (bf16 or fp16) into the cache."""
-        _current(self._device)
         tokens = k.shape[0]
         if k.shape != v.shape or k.dtype != v.dtype or k.shape[1:] != self.k.shape[1:]:
             raise ValueError("k and v are [tokens, kv_heads, dim] of one type")
@@ -206,7 +208,6 @@ class Kv8Cache(_Handle):
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Row t of q [rows, q_heads, dim] attends to positions [0, lens[t]) of its
         group's block-table row. Returns (out, lse)."""
-        _current(self._device)
         _rows(q, "q", self._device)
         rows, heads, dim = q.shape
         _int32(lens, (rows,), "lens", self._device)
@@ -234,7 +235,6 @@ class Kv8Cache(_Handle):
                            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Row t of q attends to the slots of slots[t] (int32 [rows, k], negative ones
         skipped): what PagedTopK.select returns. Returns (out, lse)."""
-        _current(self._device)
         _rows(q, "q", self._device)
         rows, heads, dim = q.shape
         if (slots.dtype != torch.int32 or slots.dim() != 2 or slots.shape[0] != rows
@@ -275,17 +275,19 @@ class Kv8Cache(_Handle):
     def _workspace(self, heads, group_rows, handle, stream):
         """(pointer, bytes, tensor) of a workspace for these heads: the stream's, or in a capture
         one of the graph's own, which the caller holds until the call is enqueued."""
-        key = (handle, heads, group_rows)
         with _on(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-            ws = None if capturing else self._workspaces.get(key)
-            if ws is None:
-                n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)
-                t = torch.empty(n, dtype=torch.uint8, device=self.k.device)
-                ws = (t.data_ptr(), n, t)
-                if not capturing:
-                    self._workspaces[key] = ws
-        return ws
+            if not _capturing():
+                key = (handle, heads, group_rows)
+                ws = self._workspaces.get(key)
+                if ws is None:
+                    ws = self._workspaces[key] = self._new_workspace(heads, group_rows)
+                return ws
+            return self._new_workspace(heads, group_rows)
+
+    def _new_workspace(self, heads, group_rows):
+        n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)
+        t = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+        return t.data_ptr(), n, t
 
 
 class KvPages(_Handle):
@@ -301,13 +303,15 @@ class KvPages(_Handle):
 
     def __init__(self, block_table: torch.Tensor, refs: torch.Tensor, page_size: int,
                  planes: Sequence[torch.Tensor] = (), max_rows: int = 1024):
-        self._device = block_table.get_device()
-        _table(block_table, self._device)
-        _int32(refs, (refs.numel(),), "refs", self._device)
+        if not block_table.is_cuda:
+            raise ValueError("block_table is a CUDA tensor")
+        device = block_table.get_device()
+        _table(block_table, device)
+        _int32(refs, (refs.numel(),), "refs", device)
         self.block_table, self.refs, self.page_size = block_table, refs, int(page_size)
         self.num_pages = refs.shape[0]
         self.tensors = list(planes)  # keeps the planes' memory alive
-        if any(t.get_device() != self._device for t in self.tensors):
+        if any(t.get_device() != device for t in self.tensors):
             raise ValueError("the planes lie on another device than block_table")
         self._planes = B.kvpages_planes(self.tensors, self.num_pages)
         self.max_rows = int(max_rows)
@@ -317,7 +321,7 @@ class KvPages(_Handle):
         self.new_ids = torch.empty(self.num_pages, dtype=torch.int32, device=dev)
         self.counts = torch.zeros(2, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._own(self.workspace, self.new_ids, self.counts, self.status)
+        self._own(device, self.workspace, self.new_ids, self.counts, self.status)
         # the state's part of the calls, made once
         self._table_args = (block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
         self._pool_args = (refs.data_ptr(), self.num_pages)
@@ -331,7 +335,6 @@ class KvPages(_Handle):
     def reserve(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
                 stream=None) -> None:
         """Makes positions [old_lens[i], new_lens[i]) of rows[i] writable."""
-        _current(self._device)
         n = rows.shape[0]
         for t, name in ((rows, "rows"), (old_lens, "old_lens"), (new_lens, "new_lens")):
             _int32(t, (n,), name, self._device)
@@ -347,7 +350,6 @@ class KvPages(_Handle):
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
              stream=None) -> None:
         """children[i] shares the pages of the first lens[i] positions of parents[i]."""
-        _current(self._device)
         n = parents.shape[0]
         for t, name in ((parents, "parents"), (children, "children"), (lens, "lens")):
             _int32(t, (n,), name, self._device)
@@ -360,7 +362,6 @@ class KvPages(_Handle):
     def free(self, rows: torch.Tensor, keep_lens: Optional[torch.Tensor] = None,
              stream=None) -> None:
         """rows[i] gives up its pages past the first keep_lens[i] positions (all of them)."""
-        _current(self._device)
         _int32(rows, (rows.shape[0],), "rows", self._device)
         if keep_lens is not None:
             _int32(keep_lens, (rows.shape[0],), "keep_lens", self._device)
@@ -375,7 +376,6 @@ class KvPages(_Handle):
         """Moves the live pages into the lowest ids. Returns (new_ids, counts): the new id
         of each page (-1 of a free one) and {live pages, pages moved}; both are this
         instance's buffers, overwritten by the next call."""
-        _current(self._device)
         with self._lock:
             code = self._lib.kvpages_compact(
                 *self._table_args, *self._pool_args, *self._plane_args, self.new_ids.data_ptr(),
@@ -385,7 +385,6 @@ class KvPages(_Handle):
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies page src[i] to page dst[i] in every plane."""
-        _current(self._device)
         n = src.shape[0]
         _int32(src, (n,), "src", self._device)
         _int32(dst, (n,), "dst", self._device)
@@ -404,8 +403,8 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
     drafts + 1, vocab], draft float32 [reqs, drafts, vocab] or None (point masses), tokens
     int32 [reqs, drafts], uniforms float32 [reqs, drafts + 1]. Returns (out_tokens [reqs,
     drafts + 1], kept [reqs]): the kept drafts, one drawn token, then -1."""
-    if tokens.dim() != 2:
-        raise ValueError("tokens is int32 [reqs, drafts]")
+    if tokens.dim() != 2 or not tokens.is_cuda:
+        raise ValueError("tokens is CUDA int32 [reqs, drafts]")
     reqs, drafts = tokens.shape
     device = tokens.get_device()
     _int32(tokens, (reqs, drafts), "tokens", device)
@@ -424,7 +423,8 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
         _int32(n_drafts, (reqs,), "n_drafts", device)
     if status is not None:
         _int32(status, (1,), "status", device)
-    _current(device)
+    if device != _current_device():  # where the library launches
+        raise ValueError(f"the current device is not the tensors', {device}")
     with _on(stream):
         out = torch.empty((reqs, drafts + 1), dtype=torch.int32, device=tokens.device)
         kept = torch.empty((reqs,), dtype=torch.int32, device=tokens.device)
@@ -441,6 +441,10 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
 
 
 _HERE = contextlib.nullcontext()
+# without the calls of Python between: they are asked for at each call of an operator
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _on(stream):
@@ -458,20 +462,15 @@ def _torch_stream(stream):
 
 
 # `device`: the index of the GPU that a handle's (or a call's other) tensors lie on
-def _current(device: int) -> None:
-    if device != torch.cuda.current_device():  # where the library launches
-        raise ValueError(f"the current device is not the tensors' device {device}")
-
-
 def _int32(t: torch.Tensor, shape, name: str, device: int) -> None:
-    if (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda
+    if (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
             or t.get_device() != device):
         raise ValueError(f"{name} is contiguous int32 {list(shape)} on device {device}")
 
 
 def _rows(t: torch.Tensor, name: str, device: int) -> None:
     """[rows, heads, dim] of bf16 / fp16 whose rows may be strided."""
-    if t.dtype not in B._KV8_TYPES or t.dim() != 3 or not t.is_cuda or t.get_device() != device:
+    if t.dtype not in B._KV8_TYPES or t.dim() != 3 or t.get_device() != device:
         raise ValueError(f"{name} is bf16 or fp16 [rows, heads, dim] on device {device}")
     if t.numel() and (not _last_contiguous(t) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
         raise ValueError(f"{name}: a row's heads are contiguous")
@@ -479,7 +478,7 @@ def _rows(t: torch.Tensor, name: str, device: int) -> None:
 
 def _table(t: torch.Tensor, device: int) -> None:
     # table_ld is a row's width as well as its stride
-    if (t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda
+    if (t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous()
             or t.get_device() != device):
         raise ValueError("block_table is contiguous int32 [n_tables, table_ld] on the handle's "
                          "device")

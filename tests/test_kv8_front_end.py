@@ -118,6 +118,9 @@ def library(monkeypatch):
     monkeypatch.setattr(api.B, "lib", lambda: lib)
     monkeypatch.setattr(api.B, "_stream", lambda s: 7 if s is None else s or None)
     monkeypatch.setattr(api, "torch", Torch())
+    monkeypatch.setattr(api, "_raw_stream", lambda device: 7)
+    monkeypatch.setattr(api, "_current_device", lambda: api.torch.cuda.index)
+    monkeypatch.setattr(api, "_capturing", lambda: api.torch.cuda.capturing)
     return lib
 
 
