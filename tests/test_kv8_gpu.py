@@ -247,6 +247,17 @@ class Dense:
         return out, lse, st
 
 
+def check_rows(d, rows):
+    """Dense.check without the references of the other rows."""
+    h = d.handle()
+    out, lse = h.attention(*d.args())
+    for r in rows:
+        ref, st = d.ref(r)
+        assert st == 0
+        close(out[r].double().cpu().numpy(), lse[r].double().cpu().numpy(), ref, d.dtype, f"row {r}")
+    assert int(h.status.item()) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("page,block", [(16, 16), (64, 64), (64, 16), (48, 16), (128, 32), (80, 80)])
@@ -383,6 +394,40 @@ def test_scales_far_apart(dtype):
     Dense(13, [500, 64, 100, 1000], 1, 8, 2, 128, 64, 16, dtype, wide=True).check()
 
 
+# Variants of units of 8 and 16 rows (a warp to a CTA) and of 32, 64 and 128 (four): (query heads, key
+# heads, group, dim)
+UNITS = [(2, 2, 1, 64), (32, 8, 1, 128), (30, 2, 1, 128), (16, 2, 4, 64), (16, 1, 4, 128),
+         (16, 1, 8, 64)]
+
+
+@pytest.mark.parametrize("hq,hk,group,dim", UNITS)
+def test_more_units_than_the_list_of_shared_ones(hq, hk, group, dim):
+    """From 2049 (group, key head) units on, a shared unit is kept by the CTA it starts in: long
+    rows that several CTAs share, beside one another and not, empty rows, the last row long."""
+    groups = 2400 // hk
+    rng = np.random.default_rng(hq + group)
+    lens = rng.integers(0, 50, groups * group)
+    long = [0, 1, 2, groups // 3, groups // 2, groups // 2 + 2, groups - 1]
+    for g, n in zip(long, (9000, 4000, 3333, 700, 12000, 2500, 5000)):
+        lens[g * group:(g + 1) * group] = np.maximum(0, n - np.arange(group)[::-1])
+    lens[(groups // 2 + 1) * group:(groups // 2 + 2) * group] = 0
+    d = Dense(100 + hq + group, lens.tolist(), group, hq, hk, dim, 32, 16, "bf16")
+    check_rows(d, sorted({g * group + i for g in long + [groups // 2 + 1] for i in (0, group - 1)}
+                         | set(range(0, groups * group, 61 * group))))
+
+
+@pytest.mark.parametrize("groups", [2047, 2048, 2049])
+@pytest.mark.parametrize("hq,group", [(4, 1), (16, 4)])
+def test_units_around_the_list_of_shared_ones(groups, hq, group):
+    lens = np.random.default_rng(groups).integers(0, 40, groups * group)
+    long = [0, 1000, groups - 2, groups - 1]
+    for g, n in zip(long, (8000, 3000, 6000, 1500)):
+        lens[g * group:(g + 1) * group] = n
+    d = Dense(110 + group, lens.tolist(), group, hq, 1, 64, 32, 16, "fp16")
+    check_rows(d, sorted({g * group for g in long} | set(range(0, groups * group, 97 * group))
+                         | {groups * group - 1}))
+
+
 def test_peaked_and_flat_rows():
     Dense(14, [400, 300], 1, 8, 2, 128, 64, 64, "bf16", q_gain=40.0).check()
     Dense(15, [400, 300], 1, 8, 2, 128, 64, 64, "fp16", q_gain=0.0).check()
@@ -425,17 +470,6 @@ def one_table(seed, rows, length, group, hq, hk, dim, block=16):
     d.lens = np.full(rows, length, np.int32)
     d.group_table = np.zeros(-(-rows // group), np.int32)
     return d
-
-
-def check_rows(d, rows):
-    """Dense.check without the references of the other rows."""
-    h = d.handle()
-    out, lse = h.attention(*d.args())
-    for r in rows:
-        ref, st = d.ref(r)
-        assert st == 0
-        close(out[r].double().cpu().numpy(), lse[r].double().cpu().numpy(), ref, d.dtype, f"row {r}")
-    assert int(h.status.item()) == 0
 
 
 # (rows, keys, group, query heads, key heads, dim) that give a warp about 100 tiles of a row: a warp
@@ -514,6 +548,23 @@ def test_nan_seen_by_the_later_rows_alone(dim, hq):
     for r in (0, 1):
         close(o[r], l[r] * 0 + d.ref(r)[0][1], d.ref(r)[0], "bf16", f"row {r}")
     assert np.isnan(o[2:]).all()
+
+
+@pytest.mark.parametrize("dim,hq", [(64, 8), (128, 8), (128, 32)])
+def test_scales_that_are_nan_past_the_end_of_a_row(dim, hq):
+    """The block after a row's last key has NaN scales, which the rows behind it see: outputs and lse
+    of the rows before are as without it."""
+    d = Dense(26, [96, 90, 97, 100], 4, hq, 2, dim, 64, 16, "bf16", poison=False)
+    slot = K8.row_slots(d.table, 0, 100, 100, 64, d.cache[0].shape[0])[0]
+    want = [d.ref(r)[0] for r in (0, 1)]
+    for which in (3, 2):
+        d.cache[which][slot[96] // 16] = np.nan
+        out, lse = d.handle().attention(*d.args())
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for r in (0, 1):
+            close(o[r], l[r], want[r], "bf16", f"row {r}")
+        assert np.isnan(o[2:]).all()
+        assert np.isnan(l[2:]).all() == (which == 2)
 
 
 def test_nan_and_infinite_queries():
@@ -730,6 +781,23 @@ def test_selected_nothing_and_strides():
 
 def test_selected_rows_many():
     check_selected(*selected_case(34, 300, 33, 4, 1, 64, 32, "fp16"), "fp16")
+
+
+@pytest.mark.parametrize("rows,hq,hk,dim,k", [
+    (1100, 4, 2, 64, 33), (300, 32, 8, 128, 100), (2500, 16, 1, 64, 5), (2060, 1, 1, 128, 0),
+    (2049, 2, 1, 128, 1), (2048, 2, 1, 128, 70), (2047, 2, 1, 64, 70)])
+def test_selected_more_units_than_the_list_of_shared_ones(rows, hq, hk, dim, k):
+    rng = np.random.default_rng(rows)
+    cache, slots, q, block, scale = selected_case(37, rows, k, hq, hk, dim, 16, "bf16")
+    slots[rng.random(slots.shape) < 0.2] = -1
+    slots[::50] = -1
+    h = Kv8Cache(*[torch.from_numpy(x).to(DEV) for x in cache], block, block)
+    out, lse = h.attention_selected(q, torch.from_numpy(slots).to(DEV), scale)
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for r in sorted(set(range(0, rows, 23)) | {50, rows - 2, rows - 1}):
+        ref = K8.attend(K8.values(bits(q[r]), "bf16"), slots[r][slots[r] >= 0], *cache, block, scale)
+        close(o[r], l[r], ref, "bf16", f"row {r}")
+    assert int(h.status.item()) == 0
 
 
 @pytest.mark.parametrize("hq,dim", [(2, 128), (24, 64)])
