@@ -35,9 +35,12 @@
 //     fp16: w' = 2^(x - m) * sv * 2^-d, m the row's maximum, which is raised only when an x
 //     passes it by 4 (in most tiles none does, and no lane asks another). While the scales
 //     met so far lie within 2^8 of each other, one d for all rows keeps the row's largest w'
-//     in [1, 2^13), and fp16 holds what is 2^-24 of it; else d is chosen per row so that
-//     the largest w' is about 1. Where a tile has one key and one value scale, they come
-//     out of the sums.
+//     in [1, 2^13), and fp16 holds what is 2^-24 of it; else (a scale of 0 counts as the
+//     least) d is chosen per row so that the largest w' is about 1. Where a tile has one key
+//     and one value scale, they come out of the sums. fp16 is what the products take in one
+//     pass: the rounding, 2^-11 of a weight at most, has no direction. It leaves bf16 outputs
+//     as far from the exact ones as fp32 weights do (relative error 1.7e-3), fp16 outputs of
+//     32 ragged rows at 3.1e-4 in place of 2.1e-4. Maxima, sums and joins are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
