@@ -24,12 +24,12 @@
  * kv8_attention takes p over positions [0, lens[t]) through a block table, for decode
  * steps and for verify steps of up to 8 query rows per request; kv8_attention_selected
  * takes p over a list of slots per query row (the out_slots of topk_select_paged),
- * skipping negative ones. A row that attends to
- * nothing gives out 0 and lse -infinity. What lies at positions that a row does not
- * attend to, NaN codes and scales among it, never reaches its result. Scales must be
- * >= 0. Scores, softmax statistics and sums are fp32; the weights exp(..) are rounded
- * to fp16 relative to the row's largest weight * value scale. The result does not
- * depend on the run (no floating-point atomics).
+ * skipping negative ones. A row that attends to nothing gives out 0 and lse -infinity.
+ * What lies at positions that a row does not attend to, NaN codes and scales among it,
+ * never reaches its result. Scales must be >= 0. Scores, softmax statistics and sums are
+ * fp32; the weights exp(..) are rounded to fp16 relative to the row's largest weight *
+ * value scale. A weight, or weight * value scale, below 2^-120 of the row's largest weight
+ * may count as 0. The result does not depend on the run (no floating-point atomics).
  */
 #ifndef KV8_ATTENTION_H
 #define KV8_ATTENTION_H
