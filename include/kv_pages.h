@@ -1,4 +1,5 @@
-/* Ownership and data of the pages of a paged cache: reserve, fork, free, compact, copy.
+/* Ownership and data of the pages of a paged cache: reserve, fork, free, compact, copy; and
+ * what a step needs to know of them: its tokens' places, and the prefixes that rows share.
  *
  * State, all on the device and owned by the caller:
  *   block_table  int32 [n_tables, table_ld]: row t holds the page ids of one sequence,
@@ -63,10 +64,12 @@ enum {
   KVPAGES_STATUS_PAGE = 4,      /* a page id >= num_pages (or a pair's id < 0 on one side
                                    only): that entry is skipped */
   KVPAGES_STATUS_NO_PAGE = 8,   /* reserve: too few free pages for a row; it and the rows
-                                   named after it that need pages get none */
+                                   named after it that need pages get none; step: a
+                                   position without a page: its slot is -1 */
   KVPAGES_STATUS_CHILD = 16,    /* fork: the child row still holds pages: skipped */
-  KVPAGES_STATUS_REFS = 32      /* free: a page without an owner: its count stays; compact:
+  KVPAGES_STATUS_REFS = 32,     /* free: a page without an owner: its count stays; compact:
                                    a table entry that names a free page: left as it is */
+  KVPAGES_STATUS_TOKENS = 64    /* step: more tokens than places: the last ones have none */
 };
 
 /* Bytes of device workspace for reserve and compact (pure). 0 for invalid arguments. */
@@ -110,6 +113,40 @@ int kvpages_compact(int32_t* block_table, int n_tables, int64_t table_ld, int32_
 int kvpages_copy(const int32_t* src, const int32_t* dst, int n, int num_pages,
                  const kvpages_plane* planes, int n_planes, int32_t* status,
                  kvpages_stream_t stream);
+
+/* The places of a step's new tokens. Request i (row rows[i]) brings positions [old_lens[i],
+ * new_lens[i]); the tokens stand one after another in the order of the requests, token t of
+ * request i from starts[i] on. With pos its position:
+ *   positions    device int32 [tokens] (written): pos
+ *   token_table  device int32 [tokens] (written): rows[i], as kv8_store, indexer_k_prologue and
+ *                (for rows of one query) kv8_attention's group_table take it
+ *   slots        device int32 [tokens] (written): table[rows[i]][pos / page_size] * page_size +
+ *                pos % page_size; -1 where the entry is negative (KVPAGES_STATUS_NO_PAGE) or
+ *                not below num_pages (KVPAGES_STATUS_PAGE)
+ *   lens         device int32 [tokens] (written): pos + 1, what a causal query row sees
+ *   starts       device int32 [n + 1] (written): min(tokens, tokens of the requests before)
+ * `tokens` is the number of places, for graphs a bound on the step's tokens: the places behind
+ * the last token hold -1, -1, -1 and 0 (an attention row of length 0 attends to nothing; a
+ * store skips a token of row -1 and sets its status bit for that). A request that fails a
+ * check brings no tokens. num_pages * page_size < 2^31. One launch. */
+int kvpages_step(const int32_t* rows, const int32_t* old_lens, const int32_t* new_lens, int n,
+                 const int32_t* block_table, int n_tables, int64_t table_ld, int page_size,
+                 int num_pages, int tokens, int32_t* positions, int32_t* token_table,
+                 int32_t* slots, int32_t* lens, int32_t* starts, int32_t* status,
+                 kvpages_stream_t stream);
+
+/* How long a prefix the rows of each set share. Set s is the requests set_starts[s] ..
+ * set_starts[s + 1] - 1 of (rows[i], lens[i]), i < n; those of length 0 are left out.
+ *   set_starts   device int32 [n_sets + 1], rising, within [0, n]
+ *   prefix_lens  device int32 [n_sets] (written): page_size times the number of leading pages,
+ *                all inside the least length of the set, that are the same page (of [0,
+ *                num_pages)) in every row of the set; 0 for a set of fewer than two rows,
+ *                and where a row or a length of the set fails a check
+ * What kv8_attention_shared takes as prefix_lens. One launch. */
+int kvpages_shared(const int32_t* rows, const int32_t* lens, int n, const int32_t* set_starts,
+                   int n_sets, const int32_t* block_table, int n_tables, int64_t table_ld,
+                   int page_size, int num_pages, int32_t* prefix_lens, int32_t* status,
+                   kvpages_stream_t stream);
 
 #ifdef __cplusplus
 }

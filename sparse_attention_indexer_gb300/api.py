@@ -7,7 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import threading
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -290,6 +290,15 @@ class Kv8Cache(_Handle):
         return t.data_ptr(), n, t
 
 
+class Step(NamedTuple):
+    """The places of a step's new tokens (kvpages_step of include/kv_pages.h)."""
+    positions: torch.Tensor    # int32 [tokens], -1 behind the last token
+    token_table: torch.Tensor  # int32 [tokens], -1 behind the last token
+    slots: torch.Tensor        # int32 [tokens], -1 behind the last token
+    lens: torch.Tensor         # int32 [tokens], 0 behind the last token
+    starts: torch.Tensor       # int32 [n + 1]: each request's first token
+
+
 class KvPages(_Handle):
     """Ownership of the pages of one or more paged tensors (include/kv_pages.h).
 
@@ -383,6 +392,45 @@ class KvPages(_Handle):
         B._kvp(code, "kvpages_compact")
         return self.new_ids, self.counts
 
+    def step(self, rows: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor,
+             tokens: int, stream=None) -> Step:
+        """The places of the tokens [old_lens[i], new_lens[i]) of rows[i], one request after
+        another, in `tokens` places: what Kv8Cache.store and attention take of them."""
+        n = rows.shape[0]
+        for t, name in ((rows, "rows"), (old_lens, "old_lens"), (new_lens, "new_lens")):
+            _int32(t, (n,), name, self._device)
+        if tokens < 0:
+            raise ValueError("tokens < 0")
+        handle = self._stream(stream)
+        with _on(stream):  # one allocation: 16 bytes from output to output, as a warp writes them
+            each = -(-tokens // 4) * 4
+            made = torch.empty(4 * each + n + 1, dtype=torch.int32, device=self.refs.device)
+        at = made.data_ptr()
+        code = self._lib.kvpages_step(
+            rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
+            self.page_size, self.num_pages, tokens, at, at + 4 * each, at + 8 * each,
+            at + 12 * each, at + 16 * each, self._status, handle)
+        B._kvp(code, "kvpages_step")
+        return Step(*(made[i * each:i * each + tokens] for i in range(4)), made[4 * each:])
+
+    def shared(self, rows: torch.Tensor, lens: torch.Tensor, set_starts: torch.Tensor,
+               stream=None) -> torch.Tensor:
+        """How long a prefix the rows of each set share, in whole pages: int32 [n_sets], what
+        Kv8Cache.attention_shared takes. Set s is rows[set_starts[s]] .. rows[set_starts[s + 1]
+        - 1] with their lengths (those of length 0 are left out)."""
+        n, sets = rows.shape[0], set_starts.numel() - 1
+        _int32(rows, (n,), "rows", self._device)
+        _int32(lens, (n,), "lens", self._device)
+        _int32(set_starts, (max(sets, 0) + 1,), "set_starts", self._device)
+        handle = self._stream(stream)
+        with _on(stream):
+            prefix = torch.empty(sets, dtype=torch.int32, device=self.refs.device)
+        code = self._lib.kvpages_shared(
+            rows.data_ptr(), lens.data_ptr(), n, set_starts.data_ptr(), sets, *self._table_args,
+            self.page_size, self.num_pages, prefix.data_ptr(), self._status, handle)
+        B._kvp(code, "kvpages_shared")
+        return prefix
+
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies page src[i] to page dst[i] in every plane."""
         n = src.shape[0]
@@ -438,6 +486,81 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: t
     if code < 0:
         raise B.VerifyError(code)
     return out, kept
+
+
+def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor,
+                  temperature: Optional[torch.Tensor] = None,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, param_rows: int = 1,
+                  with_probs: bool = False, status: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Draws a token per row of logits (bf16, fp16 or float32 [rows, vocab]) from uniforms
+    (float32 [rows]); rules in include/token_sample.h. The settings are CUDA tensors of
+    ceil(rows / param_rows) values (temperature, top_p, min_p float32, top_k int32) or None
+    (1 and off). Returns (tokens int32 [rows], probs float32 [rows, vocab] or None): a draft's
+    probabilities as verify_drafts takes them."""
+    device = _sample_args(logits, (temperature, top_k, top_p, min_p), param_rows, status)
+    if (uniforms.dtype != torch.float32 or uniforms.shape != logits.shape[:1]
+            or uniforms.get_device() != device or not uniforms.is_contiguous()):
+        raise ValueError("uniforms is contiguous CUDA float32 [rows]")
+    with _on(stream):
+        tokens = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
+        probs = (torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+                 if with_probs else None)
+    _sample(logits, uniforms, tokens, probs, (temperature, top_k, top_p, min_p), param_rows, status,
+            stream)
+    return tokens, probs
+
+
+def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                min_p: Optional[torch.Tensor] = None, param_rows: int = 1,
+                out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The probabilities from which sample_tokens would draw, float32 [rows, vocab]: a
+    target's as verify_drafts takes them."""
+    device = _sample_args(logits, (temperature, top_k, top_p, min_p), param_rows, status)
+    if out is None:
+        with _on(stream):
+            out = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+    elif (out.dtype != torch.float32 or out.shape != logits.shape or out.get_device() != device
+          or not _last_contiguous(out)):
+        raise ValueError("out is CUDA float32 [rows, vocab]")
+    _sample(logits, None, None, out, (temperature, top_k, top_p, min_p), param_rows, status, stream)
+    return out
+
+
+def _sample_args(logits, settings, param_rows, status) -> int:
+    """Checks what both forms share; the index of the logits' device."""
+    if (logits.dtype not in B._SAMPLE_TYPES or logits.dim() != 2 or not logits.is_cuda
+            or not _last_contiguous(logits)):
+        raise ValueError("logits is CUDA bf16, fp16 or float32 [rows, vocab]")
+    device = logits.get_device()
+    if param_rows < 1:
+        raise ValueError("param_rows < 1")
+    n = -(-logits.shape[0] // param_rows)
+    for t, name, dtype in zip(settings, ("temperature", "top_k", "top_p", "min_p"),
+                              (torch.float32, torch.int32, torch.float32, torch.float32)):
+        if t is not None and (t.dtype != dtype or t.shape != (n,) or t.get_device() != device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} is contiguous {dtype} [{n}] on device {device}")
+    if status is not None:
+        _int32(status, (1,), "status", device)
+    if device != _current_device():  # where the library launches
+        raise ValueError(f"the current device is not the tensors', {device}")
+    return device
+
+
+def _sample(logits, uniforms, tokens, probs, settings, param_rows, status, stream) -> None:
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    temperature, top_k, top_p, min_p = settings
+    code = B.lib().token_sample(
+        logits.data_ptr(), B._ld(logits), B._SAMPLE_TYPES[logits.dtype], logits.shape[0],
+        logits.shape[1], at(temperature), at(top_k), at(top_p), at(min_p), param_rows,
+        at(uniforms), at(tokens), at(probs), 0 if probs is None else B._ld(probs), at(status),
+        B._stream(stream))
+    if code < 0:
+        raise B.SampleError(code)
 
 
 _HERE = contextlib.nullcontext()

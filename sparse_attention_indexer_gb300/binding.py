@@ -37,7 +37,8 @@ EXPORTS = (
     "topk_select_paged_test", "indexer_mqa_logits", "hisparse_resolve_mtp",
     "kv8_store", "kv8_attention", "kv8_attention_selected", "kv8_attention_workspace_bytes",
     "kvpages_workspace_bytes", "kvpages_reserve", "kvpages_fork", "kvpages_free",
-    "kvpages_compact", "kvpages_copy", "draft_verify",
+    "kvpages_compact", "kvpages_copy", "draft_verify", "kvpages_step", "kvpages_shared",
+    "token_sample",
 )
 
 
@@ -107,6 +108,12 @@ _SIGS = {
     "kvpages_copy": (_c.c_int, [_VP, _VP, _c.c_int, _c.c_int, _VP, _c.c_int, _VP, _VP]),
     "draft_verify": (_c.c_int, [_VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64, _c.c_int64, _VP,
                                 _VP, _VP, _c.c_int, _c.c_int, _c.c_int, _VP, _VP, _VP, _VP]),
+    "kvpages_step": (_c.c_int, [_VP, _VP, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64, _c.c_int,
+                                _c.c_int, _c.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "kvpages_shared": (_c.c_int, [_VP, _VP, _c.c_int, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64,
+                                  _c.c_int, _c.c_int, _VP, _VP, _VP]),
+    "token_sample": (_c.c_int, [_VP, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _VP, _VP, _VP, _VP,
+                                _c.c_int, _VP, _VP, _VP, _c.c_int64, _VP, _VP]),
 }
 
 # include/hisparse_resolver.h
@@ -470,6 +477,7 @@ KVPAGES_STATUS_PAGE = 4
 KVPAGES_STATUS_NO_PAGE = 8
 KVPAGES_STATUS_CHILD = 16
 KVPAGES_STATUS_REFS = 32
+KVPAGES_STATUS_TOKENS = 64
 
 
 class KvPlane(_c.Structure):
@@ -551,6 +559,66 @@ def kvpages_copy(src, dst, num_pages: int, planes, n_planes: int, status=None,
     """kvpages_copy of include/kv_pages.h: src / dst int32 [n]."""
     return _kvp(lib().kvpages_copy(_ptr(src), _ptr(dst), src.shape[0], num_pages, planes,
                                    n_planes, _ptr(status), _stream(stream)), "kvpages_copy")
+
+
+def kvpages_step(rows, old_lens, new_lens, block_table, page_size: int, num_pages: int,
+                 positions, token_table, slots, lens, starts, status=None, stream=None) -> int:
+    """kvpages_step of include/kv_pages.h: rows / old_lens / new_lens int32 [n], positions /
+    token_table / slots / lens int32 [tokens], starts int32 [n + 1]."""
+    return _kvp(lib().kvpages_step(
+        _ptr(rows), _ptr(old_lens), _ptr(new_lens), rows.shape[0], _ptr(block_table),
+        block_table.shape[0], block_table.shape[1], page_size, num_pages, positions.shape[0],
+        _ptr(positions), _ptr(token_table), _ptr(slots), _ptr(lens), _ptr(starts), _ptr(status),
+        _stream(stream)), "kvpages_step")
+
+
+def kvpages_shared(rows, lens, set_starts, block_table, page_size: int, num_pages: int,
+                   prefix_lens, status=None, stream=None) -> int:
+    """kvpages_shared of include/kv_pages.h: rows / lens int32 [n], set_starts int32
+    [n_sets + 1], prefix_lens int32 [n_sets]."""
+    return _kvp(lib().kvpages_shared(
+        _ptr(rows), _ptr(lens), rows.shape[0], _ptr(set_starts), set_starts.shape[0] - 1,
+        _ptr(block_table), block_table.shape[0], block_table.shape[1], page_size, num_pages,
+        _ptr(prefix_lens), _ptr(status), _stream(stream)), "kvpages_shared")
+
+
+# include/token_sample.h
+SAMPLE_BF16 = 0
+SAMPLE_FP16 = 1
+SAMPLE_FP32 = 2
+SAMPLE_ERR_NULL = -1
+SAMPLE_ERR_SHAPE = -2
+SAMPLE_ERR_ALIGN = -3
+SAMPLE_ERR_CUDA = -4
+SAMPLE_STATUS_NAN = 1
+SAMPLE_STATUS_EMPTY = 2
+SAMPLE_STATUS_PARAM = 4
+SAMPLE_STATUS_UNIFORM = 8
+
+_SAMPLE_TYPES = {torch.bfloat16: SAMPLE_BF16, torch.float16: SAMPLE_FP16,
+                 torch.float32: SAMPLE_FP32}
+
+
+class SampleError(RuntimeError):
+    def __init__(self, code: int):
+        super().__init__(f"token_sample: {code}")
+        self.code = code
+
+
+def token_sample(logits, uniforms=None, tokens=None, probs=None, temperature=None, top_k=None,
+                 top_p=None, min_p=None, param_rows: int = 1, status=None, stream=None) -> int:
+    """token_sample of include/token_sample.h on CUDA tensors: logits bf16 / fp16 / fp32 [rows,
+    vocab] (rows may be strided), uniforms float32 [rows], tokens int32 [rows] or None, probs
+    float32 [rows, vocab] or None (rows may be strided), temperature / top_p / min_p float32 and
+    top_k int32 [ceil(rows / param_rows)] or None. Argument marshalling only."""
+    code = lib().token_sample(
+        _ptr(logits), _ld(logits), _SAMPLE_TYPES[logits.dtype], logits.shape[0], logits.shape[1],
+        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), param_rows, _ptr(uniforms),
+        _ptr(tokens), _ptr(probs), 0 if probs is None else _ld(probs), _ptr(status),
+        _stream(stream))
+    if code < 0:
+        raise SampleError(code)
+    return code
 
 
 # include/draft_verify.h
