@@ -74,7 +74,12 @@ enum {
   KV8_STATUS_SLOT = 8,         /* slot >= num_slots: position skipped / not stored */
   KV8_STATUS_TABLE_ROW = 16,   /* table row outside [0, n_tables): rows attend to nothing /
                                   token not stored */
-  KV8_STATUS_POSITION = 32     /* kv8_store: a negative position: token not stored */
+  KV8_STATUS_POSITION = 32,    /* kv8_store: a negative position: token not stored */
+  KV8_STATUS_SETS = 64,        /* kv8_attention_shared: set_starts falls or leaves [0, groups]: no
+                                  prefix is read once for several rows; or a prefix length
+                                  outside [0, max_prefix]: that set's is not */
+  KV8_STATUS_TIMEOUT = 128     /* kv8_attention_shared: a wait inside the kernel ran out (200 ms):
+                                  the results are not valid */
 };
 
 /* Quantises `tokens` tokens into the cache. One launch.
@@ -133,6 +138,41 @@ int kv8_attention_selected(const void* q, int64_t q_ld, int dtype, int rows, int
                            int64_t num_slots, void* out, int64_t out_ld, float* lse,
                            void* workspace, int64_t ws_bytes, int32_t* status,
                            kv8_stream_t stream);
+
+/* Bytes of workspace of a kv8_attention_shared call with these heads, dim and group_rows and at
+ * most `rows` query rows on the current device. Queries the device. Negative: a KV8_ERR_* code. */
+int64_t kv8_attention_shared_workspace_bytes(int rows, int q_heads, int kv_heads, int dim,
+                                             int group_rows);
+
+/* kv8_attention for batches whose requests share prefixes (samples of one prompt, requests
+ * behind one system prompt): the result is kv8_attention's, but positions that a set of
+ * groups shares are read once for the whole set, as one product of all its query rows.
+ * Four launches. Arguments as above, and
+ *   set_starts   device int32 [n_sets + 1], rising, within [0, groups]: set s is the groups
+ *                set_starts[s] .. set_starts[s + 1] - 1; groups of no set share nothing
+ *   n_sets       at most KV8_MAX_SETS
+ *   prefix_lens  device int32 [n_sets]: positions p < prefix_lens[s] hold the same keys and
+ *                values in the block-table rows of all groups of set s (kvpages_shared finds
+ *                them). They are read through the row of the set's first group that has keys, as
+ *                far as they lie below the least length > 0 of the set's rows. A set of one
+ *                such group, or less than 128 positions, is left to the rows' own pass
+ *   max_prefix   bound on every prefix length
+ *   workspace    of kv8_attention_shared_workspace_bytes; the four launches belong together
+ * Numbers are held as in kv8_attention; where value scales of a prefix lie within 2^8 of its
+ * first one, weights keep 2^-31 of the row's largest weight * value scale, else each row's
+ * weights are taken relative to its own largest. A value scale that is infinite makes the rows
+ * that see it NaN. (rows + group_rows) * (q_heads / kv_heads) < 2^31. */
+#define KV8_MAX_SETS 1024
+int kv8_attention_shared(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,
+                         int kv_heads, int dim, float sm_scale, const int32_t* lens, int max_len,
+                         int group_rows, const int32_t* group_table, const int32_t* set_starts,
+                         int n_sets, const int32_t* prefix_lens, int max_prefix,
+                         const int32_t* block_table, int n_tables, int64_t table_ld,
+                         int page_size, int block_tokens, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         int64_t num_slots, void* out, int64_t out_ld, float* lse,
+                         void* workspace, int64_t ws_bytes, int32_t* status,
+                         kv8_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -229,6 +229,41 @@ class Kv8Cache(_Handle):
             raise B.Kv8Error(code, "kv8_attention")
         return out, lse
 
+    def attention_shared(self, q: torch.Tensor, lens: torch.Tensor, max_len: int,
+                         block_table: torch.Tensor, sm_scale: float, set_starts: torch.Tensor,
+                         prefix_lens: torch.Tensor, max_prefix: int, group_rows: int = 1,
+                         group_table: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """attention() for requests that share prefixes: the groups set_starts[s] ..
+        set_starts[s + 1] - 1 (int32 [n_sets + 1]) hold the same keys below position
+        prefix_lens[s] (int32 [n_sets], at most max_prefix; KvPages.shared finds them), which
+        are read once for all of them. Returns (out, lse)."""
+        _rows(q, "q", self._device)
+        rows, heads, dim = q.shape
+        _int32(lens, (rows,), "lens", self._device)
+        _table(block_table, self._device)
+        if group_table is not None:
+            _int32(group_table, (-(-rows // max(1, group_rows)),), "group_table", self._device)
+        sets = prefix_lens.numel()
+        _int32(prefix_lens, (sets,), "prefix_lens", self._device)
+        _int32(set_starts, (sets + 1,), "set_starts", self._device)
+        handle = self._stream(stream)
+        out, lse = self._outputs(q, out, lse, stream)
+        with self._lock:
+            ws, ws_bytes, _held = self._shared_workspace(rows, heads, group_rows, handle, stream)
+            code = self._lib.kv8_attention_shared(
+                q.data_ptr(), B._ld(q), B._KV8_TYPES[q.dtype], rows, heads, self._heads, dim,
+                sm_scale, lens.data_ptr(), max_len, group_rows,
+                None if group_table is None else group_table.data_ptr(), set_starts.data_ptr(),
+                sets, prefix_lens.data_ptr(), max_prefix, block_table.data_ptr(),
+                block_table.shape[0], block_table.shape[1], self.page_size, self.block_tokens,
+                *self._args, out.data_ptr(), B._ld(out), lse.data_ptr(), ws, ws_bytes,
+                self.status.data_ptr(), handle)
+        if code < 0:
+            raise B.Kv8Error(code, "kv8_attention_shared")
+        return out, lse
+
     def attention_selected(self, q: torch.Tensor, slots: torch.Tensor, sm_scale: float,
                            out: Optional[torch.Tensor] = None,
                            lse: Optional[torch.Tensor] = None,
@@ -283,6 +318,21 @@ class Kv8Cache(_Handle):
                     ws = self._workspaces[key] = self._new_workspace(heads, group_rows)
                 return ws
             return self._new_workspace(heads, group_rows)
+
+    def _shared_workspace(self, rows, heads, group_rows, handle, stream):
+        """The same for attention_shared, whose workspace grows with the rows: the largest so far."""
+        with _on(stream):
+            key = (handle, heads, group_rows, "shared")
+            held, ws = self._workspaces.get(key, (-1, None))
+            if rows <= held and not _capturing():
+                return ws
+            n = B.kv8_attention_shared_workspace_bytes(rows, heads, self._heads, self._dim,
+                                                       group_rows)
+            t = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+            ws = t.data_ptr(), n, t
+            if not _capturing():
+                self._workspaces[key] = rows, ws
+            return ws
 
     def _new_workspace(self, heads, group_rows):
         n = B.kv8_attention_workspace_bytes(heads, self._heads, self._dim, group_rows)

@@ -17,9 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtopk_paged.so")
 SOURCES = ["select.cu", "short.cu", "medium.cu", "rowcluster.cu", "plan.cu", "abi.cu", "noalloc.cu",
-           "prologue.cu", "resolver.cu", "logits.cu", "kv8_store.cu", "kv8_attention.cu",
+           "prologue.cu", "resolver.cu", "logits.cu", "kv8_store.cu", "kv8_attention.cu", "kv8_shared.cu",
            "kv_pages.cu", "kv_step.cu", "draft_verify.cu", "token_sample.cu"]
-HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh"]
+HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh", "kv8_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,986 @@
+// Attention of requests that share prefixes over the 8-bit paged cache (rules in
+// include/kv8_attention.h).
+//
+// A set's requests read the same keys below its prefix length, so that all their query rows on
+// a key head are one product with them: 4 * dim operations a key for each of M = requests * rows
+// * (query heads / key heads) rows, and 2 * dim bytes a key once. From M of about 256 on the
+// tensor cores bound it, below that HBM. What lies behind the prefix is each request's own and is
+// read by the kernel of kv8_attention.cuh, which starts behind the prefix and adds what the
+// rows have of it.
+//
+// Launches: the prefixes' parts (below); the join of the parts of units that several CTAs
+// share; the rows' own positions; the join of those.
+//
+// Prefix kernel. One CTA to an SM. A unit is (set, key head, 256 of the set's query rows) and
+// its steps are tiles of 128 keys; the steps of all units are laid end to end and divided
+// evenly over the CTAs, from the lengths on the device. Two streams of 128 rows run in a CTA,
+// so that the products of one overlap the softmax of the other: they take the same keys for
+// different rows, or, where only 128 rows are left, the tiles of even and odd number for the
+// same rows (their sums are joined at the end).
+//   - Warps 8-11 read codes from the pages into registers a tile ahead, widen them to fp16
+//     (exact) and store them in the 128-byte swizzle; keys as they lie (K-major), values as they
+//     lie too, as the transposed (MN-major) operand.
+//   - One thread of warp 12 issues tcgen05.mma (kind::f16): S = Q K^T into tensor memory, then
+//     O += P V with the weights P read from tensor memory.
+//   - Warps 0-3 and 4-7 are the softmax of the two streams, a thread to a row: scores from
+//     tensor memory, weights back over them as fp16. O stays in tensor memory; a row's
+//     reference is raised, and its O rescaled, only when a score passes it by 2^15. It is set
+//     2^7 below the row's largest, so that fp16 holds weights down to 2^-32 of it.
+//   - Scales belong to 16 keys at least (block_tokens): key scales multiply the scores, value
+//     scales join the exponent, relative to the first of the segment, and come out of the
+//     row's sum again. Where they lie more than 2^8 apart, sums and weights get references
+//     of their own and an exponential each.
+// Every mbarrier wait is bounded; one that runs out sets KV8_STATUS_TIMEOUT and ends the CTA's
+// work after its products in flight.
+#include <cfloat>
+
+#include "kv8_attention.cuh"
+
+namespace {
+
+constexpr int kTile = 128;      // keys of a tile, rows of a stream
+constexpr int kPThreads = 512;
+constexpr int kPRows = 2 * kTile;
+constexpr int kLeast = 128;     // positions of the least prefix that is read for all
+constexpr float kRaise = 15.0f, kBelow = 7.0f;  // log2, see above
+constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
+
+// A unit whose parts CTAs first .. last have (last < 0: none).
+struct __align__(16) Split {
+  int32_t g0, h;        // first group of the set, key head
+  int32_t row0, row1;   // its rows, counted over the set's groups, rows and heads
+  int32_t first, last;
+  int32_t pad[2];
+};
+
+struct Prefix {
+  Params p;
+  const int32_t* set_starts;
+  int n_sets;
+  const int32_t* prefix_lens;
+  int max_prefix;
+  int groups;
+  int32_t* start;    // [groups] (written): positions that a group has from its set
+  float* before;     // [rows * q_heads][dim + 4] (written)
+  Split* splits;     // [CTAs] (written): the split unit that starts in each
+  float* parts;      // two parts of kPRows rows for each CTA
+};
+
+// What the softmax needs to know of a tile; sixteen keys of it have one scale.
+struct __align__(16) Meta {
+  float ks[8];    // key scales
+  float dl[8];    // log2(value scale) - ref
+  float inv[8];   // 2^-dl
+  float ref;      // log2 of the segment's first value scale
+  uint32_t in;    // sixteens that have a page
+  int32_t end;    // keys of the tile below the prefix length
+  int32_t wide;   // value scales more than 2^8 from the first, in this tile or one before
+};
+
+template <int DIM>
+struct PSmem {
+  static constexpr int kBlocks = DIM / 64;             // 64 channels of fp16: 128 bytes of a row
+  static constexpr int kOperand = kBlocks * kTile * 128;  // bytes of 128 rows of fp16
+  static constexpr int kK = 2 * kOperand;              // behind the two tiles of queries
+  static constexpr int kV = kK + 2 * kOperand;
+  static constexpr int kMeta = kV + 2 * kOperand;
+  static constexpr int kBars = kMeta + 4 * (int)sizeof(Meta);
+  static constexpr int kMul = kBars + 256;
+  static constexpr int kCum = kMul + kPRows * 4;       // int64 [sets + 1]
+  static constexpr int kStart = kCum + (KV8_MAX_SETS + 2) * 8;
+  static constexpr int kEff = kStart + (KV8_MAX_SETS + 4) * 4;
+  static constexpr int kLead = kEff + KV8_MAX_SETS * 4;
+  static constexpr int kLast = kLead + KV8_MAX_SETS * 4;
+  static constexpr int kTotal = kLast + KV8_MAX_SETS * 4 + 1024;  // base brought to 1024 bytes
+  static constexpr int kLd = DIM + 4;  // floats between rows where the streams' sums meet
+  static_assert(kTile * kLd * 4 <= 4 * kOperand, "the sums fit over the keys and values");
+  static_assert(kTotal <= 227 * 1024, "shared memory of an SM");
+};
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase of this parity, unless the CTA gave up or kWaitNs pass: then it gives up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (*quit) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *quit = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same, whether the CTA gave up or not.
+__device__ __forceinline__ void bar_wait_through(uint32_t bar, uint32_t parity, volatile int* quit) {
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity))
+    if (now_ns() - t0 > kWaitNs) {
+      *quit = 1;
+      return;
+    }
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// What this thread wrote to shared memory is seen by the tensor cores after the next barrier.
+__device__ __forceinline__ void proxy_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Arrives on `bar` once every product this thread issued before has finished.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+// D[tmem] (+)= A[smem] . B[smem], fp16 x fp16 -> fp32.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B fp16 (0 in bits 7-9 and
+// 10-12), B transposed (MN-major) in bit 16, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+// Shared-memory descriptor in the 128-byte swizzle: start >> 4 in bits 0-13, leading offset
+// >> 4 in bits 16-29 (between blocks of 64 of an MN-major operand; unused for a K-major one),
+// stride offset >> 4 in bits 32-45 (1024 bytes between groups of 8 rows), version 1 in bits
+// 46-47, swizzle mode 2 in bits 61-63.
+__device__ __forceinline__ uint64_t sdesc(uint32_t at, uint32_t leading) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Tensor memory: this warp's 32 lanes x N columns from `at`, one row of them to a thread.
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]),
+        "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]),
+        "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]),
+        "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]),
+        "=f"(v[62]), "=f"(v[63])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :
+      : "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+        "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t at, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :
+      : "r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
+        "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]),
+        "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
+        "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ kernel
+template <int DIM, bool FP16>
+__global__ void __launch_bounds__(kPThreads, 1)
+kv8_prefix_kernel(const __grid_constant__ Prefix P) {
+  using L = PSmem<DIM>;
+  constexpr int kPieces = DIM / 16;  // 16-byte pieces of a row of codes
+  const Params& p = P.p;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  Meta* const meta = reinterpret_cast<Meta*>(smem + L::kMeta);
+  float* const s_mul = reinterpret_cast<float*>(smem + L::kMul);
+  int64_t* const s_cum = reinterpret_cast<int64_t*>(smem + L::kCum);
+  int* const s_start = reinterpret_cast<int*>(smem + L::kStart);
+  int* const s_eff = reinterpret_cast<int*>(smem + L::kEff);
+  int* const s_lead = reinterpret_cast<int*>(smem + L::kLead);
+  int* const s_last = reinterpret_cast<int*>(smem + L::kLast);
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_quit, s_bad;
+  volatile int* const quit = &s_quit;
+
+  const uint32_t bars = base + L::kBars;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
+  const uint32_t m_full = bars + 64;     // [4] the tile's scales
+  const uint32_t s_full = bars + 96;     // [2] a stream's scores
+  const uint32_t p_ready = bars + 112;   // [2] a stream's weights
+  const uint32_t done = bars + 128;      // a segment's products
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ratio = p.q_heads / p.kv_heads;
+  int err = 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(k_full + 8 * i, 4);
+      bar_init(k_empty + 8 * i, 1);
+      bar_init(v_full + 8 * i, 4);
+      bar_init(v_empty + 8 * i, 1);
+      bar_init(s_full + 8 * i, 1);
+      bar_init(p_ready + 8 * i, 4);
+    }
+    for (int i = 0; i < 4; ++i) bar_init(m_full + 8 * i, 1);
+    bar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_quit = s_bad = 0;
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // ---- the sets: where they start, and what of their prefixes is read for all
+  for (int s = tid; s <= P.n_sets; s += kPThreads) s_start[s] = __ldg(P.set_starts + s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  for (int s = tid; s < P.n_sets; s += kPThreads) {
+    const int a = s_start[s], b = s_start[s + 1];
+    int pre = __ldg(P.prefix_lens + s);
+    if (a < 0 || b < a || b > P.groups) s_bad = 1;
+    if (pre < 0 || pre > P.max_prefix) {
+      err |= KV8_STATUS_SETS;
+      pre = 0;
+    }
+    s_eff[s] = pre;
+    s_lead[s] = INT32_MAX;
+    s_last[s] = -1;
+  }
+  __syncthreads();
+  const bool bad = s_bad != 0;
+  if (bad) err |= KV8_STATUS_SETS;
+  // the set of a group, or -1
+  auto set_of = [&](int g) {
+    if (bad || g < s_start[0] || g >= s_start[P.n_sets]) return -1;
+    int lo = 0, hi = P.n_sets;  // s_start[lo] <= g < s_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  for (int r = tid; r < p.rows; r += kPThreads) {
+    const int g = r / p.group_rows, s = set_of(g);
+    int ignored = 0;  // the rows' own pass reports
+    const int len = row_len(p, r, p.group_table ? __ldg(p.group_table + g) : g, &ignored);
+    if (s < 0 || len == 0) continue;
+    atomicMin(s_eff + s, len);
+    atomicMin(s_lead + s, g);
+    atomicMax(s_last + s, g);
+  }
+  __syncthreads();
+  // rows of a set on one key head; its steps on one: pairs of 128 rows take a tile to a step,
+  // 128 rows left over two
+  auto rows_of = [&](int s) { return (s_start[s + 1] - s_start[s]) * p.group_rows * ratio; };
+  auto tiles_in = [&](int s) { return (s_eff[s] + kTile - 1) / kTile; };
+  auto steps_of = [&](int s) -> int64_t {
+    const int m = (rows_of(s) + kTile - 1) / kTile, t = tiles_in(s);
+    return (int64_t)(m >> 1) * t + (m & 1) * ((t + 1) >> 1);
+  };
+  for (int s = tid; s < P.n_sets; s += kPThreads)
+    if (bad || s_last[s] <= s_lead[s] || s_eff[s] < kLeast) s_eff[s] = 0;
+  __syncthreads();
+  if (warp == 0) {  // s_cum[s]: steps of the sets before s
+    int64_t run = 0;
+    for (int s0 = 0; s0 < P.n_sets; s0 += 32) {
+      const int64_t mine = s0 + lane < P.n_sets ? steps_of(s0 + lane) * p.kv_heads : 0;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (s0 + lane < P.n_sets) s_cum[s0 + lane] = run + x - mine;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_cum[P.n_sets] = run;
+  }
+  for (int g = blockIdx.x * kPThreads + tid; g < P.groups; g += gridDim.x * kPThreads) {
+    const int s = set_of(g);
+    P.start[g] = s < 0 ? 0 : s_eff[s];
+  }
+  __syncthreads();
+
+  // ---- this CTA's steps
+  const int64_t all = s_cum[P.n_sets];
+  const int64_t n = max((int64_t)1, min((int64_t)gridDim.x, (all + 1) / 2));
+  const int64_t me = blockIdx.x;
+  const int64_t w0 = me < n ? me * all / n : all, w1 = me < n ? (me + 1) * all / n : all;
+  Split mine = {0, 0, 0, 0, 0, -1, {0, 0}};
+  uint32_t tiles_done = 0;               // of all segments: the rings' counters
+  uint32_t turns[2] = {0, 0};            // scores of the streams
+  uint32_t segments = 0;
+  int set = 0;
+
+  for (int64_t w = w0; w < w1;) {
+    // ---- the segment: a unit's steps [i0, i1) of `steps`
+    while (s_cum[set + 1] <= w) ++set;
+    const int rows = rows_of(set), eff = s_eff[set], tiles = tiles_in(set);
+    const int m = (rows + kTile - 1) / kTile;
+    const int64_t per_head = steps_of(set);
+    const int64_t rel = w - s_cum[set];
+    const int h = (int)(rel / per_head);
+    const int64_t in_head = rel - h * per_head;
+    const int pair = (int)min(in_head / tiles, (int64_t)(m >> 1));
+    const bool two = pair < (m >> 1);  // two streams of rows, else of keys
+    const int steps = two ? tiles : (tiles + 1) >> 1;
+    const int i0 = (int)(in_head - (int64_t)pair * tiles);
+    const int i1 = (int)min((int64_t)steps, i0 + (w1 - w));
+    const int row0 = pair * kPRows;            // of the set's rows on this head
+    const int g0 = s_start[set];
+    const int tile0 = two ? i0 : 2 * i0, tile1 = two ? i1 : min(2 * i1, tiles);
+    const int count[2] = {two ? i1 - i0 : (tile1 - tile0 + 1) >> 1, two ? i1 - i0 : (tile1 - tile0) >> 1};
+    const int lead = s_lead[set];
+    const int32_t* table =
+        p.block_table + (int64_t)(p.group_table ? __ldg(p.group_table + lead) : lead) * p.table_ld;
+    // query row and head of a row of the unit; row >= p.rows: none
+    auto row_at = [&](int r) { return (int64_t)g0 * p.group_rows + (row0 + r) / ratio; };
+    auto head_at = [&](int r) { return h * ratio + (row0 + r) % ratio; };
+    auto has_row = [&](int r) { return row0 + r < rows && row_at(r) < p.rows; };
+
+    // ---- queries, as kv8_attention.cuh brings them to fp16; a negative scale turns their sign
+    for (int x = tid; x < (two ? kPRows : kTile) * kPieces; x += kPThreads) {
+      const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
+      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (has_row(r)) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(r) * p.q_ld +
+                                                          (int64_t)head_at(r) * DIM + c * 16);
+        v[0] = __ldg(src);
+        v[1] = __ldg(src + 1);
+      }
+      uint32_t wds[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      float mul = fabsf(p.scale);
+      if (!FP16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top = max(top, max(wds[i] & 0x7FFFu, (wds[i] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = kPieces / 2; o; o >>= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = (int)(top >> 7);
+        const int up = e == 255 || top == 0 ? 0 : min(126, 14 - (e - 127));
+        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+        mul *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          wds[i] = pack_half(__uint_as_float(wds[i] << 16) * f,
+                             __uint_as_float(wds[i] & 0xFFFF0000u) * f);
+      }
+      const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wds[i] ^= flip;
+      const uint32_t at = base + (r / kTile) * L::kOperand + (c >> 2) * (kTile * 128) +
+                          (r % kTile) * 128;
+      const int c0 = (c & 3) * 2, sw = r & 7;
+      sts128(at + ((c0 ^ sw) << 4), wds[0], wds[1], wds[2], wds[3]);
+      sts128(at + (((c0 + 1) ^ sw) << 4), wds[4], wds[5], wds[6], wds[7]);
+      if (c == 0) s_mul[r] = mul;
+    }
+    proxy_fence();
+    __syncthreads();
+
+    const bool whole = i0 == 0 && i1 == steps;
+    float* const part = P.parts + (2 * me + (i0 == 0)) * Part<DIM, kPRows>::kFloats;
+
+    if (warp >= 8 && warp < 12) {
+      // ---------------------------------------------------------------- codes
+      const int ww = warp - 8;
+      constexpr int kKeysWarp = 32 / kPieces, kKeysPass = 4 * kKeysWarp, kPasses = kTile / kKeysPass;
+      // 8 lanes that store together meet every bank once: 4 pieces of an even and an odd key
+      const int piece = DIM == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3;
+      const int key0 = ww * kKeysWarp +
+                       (DIM == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane >> 2);
+      const int c0 = (piece & 3) * 2;
+      // first slot of the sixteen keys (lane & 7) of a tile, or -1
+      auto slot_of = [&](int tile) -> int {
+        const int pos = tile * kTile + (lane & 7) * 16;
+        if (tile >= tile1 || pos >= eff) return -1;
+        const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+        const int32_t page = __ldg(table + pg);
+        if (page < 0) {
+          err |= KV8_STATUS_TABLE_ENTRY;
+          return -1;
+        }
+        const int64_t slot = (int64_t)page * p.page_size + (pos - pg * p.page_size);
+        if (slot >= p.num_slots) {
+          err |= KV8_STATUS_SLOT;
+          return -1;
+        }
+        return (int)slot;
+      };
+      uint4 kc[kPasses], vc[kPasses];
+      auto load = [&](const uint8_t* from, uint4 (&to)[kPasses], int tile, int slot) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int key = i * kKeysPass + key0;
+          const int s = __shfl_sync(0xffffffffu, slot, key >> 4);
+          const bool in = s >= 0 && tile * kTile + key < eff;
+          to[i] = in ? __ldg(reinterpret_cast<const uint4*>(
+                           from + ((int64_t)(s + (key & 15)) * p.kv_heads + h) * DIM + piece * 16))
+                     : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto store = [&](uint32_t to, const uint4 (&from)[kPasses]) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int key = i * kKeysPass + key0;
+          const uint32_t at = to + (piece >> 2) * (kTile * 128) + key * 128;
+          uint32_t x[8];
+          widen4(from[i].x, x[0], x[1]);
+          widen4(from[i].y, x[2], x[3]);
+          widen4(from[i].z, x[4], x[5]);
+          widen4(from[i].w, x[6], x[7]);
+          sts128(at + ((c0 ^ (key & 7)) << 4), x[0], x[1], x[2], x[3]);
+          sts128(at + (((c0 + 1) ^ (key & 7)) << 4), x[4], x[5], x[6], x[7]);
+        }
+        proxy_fence();
+        __syncwarp();
+      };
+      float ks = 0.0f, vs = 0.0f;  // scales of the sixteen keys (lane & 7)
+      auto scales = [&](int slot) {
+        if (ww == 0 && slot >= 0) {
+          const int b = p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
+          ks = __ldg(p.k_scale + (int64_t)b * p.kv_heads + h);
+          vs = __ldg(p.v_scale + (int64_t)b * p.kv_heads + h);
+        }
+      };
+      float ref = 0.0f;
+      bool found = false, wide = false;
+      int slot = slot_of(tile0);
+      load(p.k, kc, tile0, slot);
+      load(p.v, vc, tile0, slot);
+      scales(slot);
+      int next = slot_of(tile0 + 1);
+      uint32_t t = tiles_done;
+      for (int tile = tile0; tile < tile1; ++tile, ++t) {
+        const uint32_t st = t & 1, ph = (t >> 1) & 1;
+        if (!__all_sync(0xffffffffu, bar_wait(k_empty + 8 * st, ph ^ 1, quit))) break;
+        store(base + L::kK + st * L::kOperand, kc);
+        if (lane == 0) bar_arrive(k_full + 8 * st);
+        if (ww == 0) {
+          // scales; the slot of four tiles before was read before this tile's place was free
+          const bool in = slot >= 0;
+          const float lv = log2f(vs);
+          const uint32_t fit = __ballot_sync(0xffffffffu, in && vs > 0.0f && vs <= FLT_MAX) & 0xFFu;
+          if (!found && fit) {
+            ref = __shfl_sync(0xffffffffu, lv, __ffs(fit) - 1);
+            found = true;
+          }
+          wide |= __any_sync(0xffffffffu, in && !(fabsf(lv - ref) <= 8.0f));
+          const uint32_t have = __ballot_sync(0xffffffffu, in) & 0xFFu;
+          Meta& d = meta[t & 3];
+          if (lane < 8) {
+            d.ks[lane] = in ? ks : 0.0f;
+            d.dl[lane] = in ? lv - ref : 0.0f;
+            d.inv[lane] = in ? exp2f(ref - lv) : 1.0f;
+          }
+          if (lane == 0) {
+            d.ref = ref;
+            d.in = have;
+            d.end = min(kTile, eff - tile * kTile);
+            d.wide = wide;
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(m_full + 8 * (t & 3));
+        }
+        load(p.k, kc, tile + 1, next);
+        if (!__all_sync(0xffffffffu, bar_wait(v_empty + 8 * st, ph ^ 1, quit))) break;
+        store(base + L::kV + st * L::kOperand, vc);
+        if (lane == 0) bar_arrive(v_full + 8 * st);
+        load(p.v, vc, tile + 1, next);
+        scales(next);
+        slot = next;
+        next = slot_of(tile + 2);
+      }
+    } else if (warp == 12) {
+      // ---------------------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc_f16(kTile, kTile, false), kIdO = idesc_f16(kTile, DIM, true);
+        bool ok = true;
+        uint32_t turn[2] = {turns[0], turns[1]};
+        // the tile that stream b takes in its turn j, counted over all segments
+        auto tile_at = [&](int b, int j) { return tiles_done + (two ? j : 2 * j + b); };
+        auto scores = [&](int b, int j) {
+          const uint32_t t = tile_at(b, j), st = t & 1;
+          ok = ok && bar_wait(k_full + 8 * st, (t >> 1) & 1, quit);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t q = base + (two ? b : 0) * L::kOperand, k = base + L::kK + st * L::kOperand;
+#pragma unroll
+          for (int i = 0; i < DIM / 16; ++i) {
+            const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
+            mma_ss(tmem + b * kTile, sdesc(q + off, 16), sdesc(k + off, 16), kIdS, i > 0);
+          }
+          tc_commit(s_full + 8 * b);
+          if (!two || b == 1) tc_commit(k_empty + 8 * st);
+        };
+        auto sums = [&](int b, int j) {
+          const uint32_t t = tile_at(b, j), st = t & 1;
+          ok = ok && bar_wait(p_ready + 8 * b, turn[b] & 1, quit);
+          ++turn[b];
+          ok = ok && bar_wait(v_full + 8 * st, (t >> 1) & 1, quit);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t v = base + L::kV + st * L::kOperand;
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_ts(tmem + 2 * kTile + b * DIM, tmem + b * kTile + i * 8,
+                   sdesc(v + i * 2048, kTile * 128), kIdO, j > 0 || i > 0);
+          if (!two || b == 1) tc_commit(v_empty + 8 * st);
+        };
+        for (int b = 0; b < 2; ++b)
+          if (count[b] > 0) scores(b, 0);
+        for (int j = 0; j < count[0] && ok; ++j)
+          for (int b = 0; b < 2; ++b)
+            if (j < count[b] && ok) {
+              sums(b, j);
+              if (j + 1 < count[b] && ok) scores(b, j + 1);
+            }
+        tc_commit(done);  // all products issued above
+        bar_wait_through(done, segments & 1, quit);
+      }
+      __syncwarp();
+    } else if (warp < 8) {
+      // ---------------------------------------------------------------- softmax
+      const int b = warp >> 2;                 // stream
+      const int r = (warp & 3) * 32 + lane;    // row of the stream
+      const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t t_s = t_lane + b * kTile, t_o = t_lane + 2 * kTile + b * DIM;
+      const float mul = s_mul[two ? b * kTile + r : r];
+      // mo: the reference of o where scales lie far apart, else m
+      float m = kNone, mo = kNone, l = 0.0f, ref = 0.0f;
+      bool wide = false, ok = true;
+      for (int j = 0; j < count[b]; ++j) {
+        const uint32_t t = tiles_done + (two ? j : 2 * j + b);
+        ok = bar_wait(s_full + 8 * b, (turns[b] + j) & 1, quit) &&
+             bar_wait(m_full + 8 * (t & 3), (t >> 2) & 1, quit);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const Meta& d = meta[t & 3];
+        float a[8], dl[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          a[c] = mul * d.ks[c];
+          if (a[c] == 0.0f) a[c] = FLT_MIN;  // times the -infinity of a masked key: not NaN
+          dl[c] = d.dl[c];
+        }
+        ref = d.ref;
+        const uint32_t in = d.in;
+        const int end = d.end;
+        const bool full = in == 0xFFu && end == kTile;
+        wide = d.wide != 0;
+        auto scores = [&](int half, float (&v)[64]) {
+          tmem_ld(t_s + half * 64, v);
+          if (!full) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (half * 64 + i >= end || !((in >> (half * 4 + i / 16)) & 1)) v[i] = -INFINITY;
+          }
+        };
+        float tm = -INFINITY, to = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float v[64];
+          scores(half, v);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x = v[16 * c];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) x = fmaxf(x, v[16 * c + i]);
+            x *= a[half * 4 + c];
+            to = fmaxf(to, x + dl[half * 4 + c]);
+            tm = fmaxf(tm, x);
+          }
+        }
+        if (!wide) tm = to;
+        const bool raise = tm > m + kRaise || (wide && to > mo + kRaise);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float top = tm > m + kRaise ? tm - kBelow : m;
+          const float topo = !wide ? top : to > mo + kRaise ? to - kBelow : mo;
+          l *= exp2_fast(m - top);
+          const float keep = exp2_fast(mo - topo);
+          m = top;
+          mo = topo;
+          if (j > 0) {  // the products of the tile before are finished: so are this tile's scores
+#pragma unroll
+            for (int c = 0; c < DIM / 32; ++c) {
+              float o[32];
+              tmem_ld(t_o + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= keep;
+              tmem_st(t_o + c * 32, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float v[64];
+          scores(half, v);
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float ac = a[half * 4 + c], z = dl[half * 4 + c] - mo;
+            float sum = 0.0f;
+            if (wide) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum += exp2_fast(fmaf(v[16 * c + i], ac, -m));
+              l += sum;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x = exp2_fast(fmaf(v[16 * c + 2 * i], ac, z));
+              const float y = exp2_fast(fmaf(v[16 * c + 2 * i + 1], ac, z));
+              sum += x + y;
+              w[8 * c + i] = pack_half(x, y);
+            }
+            if (!wide) l = fmaf(sum, d.inv[half * 4 + c], l);
+          }
+          tmem_st(t_s + half * 32, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_ready + 8 * b);
+      }
+      bar_wait_through(done, segments & 1, quit);
+      __syncwarp();
+      tc_fence_after();
+      // ---- this row's sums, joined with the other stream's where both have it
+      float* const meet = reinterpret_cast<float*>(smem + L::kK);  // [128][kLd]
+      const bool some = count[b] > 0;
+      const float mv = mo + ref;
+      if (!two) {
+        if (b == 1) {
+#pragma unroll
+          for (int c = 0; c < DIM / 32; ++c) {
+            float o[32];
+            if (some) {
+              tmem_ld(t_o + c * 32, o);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(meet + r * L::kLd + c * 32 + 4 * i) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          *reinterpret_cast<float4*>(meet + r * L::kLd + DIM) = make_float4(m, mv, l, 0.0f);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      if (two || b == 0) {
+        const int ur = two ? b * kTile + r : r;
+        const bool has = has_row(ur);
+        const int64_t row = has ? row_at(ur) : 0;
+        int ignored = 0;
+        const int g = (int)(row / p.group_rows);
+        // a row of length 0 attends to nothing, the prefix neither
+        const bool on =
+            has && row_len(p, (int)row, p.group_table ? __ldg(p.group_table + g) : g, &ignored) > 0;
+        float* const dst = whole ? P.before + (row * p.q_heads + head_at(ur)) * (DIM + 4)
+                                 : part + ur * DIM;
+        float* const stat = whole ? dst + DIM : part + Part<DIM, kPRows>::kStat + ur * 4;
+        float top = m, topv = mv, f0 = 1.0f, f1 = 0.0f;
+        if (!two) {
+          const float4 st = *reinterpret_cast<const float4*>(meet + r * L::kLd + DIM);
+          top = fmaxf(m, st.x);
+          topv = fmaxf(mv, st.y);
+          l = l * exp2_fast(m - top) + st.z * exp2_fast(st.x - top);
+          f0 = exp2_fast(mv - topv);
+          f1 = exp2_fast(st.y - topv);
+        }
+        if (has)
+          *reinterpret_cast<float4*>(stat) = on ? make_float4(top, topv, l, 0.0f)
+                                                : make_float4(kNone, kNone, 0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < DIM / 32; ++c) {
+          float o[32];
+          __syncwarp();
+          tmem_ld(t_o + c * 32, o);
+          if (has) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              if (!two) {
+                const float4 y =
+                    *reinterpret_cast<const float4*>(meet + r * L::kLd + c * 32 + 4 * i);
+                x.x = x.x * f0 + y.x * f1;
+                x.y = x.y * f0 + y.y * f1;
+                x.z = x.z * f0 + y.z * f1;
+                x.w = x.w * f0 + y.w * f1;
+              }
+              if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              *reinterpret_cast<float4*>(dst + c * 32 + 4 * i) = x;
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // ---- the unit's parts, for the join
+    if (i0 == 0 && !whole) {
+      const int64_t first_w = w - i0;
+      mine = {g0, h, row0, min(rows, row0 + (two ? kPRows : kTile)), (int32_t)me,
+              (int32_t)(((first_w + steps) * n - 1) / all), {0, 0}};
+    }
+    tiles_done += (uint32_t)(tile1 - tile0);
+    turns[0] += (uint32_t)count[0];
+    turns[1] += (uint32_t)count[1];
+    ++segments;
+    w += i1 - i0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*quit) break;
+  }
+  if (tid == 0) {
+    P.splits[me] = mine;
+    if (s_quit) err |= KV8_STATUS_TIMEOUT;
+  }
+  if (err && p.status) atomicOr(p.status, err);
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+// Joins the parts of the split units: CTA (i, y) a share of the rows of entry i, a warp to a row.
+template <int DIM>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+kv8_prefix_join_kernel(const __grid_constant__ Prefix P) {
+  constexpr int kVec = DIM / 32;
+  const Params& p = P.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Split u = P.splits[blockIdx.x];
+  if (u.last < 0) return;
+  const int ratio = p.q_heads / p.kv_heads;
+  auto part = [&](int c) {
+    return P.parts + (2 * (int64_t)(u.first + c) + (c == 0)) * Part<DIM, kPRows>::kFloats;
+  };
+  for (int r = blockIdx.y * kJoinWarps + warp; r < u.row1 - u.row0; r += gridDim.y * kJoinWarps) {
+    const int64_t row = (int64_t)u.g0 * p.group_rows + (u.row0 + r) / ratio;
+    if (row >= p.rows) return;
+    float top = -INFINITY, topv = -INFINITY, l = 0.0f, v[kVec] = {};
+    add_parts<DIM, kPRows>(part, 0, 1, u.last - u.first + 1, r, top, topv, l, v);
+    float* dst = P.before + (row * p.q_heads + u.h * ratio + (u.row0 + r) % ratio) * (DIM + 4);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) dst[lane * kVec + i] = v[i];
+    if (lane == 0) *reinterpret_cast<float4*>(dst + DIM) = make_float4(top, topv, l, 0.0f);
+  }
+}
+
+// Workspace behind that of the rows' own pass.
+struct SharedWork {
+  int64_t start, splits, parts, before, total;
+};
+
+SharedWork shared_work(int64_t own, int sms, int64_t rows, int q_heads, int dim, int group_rows) {
+  auto up = [](int64_t x) { return (x + 255) & ~int64_t(255); };
+  SharedWork w;
+  w.start = up(own);
+  w.splits = up(w.start + (rows + group_rows - 1) / group_rows * 4);
+  w.parts = up(w.splits + sms * (int64_t)sizeof(Split));
+  w.before = up(w.parts + (int64_t)sms * 2 * kPRows * (dim + 4) * 4);
+  w.total = up(w.before + rows * q_heads * (dim + 4) * 4);
+  return w;
+}
+
+template <int DIM, bool FP16>
+int launch_prefix(const Prefix& P, int dev, cudaStream_t s) {
+  const auto kernel = kv8_prefix_kernel<DIM, FP16>;
+  const auto join = kv8_prefix_join_kernel<DIM>;
+  constexpr int kBytes = PSmem<DIM>::kTotal;
+  static std::atomic<uint64_t> ready;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+            cudaSuccess)
+      return KV8_ERR_CUDA;
+    ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  const int grid = sm_count(dev);
+  kernel<<<(unsigned)grid, kPThreads, kBytes, s>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return KV8_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 8);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join, P);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KV8_OK : KV8_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int64_t kv8_attention_shared_workspace_bytes(int rows, int q_heads, int kv_heads,
+                                                        int dim, int group_rows) {
+  if (rows < 0) return KV8_ERR_SHAPE;
+  const int64_t own = kv8_attention_workspace_bytes(q_heads, kv_heads, dim, group_rows);
+  if (own < 0) return own;
+  const int sms = sm_count(current_device());
+  if (sms < 0) return KV8_ERR_CUDA;
+  return shared_work(own, sms, rows, q_heads, dim, group_rows).total;
+}
+
+extern "C" int kv8_attention_shared(
+    const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads, int dim,
+    float sm_scale, const int32_t* lens, int max_len, int group_rows, const int32_t* group_table,
+    const int32_t* set_starts, int n_sets, const int32_t* prefix_lens, int max_prefix,
+    const int32_t* block_table, int n_tables, int64_t table_ld, int page_size, int block_tokens,
+    const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    int64_t num_slots, void* out, int64_t out_ld, float* lse, void* workspace, int64_t ws_bytes,
+    int32_t* status, kv8_stream_t stream) {
+  if (max_len < 0 || n_tables < 1 || table_ld < 1 || page_size < 1 || block_tokens < 16 ||
+      page_size % block_tokens || num_slots % page_size || n_sets < 0 || n_sets > KV8_MAX_SETS ||
+      max_prefix < 0)
+    return KV8_ERR_SHAPE;
+  const int err = check_common(q, q_ld, dtype, rows, q_heads, kv_heads, dim, sm_scale,
+                               group_rows, block_tokens, k_cache, v_cache, k_scale, v_scale,
+                               num_slots, out, out_ld, lse, workspace, status);
+  if (err || rows == 0) return err;
+  if (((int64_t)rows + group_rows) * (q_heads / kv_heads) >= (int64_t(1) << 31)) return KV8_ERR_SHAPE;
+  if (!lens || !block_table || (n_sets && (!set_starts || !prefix_lens))) return KV8_ERR_NULL;
+  if (!aligned(lens, 4) || !aligned(group_table, 4) || !aligned(block_table, 4) ||
+      !aligned(set_starts, 4) || !aligned(prefix_lens, 4))
+    return KV8_ERR_ALIGN;
+  const int64_t own = kv8_attention_workspace_bytes(q_heads, kv_heads, dim, group_rows);
+  if (own < 0) return (int)own;
+  const int dev = current_device(), sms = sm_count(dev);
+  if (sms < 0) return KV8_ERR_CUDA;
+  const SharedWork at = shared_work(own, sms, rows, q_heads, dim, group_rows);
+  if (ws_bytes < at.total) return KV8_ERR_WORKSPACE;
+  Params p = common(q, q_ld, rows, q_heads, kv_heads, sm_scale, block_tokens, k_cache, v_cache,
+                    k_scale, v_scale, num_slots, out, out_ld, lse, status);
+  p.lens = lens;
+  p.max_len = max_len;
+  p.group_rows = group_rows;
+  p.group_table = group_table;
+  p.block_table = block_table;
+  p.n_tables = n_tables;
+  p.table_ld = table_ld;
+  p.page_size = page_size;
+  p.page_shift = shift_of(page_size);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (n_sets == 0 || max_prefix < kLeast) return run<false>(p, dim, dtype, workspace, own, s);
+  char* const ws = reinterpret_cast<char*>(workspace);
+  Prefix P = {};
+  P.p = p;
+  P.set_starts = set_starts;
+  P.n_sets = n_sets;
+  P.prefix_lens = prefix_lens;
+  P.max_prefix = max_prefix;
+  P.groups = (rows + group_rows - 1) / group_rows;
+  P.start = reinterpret_cast<int32_t*>(ws + at.start);
+  P.splits = reinterpret_cast<Split*>(ws + at.splits);
+  P.parts = reinterpret_cast<float*>(ws + at.parts);
+  P.before = reinterpret_cast<float*>(ws + at.before);
+  const int code = dim == 128 ? dtype == KV8_FP16 ? launch_prefix<128, true>(P, dev, s)
+                                                  : launch_prefix<128, false>(P, dev, s)
+                   : dtype == KV8_FP16 ? launch_prefix<64, true>(P, dev, s)
+                                       : launch_prefix<64, false>(P, dev, s);
+  if (code) return code;
+  p.start = P.start;
+  p.before = P.before;
+  return run<false, true>(p, dim, dtype, workspace, own, s);
+}
