@@ -196,6 +196,28 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
                : "memory");
 }
 
+// Two floats to an operation.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Tensor memory: this warp's 32 lanes x N columns from `at`, one row of them to a thread.
 __device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32]) {
   asm volatile(
@@ -260,6 +282,27 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const float (&v)[32]) {
         "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
         "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
         "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8};"
+      :
+      : "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
@@ -644,93 +687,131 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
       const float mul = s_mul[two ? b * kTile + r : r];
       // mo: the reference of o where scales lie far apart, else m
       float m = kNone, mo = kNone, l = 0.0f, ref = 0.0f;
-      bool wide = false, ok = true;
+      bool ok = true;
       for (int j = 0; j < count[b]; ++j) {
         const uint32_t t = tiles_done + (two ? j : 2 * j + b);
         ok = bar_wait(s_full + 8 * b, (turns[b] + j) & 1, quit) &&
              bar_wait(m_full + 8 * (t & 3), (t >> 2) & 1, quit);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
+        // The loops over parts of a row stay rolled: their code has to stay in the instruction
+        // cache beside that of the other roles
         const Meta& d = meta[t & 3];
-        float a[8], dl[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          a[c] = mul * d.ks[c];
-          if (a[c] == 0.0f) a[c] = FLT_MIN;  // times the -infinity of a masked key: not NaN
-          dl[c] = d.dl[c];
-        }
         ref = d.ref;
-        const uint32_t in = d.in;
-        const int end = d.end;
-        const bool full = in == 0xFFu && end == kTile;
-        wide = d.wide != 0;
-        auto scores = [&](int half, float (&v)[64]) {
-          tmem_ld(t_s + half * 64, v);
-          if (!full) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (half * 64 + i >= end || !((in >> (half * 4 + i / 16)) & 1)) v[i] = -INFINITY;
-          }
-        };
-        float tm = -INFINITY, to = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float v[64];
-          scores(half, v);
-#pragma unroll
+        if (d.in != 0xFFu || d.end != kTile) {  // keys that are not there
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            float x = v[16 * c];
+            uint32_t have = (d.in >> (2 * c) & 1 ? 0xFFFFu : 0u) | (d.in >> (2 * c + 1) & 1 ? 0xFFFF0000u : 0u);
+            const int left = d.end - c * 32;
+            if (left < 32) have &= left <= 0 ? 0u : (1u << left) - 1;
+            float v[32];
+            tmem_ld(t_s + c * 32, v);
 #pragma unroll
-            for (int i = 1; i < 16; ++i) x = fmaxf(x, v[16 * c + i]);
-            x *= a[half * 4 + c];
-            to = fmaxf(to, x + dl[half * 4 + c]);
-            tm = fmaxf(tm, x);
+            for (int i = 0; i < 32; ++i)
+              if (!(have >> i & 1)) v[i] = -INFINITY;
+            tmem_st(t_s + c * 32, v);
           }
+          tmem_st_wait();
         }
-        if (!wide) tm = to;
-        const bool raise = tm > m + kRaise || (wide && to > mo + kRaise);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float top = tm > m + kRaise ? tm - kBelow : m;
-          const float topo = !wide ? top : to > mo + kRaise ? to - kBelow : mo;
+        // a score times this is x; never 0, which would make a masked -infinity NaN
+        auto factor = [&](float ks) {
+          const float a = mul * ks;
+          return a == 0.0f ? FLT_MIN : a;
+        };
+        // references raised to kBelow below the maxima tm and to, sums with them
+        auto raise = [&](float tm, float to, bool apart) {
+          const bool up = tm > m + kRaise;
+          const float top = up ? tm - kBelow : m;
+          const float topo = !apart ? top : to > mo + kRaise ? to - kBelow : mo;
           l *= exp2_fast(m - top);
           const float keep = exp2_fast(mo - topo);
           m = top;
           mo = topo;
-          if (j > 0) {  // the products of the tile before are finished: so are this tile's scores
+          if (j == 0) return;
+          // the products of the tile before are finished: so are this tile's scores
+#pragma unroll 1
+          for (int c = 0; c < DIM / 32; ++c) {
+            float o[32];
+            tmem_ld(t_o + c * 32, o);
 #pragma unroll
-            for (int c = 0; c < DIM / 32; ++c) {
-              float o[32];
-              tmem_ld(t_o + c * 32, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= keep;
-              tmem_st(t_o + c * 32, o);
-            }
+            for (int i = 0; i < 32; ++i) o[i] *= keep;
+            tmem_st(t_o + c * 32, o);
           }
-        }
+        };
+        if (!d.wide) {
+          float tm = -INFINITY;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const float4 ks = *reinterpret_cast<const float4*>(d.ks + half * 4);
+            const float4 dl = *reinterpret_cast<const float4*>(d.dl + half * 4);
+            float v[64];
+            tmem_ld(t_s + half * 64, v);
+            float x[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float v[64];
-          scores(half, v);
-          uint32_t w[32];
+            for (int c = 0; c < 4; ++c) {
+              x[c] = v[16 * c];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float ac = a[half * 4 + c], z = dl[half * 4 + c] - mo;
-            float sum = 0.0f;
-            if (wide) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) sum += exp2_fast(fmaf(v[16 * c + i], ac, -m));
-              l += sum;
+              for (int i = 1; i < 16; ++i) x[c] = fmaxf(x[c], v[16 * c + i]);
             }
+            tm = fmaxf(tm, fmaxf(fmaxf(fmaf(x[0], factor(ks.x), dl.x), fmaf(x[1], factor(ks.y), dl.y)),
+                                 fmaxf(fmaf(x[2], factor(ks.z), dl.z), fmaf(x[3], factor(ks.w), dl.w))));
+          }
+          if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, tm, false);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const float4 ks4 = *reinterpret_cast<const float4*>(d.ks + half * 4);
+            const float4 dl4 = *reinterpret_cast<const float4*>(d.dl + half * 4);
+            const float4 inv4 = *reinterpret_cast<const float4*>(d.inv + half * 4);
+            const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, dl[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
+            const float inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
+            float v[64];
+            tmem_ld(t_s + half * 64, v);
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float a = factor(ks[c]), z = dl[c] - m;
+              const uint64_t a2 = pack2(a, a), z2 = pack2(z, z);
+              uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 x = unpack2(fma2(pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]), a2, z2));
+                const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+                sum = add2(sum, pack2(e0, e1));
+                w[8 * c + i] = pack_half(e0, e1);
+              }
+              const float2 both = unpack2(sum);
+              l = fmaf(both.x + both.y, inv[c], l);
+            }
+            tmem_st(t_s + half * 32, w);
+          }
+          mo = m;
+        } else {
+          float tm = -INFINITY, to = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float v[16];
+            tmem_ld(t_s + c * 16, v);
+            float x = v[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) x = fmaxf(x, v[i]);
+            x *= factor(d.ks[c]);
+            tm = fmaxf(tm, x);
+            to = fmaxf(to, x + d.dl[c]);
+          }
+          if (__any_sync(0xffffffffu, tm > m + kRaise || to > mo + kRaise)) raise(tm, to, true);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            const float a = factor(d.ks[c]), z = d.dl[c] - mo;
+            float v[16];
+            tmem_ld(t_s + c * 16, v);
+            uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float x = exp2_fast(fmaf(v[16 * c + 2 * i], ac, z));
-              const float y = exp2_fast(fmaf(v[16 * c + 2 * i + 1], ac, z));
-              sum += x + y;
-              w[8 * c + i] = pack_half(x, y);
+              l += exp2_fast(fmaf(v[2 * i], a, -m)) + exp2_fast(fmaf(v[2 * i + 1], a, -m));
+              w[i] = pack_half(exp2_fast(fmaf(v[2 * i], a, z)), exp2_fast(fmaf(v[2 * i + 1], a, z)));
             }
-            if (!wide) l = fmaf(sum, d.inv[half * 4 + c], l);
+            tmem_st(t_s + c * 8, w);
           }
-          tmem_st(t_s + half * 32, w);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -746,7 +827,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
       const float mv = mo + ref;
       if (!two) {
         if (b == 1) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DIM / 32; ++c) {
             float o[32];
             if (some) {
@@ -788,7 +869,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
         if (has)
           *reinterpret_cast<float4*>(stat) = on ? make_float4(top, topv, l, 0.0f)
                                                 : make_float4(kNone, kNone, 0.0f, 0.0f);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DIM / 32; ++c) {
           float o[32];
           __syncwarp();
