@@ -20,10 +20,10 @@
 //   - Warps 8-11 read codes from the pages into registers a tile ahead, widen them to fp16
 //     (exact) and store them in the 128-byte swizzle; keys as they lie (K-major), values as they
 //     lie too, as the transposed (MN-major) operand.
-//   - One thread of warp 12 issues tcgen05.mma (kind::f16): S = Q K^T into tensor memory, then
-//     O += P V with the weights P read from tensor memory.
-//   - Warps 0-3 and 4-7 are the softmax of the two streams, a thread to a row: scores from
-//     tensor memory, weights back over them as fp16. O stays in tensor memory; a row's
+//   - Warps 0-3 and 4-7 are the two streams, a thread to a row. The first thread of each issues
+//     its tcgen05.mma (kind::f16): S = Q K^T into tensor memory, and O += P V with the weights P
+//     read from tensor memory. All take the scores from there and put weights back over them
+//     as fp16. O stays in tensor memory; a row's
 //     reference is raised, and its O rescaled, only when a score passes it by 2^15. It is set
 //     2^7 below the row's largest, so that fp16 holds weights down to 2^-32 of it.
 //   - Scales belong to 16 keys at least (block_tokens): key scales multiply the scores, value
@@ -39,7 +39,7 @@
 namespace {
 
 constexpr int kTile = 128;      // keys of a tile, rows of a stream
-constexpr int kPThreads = 512;
+constexpr int kPThreads = 384;
 constexpr int kPRows = 2 * kTile;
 constexpr int kLeast = 128;     // positions of the least prefix that is read for all
 constexpr float kRaise = 15.0f, kBelow = 7.0f;  // log2, see above
@@ -81,19 +81,26 @@ template <int DIM>
 struct PSmem {
   static constexpr int kBlocks = DIM / 64;             // 64 channels of fp16: 128 bytes of a row
   static constexpr int kOperand = kBlocks * kTile * 128;  // bytes of 128 rows of fp16
-  static constexpr int kK = 2 * kOperand;              // behind the two tiles of queries
-  static constexpr int kV = kK + 2 * kOperand;
-  static constexpr int kMeta = kV + 2 * kOperand;
+  static constexpr int kHalf = kTile * DIM;            // codes of a tile's keys (or values)
+  static constexpr int kK = 2 * kOperand;              // two tiles, behind the two of queries
+  static constexpr int kV = kK + 2 * kOperand;         // one
+  static constexpr int kRaw = kV + kOperand;           // codes on their way: kSlots halves, and
+  static constexpr int kSlots = 3;                     // kMoreSlots over the second queries'
+  static constexpr int kMoreSlots = 2;                 // place where there is one tile of them
+  static constexpr int kMeta = kRaw + kSlots * kHalf;
   static constexpr int kBars = kMeta + 4 * (int)sizeof(Meta);
   static constexpr int kMul = kBars + 256;
-  static constexpr int kCum = kMul + kPRows * 4;       // int64 [sets + 1]
-  static constexpr int kStart = kCum + (KV8_MAX_SETS + 2) * 8;
+  static constexpr int kStart = kMul + kPRows * 4;
   static constexpr int kEff = kStart + (KV8_MAX_SETS + 4) * 4;
   static constexpr int kLead = kEff + KV8_MAX_SETS * 4;
-  static constexpr int kLast = kLead + KV8_MAX_SETS * 4;
-  static constexpr int kTotal = kLast + KV8_MAX_SETS * 4 + 1024;  // base brought to 1024 bytes
+  static constexpr int kTotal = kLead + KV8_MAX_SETS * 4 + 1024;  // base brought to 1024 bytes
+  // before the first segment, over keys and values
+  static constexpr int kCum = kK;                      // int64 [sets + 1]
+  static constexpr int kLast = kCum + (KV8_MAX_SETS + 2) * 8;
+  static_assert(kLast + KV8_MAX_SETS * 4 <= kMeta, "over keys, values and codes");
   static constexpr int kLd = DIM + 4;  // floats between rows where the streams' sums meet
-  static_assert(kTile * kLd * 4 <= 4 * kOperand, "the sums fit over the keys and values");
+  static_assert(kK + kTile * kLd * 4 <= kMeta, "the sums fit over keys and values");
+  static_assert(kMoreSlots * kHalf <= kOperand, "halves over the second queries");
   static_assert(kTotal <= 227 * 1024, "shared memory of an SM");
 };
 
@@ -309,12 +316,528 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ a segment
+// What a CTA does of one unit at a time; written by its first thread. The roles are functions of
+// their own, so that each has the registers to itself.
+struct __align__(16) Segment {
+  const int32_t* table;  // block-table row through which the prefix is read
+  float* part;           // where the sums go if the unit is split
+  int32_t g0, h;         // first group of the set, key head
+  int32_t row0, rows;    // first row of the unit; rows of the set on a key head
+  int32_t eff;           // positions of the prefix
+  int32_t tile0, tile1;
+  int32_t two;           // two streams of rows, else of keys
+  int32_t whole;         // the CTA has all of the unit
+  int32_t count[2];      // tiles of each stream
+  uint32_t tiles_done, turns[2], parity;  // of the segments before: the barriers' counters
+
+  // query row and head of a row of the unit
+  __device__ __forceinline__ int64_t row_at(const Params& p, int ratio, int r) const {
+    return (int64_t)g0 * p.group_rows + (row0 + r) / ratio;
+  }
+  __device__ __forceinline__ int head_at(int ratio, int r) const {
+    return h * ratio + (row0 + r) % ratio;
+  }
+  __device__ __forceinline__ bool has_row(const Params& p, int ratio, int r) const {
+    return row0 + r < rows && row_at(p, ratio, r) < p.rows;
+  }
+};
+
+// Queries, as kv8_attention.cuh brings them to fp16; a negative scale turns their sign.
+template <int DIM, bool FP16>
+__device__ __noinline__ void load_queries(const Prefix& P, const Segment& g, uint32_t base,
+                                          float* s_mul) {
+  using L = PSmem<DIM>;
+  constexpr int kPieces = DIM / 16;
+  const Params& p = P.p;
+  const int tid = threadIdx.x, ratio = p.q_heads / p.kv_heads;
+  for (int x = tid; x < (g.two ? kPRows : kTile) * kPieces; x += kPThreads) {
+    const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
+    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (g.has_row(p, ratio, r)) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + g.row_at(p, ratio, r) * p.q_ld +
+                                                        (int64_t)g.head_at(ratio, r) * DIM + c * 16);
+      v[0] = __ldg(src);
+      v[1] = __ldg(src + 1);
+    }
+    uint32_t wds[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    float mul = fabsf(p.scale);
+    if (!FP16) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = max(top, max(wds[i] & 0x7FFFu, (wds[i] >> 16) & 0x7FFFu));
+#pragma unroll
+      for (int o = kPieces / 2; o; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = (int)(top >> 7);
+      const int up = e == 255 || top == 0 ? 0 : min(126, 14 - (e - 127));
+      const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+      mul *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        wds[i] = pack_half(__uint_as_float(wds[i] << 16) * f,
+                           __uint_as_float(wds[i] & 0xFFFF0000u) * f);
+    }
+    const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wds[i] ^= flip;
+    const uint32_t at = base + (r / kTile) * L::kOperand + (c >> 2) * (kTile * 128) +
+                        (r % kTile) * 128;
+    const int c0 = (c & 3) * 2, sw = r & 7;
+    sts128(at + ((c0 ^ sw) << 4), wds[0], wds[1], wds[2], wds[3]);
+    sts128(at + (((c0 + 1) ^ sw) << 4), wds[4], wds[5], wds[6], wds[7]);
+    if (c == 0) s_mul[r] = mul;
+  }
+  proxy_fence();
+}
+
+// Warps 8-11: codes of the segment's tiles into shared memory as fp16, and the tiles' scales.
+// Returns status bits.
+template <int DIM>
+__device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint32_t base, Meta* meta,
+                                        uint32_t bars, volatile int* quit) {
+  using L = PSmem<DIM>;
+  constexpr int kPieces = DIM / 16;  // 16-byte pieces of a row of codes
+  const Params& p = P.p;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  const uint32_t m_full = bars + 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile0 = g.tile0, tile1 = g.tile1, eff = g.eff, h = g.h;
+  const int32_t* const table = g.table;
+  const uint32_t tiles_done = g.tiles_done;
+  int err = 0;
+  const int ww = warp - 8;
+  constexpr int kKeysWarp = 32 / kPieces, kKeysPass = 4 * kKeysWarp, kPasses = kTile / kKeysPass;
+  // 8 lanes that store together meet every bank once: 4 pieces of an even and an odd key
+  const int piece = DIM == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3;
+  const int key0 = ww * kKeysWarp +
+                   (DIM == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane >> 2);
+  const int c0 = (piece & 3) * 2;
+  // Halves of tiles come by cp.async into a ring, each thread the pieces that it widens, so that
+  // no thread waits for another's: keys 0, keys 1, values 0, keys 2, values 1, .. . (Loads into
+  // registers go through what shared memory leaves of the L1 cache, 28 KB, which bounds what is on
+  // its way.) Slots and scales come four tiles at a time, a lane for each sixteen keys.
+  const int tiles = tile1 - tile0, halves = 2 * tiles;
+  const int ring = g.two ? L::kSlots : L::kSlots + L::kMoreSlots;
+  const uint32_t mine = (threadIdx.x - 256) * 16;
+  auto place = [&](int slot) {
+    return base + mine + (slot < L::kSlots ? L::kRaw + slot * L::kHalf
+                                           : L::kOperand + (slot - L::kSlots) * L::kHalf);
+  };
+  // half x: values or keys, and of which tile
+  auto values_at = [&](int x) { return x > 0 && ((x & 1) == 0 || x == halves - 1); };
+  auto tile_at = [&](int x) { return values_at(x) ? (x - 1) >> 1 : (x + 1) >> 1; };
+  // first slot of this lane's sixteen keys of tiles tile0 + 4 * batch .. + 3, or -1
+  auto slots_of = [&](int batch) -> int {
+    const int64_t tile = tile0 + 4 * (int64_t)batch + (lane >> 3);
+    const int64_t pos64 = tile * kTile + (lane & 7) * 16;
+    if (tile >= tile1 || pos64 >= eff) return -1;
+    const int pos = (int)pos64;
+    const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+    const int32_t page = __ldg(table + pg);
+    if (page < 0) {
+      err |= KV8_STATUS_TABLE_ENTRY;
+      return -1;
+    }
+    const int64_t slot = (int64_t)page * p.page_size + (pos - pg * p.page_size);
+    if (slot >= p.num_slots) {
+      err |= KV8_STATUS_SLOT;
+      return -1;
+    }
+    return (int)slot;
+  };
+  int slots_k = slots_of(0), slots_next = slots_of(1), slots_v = slots_k;
+  float ks = 0.0f, vs = 1.0f, ks_next = 0.0f, vs_next = 1.0f;
+  int at = -1, at_next = -1;  // slots of the scales
+  auto scales = [&] {
+    at_next = slots_k;
+    if (ww == 0 && slots_k >= 0) {
+      const int b = p.block_shift >= 0 ? slots_k >> p.block_shift : slots_k / p.block;
+      ks_next = __ldg(p.k_scale + (int64_t)b * p.kv_heads + h);
+      vs_next = __ldg(p.v_scale + (int64_t)b * p.kv_heads + h);
+    }
+  };
+  scales();
+  const int stride = p.kv_heads * DIM;
+  const uint8_t *const from_k = p.k + h * DIM + piece * 16, *const from_v = p.v + h * DIM + piece * 16;
+  auto load = [&](int x, int slot) {  // x rises call by call
+    if (x < halves) {
+      const bool values = values_at(x);
+      const int tile = tile_at(x);
+      if (tile > 0 && (tile & 3) == 0) {
+        if (values) {
+          slots_v = slots_k;
+        } else {
+          slots_k = slots_next;
+          slots_next = slots_of((tile >> 2) + 1);
+          scales();
+        }
+      }
+      const uint8_t* from = values ? from_v : from_k;
+      const int here = values ? slots_v : slots_k;
+      const int lane0 = (tile & 3) * 8, left = eff - (tile0 + tile) * kTile;
+      const uint32_t to = place(slot);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int key = i * kKeysPass + key0;
+        const int s = __shfl_sync(0xffffffffu, here, lane0 + (key >> 4));
+        copy16(to + i * 2048, from + (int64_t)(max(s, 0) + (key & 15)) * stride, s >= 0 && key < left);
+      }
+    }
+    copy_commit();
+  };
+  float ref = 0.0f, lv = 0.0f;
+  bool found = false, wide = false;
+#pragma unroll 1
+  for (int x = 0; x < ring; ++x) load(x, x);
+  int slot = 0;
+#pragma unroll 1
+  for (int x = 0; x < halves; ++x) {
+    const bool values = values_at(x);
+    const int tile = tile_at(x);
+    const uint32_t t = tiles_done + tile;
+    const uint32_t full = values ? v_full : k_full + 8 * (t & 1);
+    const uint32_t empty = values ? v_empty : k_empty + 8 * (t & 1);
+    const uint32_t turn = values ? t : t >> 1;
+    if (g.two) copy_wait<L::kSlots - 1>();
+    else copy_wait<L::kSlots + L::kMoreSlots - 1>();
+    if (!__all_sync(0xffffffffu, bar_wait(empty, (turn & 1) ^ 1, quit))) break;
+    const uint32_t from = place(slot);
+    const uint32_t to = base + (values ? L::kV : L::kK + (t & 1) * L::kOperand) +
+                        (piece >> 2) * (kTile * 128);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int key = i * kKeysPass + key0;
+      const uint4 c = lds128(from + i * 2048);
+      uint32_t y[8];
+      widen4(c.x, y[0], y[1]);
+      widen4(c.y, y[2], y[3]);
+      widen4(c.z, y[4], y[5]);
+      widen4(c.w, y[6], y[7]);
+      sts128(to + key * 128 + ((c0 ^ (key & 7)) << 4), y[0], y[1], y[2], y[3]);
+      sts128(to + key * 128 + (((c0 + 1) ^ (key & 7)) << 4), y[4], y[5], y[6], y[7]);
+    }
+    proxy_fence();
+    __syncwarp();
+    if (lane == 0) bar_arrive(full);
+    load(x + ring, slot);
+    slot = slot == ring - 1 ? 0 : slot + 1;
+    if (ww == 0 && !values) {
+      // scales; those of four tiles before were read before this tile's place was free
+      if ((tile & 3) == 0) {
+        ks = ks_next;
+        vs = vs_next;
+        at = at_next;
+        lv = log2f(vs);
+      }
+      const int lane0 = (tile & 3) * 8;
+      const bool in = (lane & 24) == lane0 && at >= 0;
+      const uint32_t fit = __ballot_sync(0xffffffffu, in && vs > 0.0f && vs <= FLT_MAX);
+      if (!found && fit) {
+        ref = __shfl_sync(0xffffffffu, lv, __ffs(fit) - 1);
+        found = true;
+      }
+      wide |= __any_sync(0xffffffffu, in && !(fabsf(lv - ref) <= 8.0f));
+      const uint32_t have = __ballot_sync(0xffffffffu, in) >> lane0;
+      Meta& d = meta[t & 3];
+      if ((lane & 24) == lane0) {
+        d.ks[lane & 7] = in ? ks : 0.0f;
+        d.dl[lane & 7] = in ? lv - ref : 0.0f;
+        d.inv[lane & 7] = in ? exp2f(ref - lv) : 1.0f;
+      }
+      if (lane == 0) {
+        d.ref = ref;
+        d.in = have & 0xFFu;
+        d.end = min(kTile, eff - (tile0 + tile) * kTile);
+        d.wide = wide;
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(m_full + 8 * (t & 3));
+    }
+  }
+  copy_wait<0>();
+  return err;
+}
+
+// Warps 0-3 and 4-7: the streams' products and softmax, and the sums of their rows at the end.
+template <int DIM>
+__device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint32_t base,
+                                         uint8_t* smem, uint32_t bars, uint32_t tmem,
+                                         volatile int* quit) {
+  using L = PSmem<DIM>;
+  const Params& p = P.p;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ratio = p.q_heads / p.kv_heads;
+  const Meta* const meta = reinterpret_cast<const Meta*>(smem + L::kMeta);
+  const float* const s_mul = reinterpret_cast<const float*>(smem + L::kMul);
+  const bool two = g.two != 0;
+  const uint32_t tiles_done = g.tiles_done;
+  const int b = warp >> 2;                 // stream
+  const int count = g.count[b];
+  const uint32_t turns = g.turns[b];
+  const int r = (warp & 3) * 32 + lane;    // row of the stream
+  const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t t_s = t_lane + b * kTile, t_o = t_lane + 2 * kTile + b * DIM;
+  const float mul = s_mul[two ? b * kTile + r : r];
+  // Products of this stream, issued by its first thread: the scores of its turn j, and the
+  // sums of its turn j once its four warps have their weights in place. Keys and values are
+  // given back by both streams, by one of them twice where it alone had them.
+  constexpr uint32_t kIdS = idesc_f16(kTile, kTile, false), kIdO = idesc_f16(kTile, DIM, true);
+  auto tile_at = [&](int j) { return tiles_done + (uint32_t)(two ? j : 2 * j + b); };
+  auto issue_scores = [&](int j) {
+    const uint32_t t = tile_at(j), st = t & 1;
+    if (!bar_wait(k_full + 8 * st, (t >> 1) & 1, quit)) return;
+    tc_fence_after();
+    const uint32_t q = base + (two ? b : 0) * L::kOperand, k = base + L::kK + st * L::kOperand;
+#pragma unroll
+    for (int i = 0; i < DIM / 16; ++i) {
+      const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
+      mma_ss(tmem + b * kTile, sdesc(q + off, 16), sdesc(k + off, 16), kIdS, i > 0);
+    }
+    tc_commit(s_full + 8 * b);
+    tc_commit(k_empty + 8 * st);
+    if (!two) tc_commit(k_empty + 8 * st);
+  };
+  auto issue_sums = [&](int j) {
+    if (!bar_wait(p_ready + 8 * b, (turns + j) & 1, quit) ||
+        !bar_wait(v_full, tile_at(j) & 1, quit))
+      return;
+    tc_fence_after();
+    const uint32_t v = base + L::kV;
+#pragma unroll
+    for (int i = 0; i < kTile / 16; ++i)
+      mma_ts(tmem + 2 * kTile + b * DIM, tmem + b * kTile + i * 8,
+             sdesc(v + i * 2048, kTile * 128), kIdO, j > 0 || i > 0);
+    tc_commit(v_empty);
+    if (!two) tc_commit(v_empty);
+  };
+  const bool first = (tid & 127) == 0;
+  if (first && count > 0) issue_scores(0);
+  __syncwarp();
+  // mo: the reference of o where scales lie far apart, else m
+  float m = kNone, mo = kNone, l = 0.0f, ref = 0.0f;
+  bool ok = true;
+  for (int j = 0; j < count; ++j) {
+    const uint32_t t = tile_at(j);
+    ok = bar_wait(s_full + 8 * b, (turns + j) & 1, quit) &&
+         bar_wait(m_full + 8 * (t & 3), (t >> 2) & 1, quit);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after();
+    // The loops over parts of a row stay rolled: their code has to stay in the instruction
+    // cache beside that of the other roles
+    const Meta& d = meta[t & 3];
+    ref = d.ref;
+    if (d.in != 0xFFu || d.end != kTile) {  // keys that are not there
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t have = (d.in >> (2 * c) & 1 ? 0xFFFFu : 0u) | (d.in >> (2 * c + 1) & 1 ? 0xFFFF0000u : 0u);
+        const int left = d.end - c * 32;
+        if (left < 32) have &= left <= 0 ? 0u : (1u << left) - 1;
+        float v[32];
+        tmem_ld(t_s + c * 32, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(have >> i & 1)) v[i] = -INFINITY;
+        tmem_st(t_s + c * 32, v);
+      }
+      tmem_st_wait();
+    }
+    // a score times this is x; never 0, which would make a masked -infinity NaN
+    auto factor = [&](float ks) {
+      const float a = mul * ks;
+      return a == 0.0f ? FLT_MIN : a;
+    };
+    // references raised to kBelow below the maxima tm and to, sums with them
+    auto raise = [&](float tm, float to, bool apart) {
+      const bool up = tm > m + kRaise;
+      const float top = up ? tm - kBelow : m;
+      const float topo = !apart ? top : to > mo + kRaise ? to - kBelow : mo;
+      l *= exp2_fast(m - top);
+      const float keep = exp2_fast(mo - topo);
+      m = top;
+      mo = topo;
+      if (j == 0) return;
+      // the products of the tile before are finished: so are this tile's scores
+#pragma unroll 1
+      for (int c = 0; c < DIM / 32; ++c) {
+        float o[32];
+        tmem_ld(t_o + c * 32, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= keep;
+        tmem_st(t_o + c * 32, o);
+      }
+    };
+    if (!d.wide) {
+      float tm = -INFINITY;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const float4 ks = *reinterpret_cast<const float4*>(d.ks + half * 4);
+        const float4 dl = *reinterpret_cast<const float4*>(d.dl + half * 4);
+        float v[64];
+        tmem_ld(t_s + half * 64, v);
+        float x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[c] = v[16 * c];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) x[c] = fmaxf(x[c], v[16 * c + i]);
+        }
+        tm = fmaxf(tm, fmaxf(fmaxf(fmaf(x[0], factor(ks.x), dl.x), fmaf(x[1], factor(ks.y), dl.y)),
+                             fmaxf(fmaf(x[2], factor(ks.z), dl.z), fmaf(x[3], factor(ks.w), dl.w))));
+      }
+      if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, tm, false);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const float4 ks4 = *reinterpret_cast<const float4*>(d.ks + half * 4);
+        const float4 dl4 = *reinterpret_cast<const float4*>(d.dl + half * 4);
+        const float4 inv4 = *reinterpret_cast<const float4*>(d.inv + half * 4);
+        const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, dl[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
+        const float inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
+        float v[64];
+        tmem_ld(t_s + half * 64, v);
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float a = factor(ks[c]), z = dl[c] - m;
+          const uint64_t a2 = pack2(a, a), z2 = pack2(z, z);
+          uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = unpack2(fma2(pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]), a2, z2));
+            const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+            sum = add2(sum, pack2(e0, e1));
+            w[8 * c + i] = pack_half(e0, e1);
+          }
+          const float2 both = unpack2(sum);
+          l = fmaf(both.x + both.y, inv[c], l);
+        }
+        tmem_st(t_s + half * 32, w);
+      }
+      mo = m;
+    } else {
+      float tm = -INFINITY, to = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        float v[16];
+        tmem_ld(t_s + c * 16, v);
+        float x = v[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) x = fmaxf(x, v[i]);
+        x *= factor(d.ks[c]);
+        tm = fmaxf(tm, x);
+        to = fmaxf(to, x + d.dl[c]);
+      }
+      if (__any_sync(0xffffffffu, tm > m + kRaise || to > mo + kRaise)) raise(tm, to, true);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const float a = factor(d.ks[c]), z = d.dl[c] - mo;
+        float v[16];
+        tmem_ld(t_s + c * 16, v);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          l += exp2_fast(fmaf(v[2 * i], a, -m)) + exp2_fast(fmaf(v[2 * i + 1], a, -m));
+          w[i] = pack_half(exp2_fast(fmaf(v[2 * i], a, z)), exp2_fast(fmaf(v[2 * i + 1], a, z)));
+        }
+        tmem_st(t_s + c * 8, w);
+      }
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(p_ready + 8 * b);
+    if (first) {
+      issue_sums(j);
+      if (j + 1 < count) issue_scores(j + 1);
+    }
+    __syncwarp();
+  }
+  if (first) tc_commit(done);  // all products issued above
+  bar_wait_through(done, g.parity, quit);
+  __syncwarp();
+  tc_fence_after();
+  // ---- this row's sums, joined with the other stream's where both have it
+  float* const meet = reinterpret_cast<float*>(smem + L::kK);  // [128][kLd]
+  const bool some = count > 0;
+  const float mv = mo + ref;
+  if (!two) {
+    if (b == 1) {
+#pragma unroll 1
+      for (int c = 0; c < DIM / 32; ++c) {
+        float o[32];
+        if (some) {
+          tmem_ld(t_o + c * 32, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(meet + r * L::kLd + c * 32 + 4 * i) =
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+      *reinterpret_cast<float4*>(meet + r * L::kLd + DIM) = make_float4(m, mv, l, 0.0f);
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+  if (two || b == 0) {
+    const int ur = two ? b * kTile + r : r;
+    const bool has = g.has_row(p, ratio, ur);
+    const int64_t row = has ? g.row_at(p, ratio, ur) : 0;
+    int ignored = 0;
+    const int gr = (int)(row / p.group_rows);
+    // a row of length 0 attends to nothing, the prefix neither
+    const bool on =
+        has && row_len(p, (int)row, p.group_table ? __ldg(p.group_table + gr) : gr, &ignored) > 0;
+    float* const dst = g.whole ? P.before + (row * p.q_heads + g.head_at(ratio, ur)) * (DIM + 4)
+                             : g.part + ur * DIM;
+    float* const stat = g.whole ? dst + DIM : g.part + Part<DIM, kPRows>::kStat + ur * 4;
+    float top = m, topv = mv, f0 = 1.0f, f1 = 0.0f;
+    if (!two) {
+      const float4 st = *reinterpret_cast<const float4*>(meet + r * L::kLd + DIM);
+      top = fmaxf(m, st.x);
+      topv = fmaxf(mv, st.y);
+      l = l * exp2_fast(m - top) + st.z * exp2_fast(st.x - top);
+      f0 = exp2_fast(mv - topv);
+      f1 = exp2_fast(st.y - topv);
+    }
+    if (has)
+      *reinterpret_cast<float4*>(stat) = on ? make_float4(top, topv, l, 0.0f)
+                                            : make_float4(kNone, kNone, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int c = 0; c < DIM / 32; ++c) {
+      float o[32];
+      __syncwarp();
+      tmem_ld(t_o + c * 32, o);
+      if (has) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          if (!two) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(meet + r * L::kLd + c * 32 + 4 * i);
+            x.x = x.x * f0 + y.x * f1;
+            x.y = x.y * f0 + y.y * f1;
+            x.z = x.z * f0 + y.z * f1;
+            x.w = x.w * f0 + y.w * f1;
+          }
+          if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          *reinterpret_cast<float4*>(dst + c * 32 + 4 * i) = x;
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 template <int DIM, bool FP16>
 __global__ void __launch_bounds__(kPThreads, 1)
 kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   using L = PSmem<DIM>;
-  constexpr int kPieces = DIM / 16;  // 16-byte pieces of a row of codes
   const Params& p = P.p;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -328,15 +851,15 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   int* const s_lead = reinterpret_cast<int*>(smem + L::kLead);
   int* const s_last = reinterpret_cast<int*>(smem + L::kLast);
   __shared__ uint32_t s_tmem;
+  __shared__ Segment seg;
   __shared__ int s_quit, s_bad;
   volatile int* const quit = &s_quit;
 
   const uint32_t bars = base + L::kBars;
-  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
-  const uint32_t m_full = bars + 64;     // [4] the tile's scales
-  const uint32_t s_full = bars + 96;     // [2] a stream's scores
-  const uint32_t p_ready = bars + 112;   // [2] a stream's weights
-  const uint32_t done = bars + 128;      // a segment's products
+  // keys in place [2] and their places free [2], values the same, a tile's scales [4], a stream's
+  // scores [2] and weights [2], a segment's products
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ratio = p.q_heads / p.kv_heads;
@@ -345,18 +868,18 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(k_full + 8 * i, 4);
-      bar_init(k_empty + 8 * i, 1);
-      bar_init(v_full + 8 * i, 4);
-      bar_init(v_empty + 8 * i, 1);
+      bar_init(k_empty + 8 * i, 2);
       bar_init(s_full + 8 * i, 1);
       bar_init(p_ready + 8 * i, 4);
     }
     for (int i = 0; i < 4; ++i) bar_init(m_full + 8 * i, 1);
-    bar_init(done, 1);
+    bar_init(v_full, 4);
+    bar_init(v_empty, 2);
+    bar_init(done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_quit = s_bad = 0;
   }
-  if (warp == 12) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&s_tmem)),
                  "r"(512)
@@ -443,466 +966,62 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   const int64_t n = max((int64_t)1, min((int64_t)gridDim.x, (all + 1) / 2));
   const int64_t me = blockIdx.x;
   const int64_t w0 = me < n ? me * all / n : all, w1 = me < n ? (me + 1) * all / n : all;
+  int set = 0;  // the set of the steps at hand, and the steps before it
+  while (set + 1 < P.n_sets && s_cum[set + 1] <= w0) ++set;
+  int64_t before = s_cum[set];
+  __syncthreads();  // s_cum gives way to keys
   Split mine = {0, 0, 0, 0, 0, -1, {0, 0}};
-  uint32_t tiles_done = 0;               // of all segments: the rings' counters
-  uint32_t turns[2] = {0, 0};            // scores of the streams
-  uint32_t segments = 0;
-  int set = 0;
-
+  uint32_t tiles_done = 0, turns[2] = {0, 0}, segments = 0;
   for (int64_t w = w0; w < w1;) {
     // ---- the segment: a unit's steps [i0, i1) of `steps`
-    while (s_cum[set + 1] <= w) ++set;
-    const int rows = rows_of(set), eff = s_eff[set], tiles = tiles_in(set);
-    const int m = (rows + kTile - 1) / kTile;
+    for (int64_t of_set; (of_set = steps_of(set) * p.kv_heads) <= w - before; ++set) before += of_set;
+    const int tiles = tiles_in(set), rows = rows_of(set);
+    const int pairs = ((rows + kTile - 1) / kTile) >> 1;
     const int64_t per_head = steps_of(set);
-    const int64_t rel = w - s_cum[set];
+    const int64_t rel = w - before;
     const int h = (int)(rel / per_head);
     const int64_t in_head = rel - h * per_head;
-    const int pair = (int)min(in_head / tiles, (int64_t)(m >> 1));
-    const bool two = pair < (m >> 1);  // two streams of rows, else of keys
+    const int pair = (int)min(in_head / tiles, (int64_t)pairs);
+    const bool two = pair < pairs;
     const int steps = two ? tiles : (tiles + 1) >> 1;
     const int i0 = (int)(in_head - (int64_t)pair * tiles);
     const int i1 = (int)min((int64_t)steps, i0 + (w1 - w));
-    const int row0 = pair * kPRows;            // of the set's rows on this head
-    const int g0 = s_start[set];
     const int tile0 = two ? i0 : 2 * i0, tile1 = two ? i1 : min(2 * i1, tiles);
-    const int count[2] = {two ? i1 - i0 : (tile1 - tile0 + 1) >> 1, two ? i1 - i0 : (tile1 - tile0) >> 1};
-    const int lead = s_lead[set];
-    const int32_t* table =
-        p.block_table + (int64_t)(p.group_table ? __ldg(p.group_table + lead) : lead) * p.table_ld;
-    // query row and head of a row of the unit; row >= p.rows: none
-    auto row_at = [&](int r) { return (int64_t)g0 * p.group_rows + (row0 + r) / ratio; };
-    auto head_at = [&](int r) { return h * ratio + (row0 + r) % ratio; };
-    auto has_row = [&](int r) { return row0 + r < rows && row_at(r) < p.rows; };
-
-    // ---- queries, as kv8_attention.cuh brings them to fp16; a negative scale turns their sign
-    for (int x = tid; x < (two ? kPRows : kTile) * kPieces; x += kPThreads) {
-      const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
-      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (has_row(r)) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(r) * p.q_ld +
-                                                          (int64_t)head_at(r) * DIM + c * 16);
-        v[0] = __ldg(src);
-        v[1] = __ldg(src + 1);
-      }
-      uint32_t wds[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-      float mul = fabsf(p.scale);
-      if (!FP16) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          top = max(top, max(wds[i] & 0x7FFFu, (wds[i] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = kPieces / 2; o; o >>= 1)
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = (int)(top >> 7);
-        const int up = e == 255 || top == 0 ? 0 : min(126, 14 - (e - 127));
-        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-        mul *= __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          wds[i] = pack_half(__uint_as_float(wds[i] << 16) * f,
-                             __uint_as_float(wds[i] & 0xFFFF0000u) * f);
-      }
-      const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wds[i] ^= flip;
-      const uint32_t at = base + (r / kTile) * L::kOperand + (c >> 2) * (kTile * 128) +
-                          (r % kTile) * 128;
-      const int c0 = (c & 3) * 2, sw = r & 7;
-      sts128(at + ((c0 ^ sw) << 4), wds[0], wds[1], wds[2], wds[3]);
-      sts128(at + (((c0 + 1) ^ sw) << 4), wds[4], wds[5], wds[6], wds[7]);
-      if (c == 0) s_mul[r] = mul;
-    }
-    proxy_fence();
-    __syncthreads();
-
+    const int count0 = two ? i1 - i0 : (tile1 - tile0 + 1) >> 1;
+    const int count1 = two ? i1 - i0 : (tile1 - tile0) >> 1;
     const bool whole = i0 == 0 && i1 == steps;
-    float* const part = P.parts + (2 * me + (i0 == 0)) * Part<DIM, kPRows>::kFloats;
-
-    if (warp >= 8 && warp < 12) {
-      // ---------------------------------------------------------------- codes
-      const int ww = warp - 8;
-      constexpr int kKeysWarp = 32 / kPieces, kKeysPass = 4 * kKeysWarp, kPasses = kTile / kKeysPass;
-      // 8 lanes that store together meet every bank once: 4 pieces of an even and an odd key
-      const int piece = DIM == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3;
-      const int key0 = ww * kKeysWarp +
-                       (DIM == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane >> 2);
-      const int c0 = (piece & 3) * 2;
-      // first slot of the sixteen keys (lane & 7) of a tile, or -1
-      auto slot_of = [&](int tile) -> int {
-        const int pos = tile * kTile + (lane & 7) * 16;
-        if (tile >= tile1 || pos >= eff) return -1;
-        const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
-        const int32_t page = __ldg(table + pg);
-        if (page < 0) {
-          err |= KV8_STATUS_TABLE_ENTRY;
-          return -1;
-        }
-        const int64_t slot = (int64_t)page * p.page_size + (pos - pg * p.page_size);
-        if (slot >= p.num_slots) {
-          err |= KV8_STATUS_SLOT;
-          return -1;
-        }
-        return (int)slot;
-      };
-      uint4 kc[kPasses], vc[kPasses];
-      auto load = [&](const uint8_t* from, uint4 (&to)[kPasses], int tile, int slot) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int key = i * kKeysPass + key0;
-          const int s = __shfl_sync(0xffffffffu, slot, key >> 4);
-          const bool in = s >= 0 && tile * kTile + key < eff;
-          to[i] = in ? __ldg(reinterpret_cast<const uint4*>(
-                           from + ((int64_t)(s + (key & 15)) * p.kv_heads + h) * DIM + piece * 16))
-                     : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto store = [&](uint32_t to, const uint4 (&from)[kPasses]) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int key = i * kKeysPass + key0;
-          const uint32_t at = to + (piece >> 2) * (kTile * 128) + key * 128;
-          uint32_t x[8];
-          widen4(from[i].x, x[0], x[1]);
-          widen4(from[i].y, x[2], x[3]);
-          widen4(from[i].z, x[4], x[5]);
-          widen4(from[i].w, x[6], x[7]);
-          sts128(at + ((c0 ^ (key & 7)) << 4), x[0], x[1], x[2], x[3]);
-          sts128(at + (((c0 + 1) ^ (key & 7)) << 4), x[4], x[5], x[6], x[7]);
-        }
-        proxy_fence();
-        __syncwarp();
-      };
-      float ks = 0.0f, vs = 0.0f;  // scales of the sixteen keys (lane & 7)
-      auto scales = [&](int slot) {
-        if (ww == 0 && slot >= 0) {
-          const int b = p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
-          ks = __ldg(p.k_scale + (int64_t)b * p.kv_heads + h);
-          vs = __ldg(p.v_scale + (int64_t)b * p.kv_heads + h);
-        }
-      };
-      float ref = 0.0f;
-      bool found = false, wide = false;
-      int slot = slot_of(tile0);
-      load(p.k, kc, tile0, slot);
-      load(p.v, vc, tile0, slot);
-      scales(slot);
-      int next = slot_of(tile0 + 1);
-      uint32_t t = tiles_done;
-      for (int tile = tile0; tile < tile1; ++tile, ++t) {
-        const uint32_t st = t & 1, ph = (t >> 1) & 1;
-        if (!__all_sync(0xffffffffu, bar_wait(k_empty + 8 * st, ph ^ 1, quit))) break;
-        store(base + L::kK + st * L::kOperand, kc);
-        if (lane == 0) bar_arrive(k_full + 8 * st);
-        if (ww == 0) {
-          // scales; the slot of four tiles before was read before this tile's place was free
-          const bool in = slot >= 0;
-          const float lv = log2f(vs);
-          const uint32_t fit = __ballot_sync(0xffffffffu, in && vs > 0.0f && vs <= FLT_MAX) & 0xFFu;
-          if (!found && fit) {
-            ref = __shfl_sync(0xffffffffu, lv, __ffs(fit) - 1);
-            found = true;
-          }
-          wide |= __any_sync(0xffffffffu, in && !(fabsf(lv - ref) <= 8.0f));
-          const uint32_t have = __ballot_sync(0xffffffffu, in) & 0xFFu;
-          Meta& d = meta[t & 3];
-          if (lane < 8) {
-            d.ks[lane] = in ? ks : 0.0f;
-            d.dl[lane] = in ? lv - ref : 0.0f;
-            d.inv[lane] = in ? exp2f(ref - lv) : 1.0f;
-          }
-          if (lane == 0) {
-            d.ref = ref;
-            d.in = have;
-            d.end = min(kTile, eff - tile * kTile);
-            d.wide = wide;
-          }
-          __syncwarp();
-          if (lane == 0) bar_arrive(m_full + 8 * (t & 3));
-        }
-        load(p.k, kc, tile + 1, next);
-        if (!__all_sync(0xffffffffu, bar_wait(v_empty + 8 * st, ph ^ 1, quit))) break;
-        store(base + L::kV + st * L::kOperand, vc);
-        if (lane == 0) bar_arrive(v_full + 8 * st);
-        load(p.v, vc, tile + 1, next);
-        scales(next);
-        slot = next;
-        next = slot_of(tile + 2);
-      }
-    } else if (warp == 12) {
-      // ---------------------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc_f16(kTile, kTile, false), kIdO = idesc_f16(kTile, DIM, true);
-        bool ok = true;
-        uint32_t turn[2] = {turns[0], turns[1]};
-        // the tile that stream b takes in its turn j, counted over all segments
-        auto tile_at = [&](int b, int j) { return tiles_done + (two ? j : 2 * j + b); };
-        auto scores = [&](int b, int j) {
-          const uint32_t t = tile_at(b, j), st = t & 1;
-          ok = ok && bar_wait(k_full + 8 * st, (t >> 1) & 1, quit);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t q = base + (two ? b : 0) * L::kOperand, k = base + L::kK + st * L::kOperand;
-#pragma unroll
-          for (int i = 0; i < DIM / 16; ++i) {
-            const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
-            mma_ss(tmem + b * kTile, sdesc(q + off, 16), sdesc(k + off, 16), kIdS, i > 0);
-          }
-          tc_commit(s_full + 8 * b);
-          if (!two || b == 1) tc_commit(k_empty + 8 * st);
-        };
-        auto sums = [&](int b, int j) {
-          const uint32_t t = tile_at(b, j), st = t & 1;
-          ok = ok && bar_wait(p_ready + 8 * b, turn[b] & 1, quit);
-          ++turn[b];
-          ok = ok && bar_wait(v_full + 8 * st, (t >> 1) & 1, quit);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t v = base + L::kV + st * L::kOperand;
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_ts(tmem + 2 * kTile + b * DIM, tmem + b * kTile + i * 8,
-                   sdesc(v + i * 2048, kTile * 128), kIdO, j > 0 || i > 0);
-          if (!two || b == 1) tc_commit(v_empty + 8 * st);
-        };
-        for (int b = 0; b < 2; ++b)
-          if (count[b] > 0) scores(b, 0);
-        for (int j = 0; j < count[0] && ok; ++j)
-          for (int b = 0; b < 2; ++b)
-            if (j < count[b] && ok) {
-              sums(b, j);
-              if (j + 1 < count[b] && ok) scores(b, j + 1);
-            }
-        tc_commit(done);  // all products issued above
-        bar_wait_through(done, segments & 1, quit);
-      }
-      __syncwarp();
-    } else if (warp < 8) {
-      // ---------------------------------------------------------------- softmax
-      const int b = warp >> 2;                 // stream
-      const int r = (warp & 3) * 32 + lane;    // row of the stream
-      const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t t_s = t_lane + b * kTile, t_o = t_lane + 2 * kTile + b * DIM;
-      const float mul = s_mul[two ? b * kTile + r : r];
-      // mo: the reference of o where scales lie far apart, else m
-      float m = kNone, mo = kNone, l = 0.0f, ref = 0.0f;
-      bool ok = true;
-      for (int j = 0; j < count[b]; ++j) {
-        const uint32_t t = tiles_done + (two ? j : 2 * j + b);
-        ok = bar_wait(s_full + 8 * b, (turns[b] + j) & 1, quit) &&
-             bar_wait(m_full + 8 * (t & 3), (t >> 2) & 1, quit);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        // The loops over parts of a row stay rolled: their code has to stay in the instruction
-        // cache beside that of the other roles
-        const Meta& d = meta[t & 3];
-        ref = d.ref;
-        if (d.in != 0xFFu || d.end != kTile) {  // keys that are not there
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t have = (d.in >> (2 * c) & 1 ? 0xFFFFu : 0u) | (d.in >> (2 * c + 1) & 1 ? 0xFFFF0000u : 0u);
-            const int left = d.end - c * 32;
-            if (left < 32) have &= left <= 0 ? 0u : (1u << left) - 1;
-            float v[32];
-            tmem_ld(t_s + c * 32, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(have >> i & 1)) v[i] = -INFINITY;
-            tmem_st(t_s + c * 32, v);
-          }
-          tmem_st_wait();
-        }
-        // a score times this is x; never 0, which would make a masked -infinity NaN
-        auto factor = [&](float ks) {
-          const float a = mul * ks;
-          return a == 0.0f ? FLT_MIN : a;
-        };
-        // references raised to kBelow below the maxima tm and to, sums with them
-        auto raise = [&](float tm, float to, bool apart) {
-          const bool up = tm > m + kRaise;
-          const float top = up ? tm - kBelow : m;
-          const float topo = !apart ? top : to > mo + kRaise ? to - kBelow : mo;
-          l *= exp2_fast(m - top);
-          const float keep = exp2_fast(mo - topo);
-          m = top;
-          mo = topo;
-          if (j == 0) return;
-          // the products of the tile before are finished: so are this tile's scores
-#pragma unroll 1
-          for (int c = 0; c < DIM / 32; ++c) {
-            float o[32];
-            tmem_ld(t_o + c * 32, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= keep;
-            tmem_st(t_o + c * 32, o);
-          }
-        };
-        if (!d.wide) {
-          float tm = -INFINITY;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const float4 ks = *reinterpret_cast<const float4*>(d.ks + half * 4);
-            const float4 dl = *reinterpret_cast<const float4*>(d.dl + half * 4);
-            float v[64];
-            tmem_ld(t_s + half * 64, v);
-            float x[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              x[c] = v[16 * c];
-#pragma unroll
-              for (int i = 1; i < 16; ++i) x[c] = fmaxf(x[c], v[16 * c + i]);
-            }
-            tm = fmaxf(tm, fmaxf(fmaxf(fmaf(x[0], factor(ks.x), dl.x), fmaf(x[1], factor(ks.y), dl.y)),
-                                 fmaxf(fmaf(x[2], factor(ks.z), dl.z), fmaf(x[3], factor(ks.w), dl.w))));
-          }
-          if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, tm, false);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const float4 ks4 = *reinterpret_cast<const float4*>(d.ks + half * 4);
-            const float4 dl4 = *reinterpret_cast<const float4*>(d.dl + half * 4);
-            const float4 inv4 = *reinterpret_cast<const float4*>(d.inv + half * 4);
-            const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, dl[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
-            const float inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
-            float v[64];
-            tmem_ld(t_s + half * 64, v);
-            uint32_t w[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float a = factor(ks[c]), z = dl[c] - m;
-              const uint64_t a2 = pack2(a, a), z2 = pack2(z, z);
-              uint64_t sum = pack2(0.0f, 0.0f);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 x = unpack2(fma2(pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]), a2, z2));
-                const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
-                sum = add2(sum, pack2(e0, e1));
-                w[8 * c + i] = pack_half(e0, e1);
-              }
-              const float2 both = unpack2(sum);
-              l = fmaf(both.x + both.y, inv[c], l);
-            }
-            tmem_st(t_s + half * 32, w);
-          }
-          mo = m;
-        } else {
-          float tm = -INFINITY, to = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            float v[16];
-            tmem_ld(t_s + c * 16, v);
-            float x = v[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) x = fmaxf(x, v[i]);
-            x *= factor(d.ks[c]);
-            tm = fmaxf(tm, x);
-            to = fmaxf(to, x + d.dl[c]);
-          }
-          if (__any_sync(0xffffffffu, tm > m + kRaise || to > mo + kRaise)) raise(tm, to, true);
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            const float a = factor(d.ks[c]), z = d.dl[c] - mo;
-            float v[16];
-            tmem_ld(t_s + c * 16, v);
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              l += exp2_fast(fmaf(v[2 * i], a, -m)) + exp2_fast(fmaf(v[2 * i + 1], a, -m));
-              w[i] = pack_half(exp2_fast(fmaf(v[2 * i], a, z)), exp2_fast(fmaf(v[2 * i + 1], a, z)));
-            }
-            tmem_st(t_s + c * 8, w);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(p_ready + 8 * b);
-      }
-      bar_wait_through(done, segments & 1, quit);
-      __syncwarp();
-      tc_fence_after();
-      // ---- this row's sums, joined with the other stream's where both have it
-      float* const meet = reinterpret_cast<float*>(smem + L::kK);  // [128][kLd]
-      const bool some = count[b] > 0;
-      const float mv = mo + ref;
-      if (!two) {
-        if (b == 1) {
-#pragma unroll 1
-          for (int c = 0; c < DIM / 32; ++c) {
-            float o[32];
-            if (some) {
-              tmem_ld(t_o + c * 32, o);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(meet + r * L::kLd + c * 32 + 4 * i) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          *reinterpret_cast<float4*>(meet + r * L::kLd + DIM) = make_float4(m, mv, l, 0.0f);
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-      }
-      if (two || b == 0) {
-        const int ur = two ? b * kTile + r : r;
-        const bool has = has_row(ur);
-        const int64_t row = has ? row_at(ur) : 0;
-        int ignored = 0;
-        const int g = (int)(row / p.group_rows);
-        // a row of length 0 attends to nothing, the prefix neither
-        const bool on =
-            has && row_len(p, (int)row, p.group_table ? __ldg(p.group_table + g) : g, &ignored) > 0;
-        float* const dst = whole ? P.before + (row * p.q_heads + head_at(ur)) * (DIM + 4)
-                                 : part + ur * DIM;
-        float* const stat = whole ? dst + DIM : part + Part<DIM, kPRows>::kStat + ur * 4;
-        float top = m, topv = mv, f0 = 1.0f, f1 = 0.0f;
-        if (!two) {
-          const float4 st = *reinterpret_cast<const float4*>(meet + r * L::kLd + DIM);
-          top = fmaxf(m, st.x);
-          topv = fmaxf(mv, st.y);
-          l = l * exp2_fast(m - top) + st.z * exp2_fast(st.x - top);
-          f0 = exp2_fast(mv - topv);
-          f1 = exp2_fast(st.y - topv);
-        }
-        if (has)
-          *reinterpret_cast<float4*>(stat) = on ? make_float4(top, topv, l, 0.0f)
-                                                : make_float4(kNone, kNone, 0.0f, 0.0f);
-#pragma unroll 1
-        for (int c = 0; c < DIM / 32; ++c) {
-          float o[32];
-          __syncwarp();
-          tmem_ld(t_o + c * 32, o);
-          if (has) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              if (!two) {
-                const float4 y =
-                    *reinterpret_cast<const float4*>(meet + r * L::kLd + c * 32 + 4 * i);
-                x.x = x.x * f0 + y.x * f1;
-                x.y = x.y * f0 + y.y * f1;
-                x.z = x.z * f0 + y.z * f1;
-                x.w = x.w * f0 + y.w * f1;
-              }
-              if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              *reinterpret_cast<float4*>(dst + c * 32 + 4 * i) = x;
-            }
-          }
-        }
-        __syncwarp();
-      }
+    if (tid == 0) {
+      const int lead = s_lead[set];
+      seg.table = p.block_table +
+                  (int64_t)(p.group_table ? __ldg(p.group_table + lead) : lead) * p.table_ld;
+      seg.part = P.parts + (2 * me + (i0 == 0)) * Part<DIM, kPRows>::kFloats;
+      seg.g0 = s_start[set];
+      seg.h = h;
+      seg.row0 = pair * kPRows;
+      seg.rows = rows;
+      seg.eff = s_eff[set];
+      seg.tile0 = tile0;
+      seg.tile1 = tile1;
+      seg.two = two;
+      seg.whole = whole;
+      seg.count[0] = count0;
+      seg.count[1] = count1;
+      seg.tiles_done = tiles_done;
+      seg.turns[0] = turns[0];
+      seg.turns[1] = turns[1];
+      seg.parity = segments & 1;
+      if (i0 == 0 && !whole)  // for the join
+        mine = {seg.g0, h, seg.row0, min(rows, seg.row0 + (two ? kPRows : kTile)), (int32_t)me,
+                (int32_t)(((w + steps) * n - 1) / all), {0, 0}};
     }
-    // ---- the unit's parts, for the join
-    if (i0 == 0 && !whole) {
-      const int64_t first_w = w - i0;
-      mine = {g0, h, row0, min(rows, row0 + (two ? kPRows : kTile)), (int32_t)me,
-              (int32_t)(((first_w + steps) * n - 1) / all), {0, 0}};
-    }
+    __syncthreads();
+    load_queries<DIM, FP16>(P, seg, base, s_mul);
+    __syncthreads();
+    if (warp >= 8) err |= widen_tiles<DIM>(P, seg, base, meta, bars, quit);
+    else stream_rows<DIM>(P, seg, base, smem, bars, tmem, quit);
     tiles_done += (uint32_t)(tile1 - tile0);
-    turns[0] += (uint32_t)count[0];
-    turns[1] += (uint32_t)count[1];
+    turns[0] += (uint32_t)count0;
+    turns[1] += (uint32_t)count1;
     ++segments;
     w += i1 - i0;
     tc_fence_before();
@@ -915,7 +1034,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
     if (s_quit) err |= KV8_STATUS_TIMEOUT;
   }
   if (err && p.status) atomicOr(p.status, err);
-  if (warp == 12)
+  if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
 }
