@@ -17,7 +17,7 @@
 // so that the products of one overlap the softmax of the other: they take the same keys for
 // different rows, or, where only 128 rows are left, the tiles of even and odd number for the
 // same rows (their sums are joined at the end).
-//   - Warps 8-11 read codes from the pages into registers a tile ahead, widen them to fp16
+//   - Warps 8-15 read codes from the pages into registers a tile ahead, widen them to fp16
 //     (exact) and store them in the 128-byte swizzle; keys as they lie (K-major), values as they
 //     lie too, as the transposed (MN-major) operand.
 //   - Warps 0-3 and 4-7 are the two streams, a thread to a row. The first thread of each issues
@@ -39,7 +39,8 @@
 namespace {
 
 constexpr int kTile = 128;      // keys of a tile, rows of a stream
-constexpr int kPThreads = 384;
+constexpr int kWidenWarps = 8;  // behind the eight of the streams
+constexpr int kPThreads = 256 + 32 * kWidenWarps;
 constexpr int kPRows = 2 * kTile;
 constexpr int kLeast = 128;     // positions of the least prefix that is read for all
 constexpr float kRaise = 15.0f, kBelow = 7.0f;  // log2, see above
@@ -392,7 +393,7 @@ __device__ __noinline__ void load_queries(const Prefix& P, const Segment& g, uin
   proxy_fence();
 }
 
-// Warps 8-11: codes of the segment's tiles into shared memory as fp16, and the tiles' scales.
+// Warps 8-15: codes of the segment's tiles into shared memory as fp16, and the tiles' scales.
 // Returns status bits.
 template <int DIM>
 __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint32_t base, Meta* meta,
@@ -408,7 +409,7 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
   const uint32_t tiles_done = g.tiles_done;
   int err = 0;
   const int ww = warp - 8;
-  constexpr int kKeysWarp = 32 / kPieces, kKeysPass = 4 * kKeysWarp, kPasses = kTile / kKeysPass;
+  constexpr int kKeysWarp = 32 / kPieces, kKeysPass = kWidenWarps * kKeysWarp, kPasses = kTile / kKeysPass;
   // 8 lanes that store together meet every bank once: 4 pieces of an even and an odd key
   const int piece = DIM == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3;
   const int key0 = ww * kKeysWarp +
@@ -482,7 +483,7 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
       for (int i = 0; i < kPasses; ++i) {
         const int key = i * kKeysPass + key0;
         const int s = __shfl_sync(0xffffffffu, here, lane0 + (key >> 4));
-        copy16(to + i * 2048, from + (int64_t)(max(s, 0) + (key & 15)) * stride, s >= 0 && key < left);
+        copy16(to + i * (512 * kWidenWarps), from + (int64_t)(max(s, 0) + (key & 15)) * stride, s >= 0 && key < left);
       }
     }
     copy_commit();
@@ -509,7 +510,7 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int key = i * kKeysPass + key0;
-      const uint4 c = lds128(from + i * 2048);
+      const uint4 c = lds128(from + i * (512 * kWidenWarps));
       uint32_t y[8];
       widen4(c.x, y[0], y[1]);
       widen4(c.y, y[2], y[3]);
@@ -867,13 +868,13 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(k_full + 8 * i, 4);
+      bar_init(k_full + 8 * i, kWidenWarps);
       bar_init(k_empty + 8 * i, 2);
       bar_init(s_full + 8 * i, 1);
       bar_init(p_ready + 8 * i, 4);
     }
     for (int i = 0; i < 4; ++i) bar_init(m_full + 8 * i, 1);
-    bar_init(v_full, 4);
+    bar_init(v_full, kWidenWarps);
     bar_init(v_empty, 2);
     bar_init(done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
