@@ -43,7 +43,8 @@ constexpr int kWidenWarps = 8;  // behind the eight of the streams
 constexpr int kPThreads = 256 + 32 * kWidenWarps;
 constexpr int kPRows = 2 * kTile;
 constexpr int kLeast = 128;     // positions of the least prefix that is read for all
-constexpr float kRaise = 15.0f, kBelow = 7.0f;  // log2, see above
+constexpr float kRaise = 11.0f, kBelow = 7.0f;  // log2: a reference is raised from here, to there
+constexpr float kMost = 32768.0f;  // of 16 weights together: 2^15, which is 2^kRaise for the largest
 constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
 
 // A unit whose parts CTAs first .. last have (last < 0: none).
@@ -242,40 +243,24 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[64]) {
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
-        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
-        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]),
-        "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]),
-        "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]),
-        "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
-        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]),
-        "=f"(v[62]), "=f"(v[63])
-      : "r"(at)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {"
       "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, "
+      "%33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, "
+      "%49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};"
       :
       : "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(v[32]), "r"(v[33]), "r"(v[34]),
+        "r"(v[35]), "r"(v[36]), "r"(v[37]), "r"(v[38]), "r"(v[39]), "r"(v[40]), "r"(v[41]),
+        "r"(v[42]), "r"(v[43]), "r"(v[44]), "r"(v[45]), "r"(v[46]), "r"(v[47]), "r"(v[48]),
+        "r"(v[49]), "r"(v[50]), "r"(v[51]), "r"(v[52]), "r"(v[53]), "r"(v[54]), "r"(v[55]),
+        "r"(v[56]), "r"(v[57]), "r"(v[58]), "r"(v[59]), "r"(v[60]), "r"(v[61]), "r"(v[62]),
+        "r"(v[63])
       : "memory");
 }
 
@@ -312,6 +297,27 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[8]) {
       : "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
         "r"(v[7])
       : "memory");
+}
+// The same in two steps: the registers are not to be touched before the wait, which is for all
+// loads of the thread.
+__device__ __forceinline__ void tmem_ld_start(uint32_t at, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -401,7 +407,7 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
   using L = PSmem<DIM>;
   constexpr int kPieces = DIM / 16;  // 16-byte pieces of a row of codes
   const Params& p = P.p;
-  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
   const uint32_t m_full = bars + 64;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile0 = g.tile0, tile1 = g.tile1, eff = g.eff, h = g.h;
@@ -498,7 +504,6 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
     const bool values = values_at(x);
     const int tile = tile_at(x);
     const uint32_t t = tiles_done + tile;
-    const uint32_t full = values ? v_full : k_full + 8 * (t & 1);
     const uint32_t empty = values ? v_empty : k_empty + 8 * (t & 1);
     const uint32_t turn = values ? t : t >> 1;
     if (g.two) copy_wait<L::kSlots - 1>();
@@ -521,7 +526,13 @@ __device__ __noinline__ int widen_tiles(const Prefix& P, const Segment& g, uint3
     }
     proxy_fence();
     __syncwarp();
-    if (lane == 0) bar_arrive(full);
+    if (lane == 0) {
+      // values: to the stream that takes them. (One barrier for both would let a stream that
+      // skips a tile take its phase for that of the tile before.)
+      if (!values) bar_arrive(k_full + 8 * (t & 1));
+      if (values && (g.two || (tile & 1) == 0)) bar_arrive(v_full);
+      if (values && (g.two || (tile & 1) == 1)) bar_arrive(v_full + 8);
+    }
     load(x + ring, slot);
     slot = slot == ring - 1 ? 0 : slot + 1;
     if (ww == 0 && !values) {
@@ -568,7 +579,7 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
                                          volatile int* quit) {
   using L = PSmem<DIM>;
   const Params& p = P.p;
-  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
   const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ratio = p.q_heads / p.kv_heads;
@@ -604,7 +615,7 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
   };
   auto issue_sums = [&](int j) {
     if (!bar_wait(p_ready + 8 * b, (turns + j) & 1, quit) ||
-        !bar_wait(v_full, tile_at(j) & 1, quit))
+        !bar_wait(v_full + 8 * b, (turns + j) & 1, quit))
       return;
     tc_fence_after();
     const uint32_t v = base + L::kV;
@@ -672,52 +683,53 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
       }
     };
     if (!d.wide) {
-      float tm = -INFINITY;
+      // The weights by the reference as it is. If sixteen of them pass kMost, some score lies 2^kRaise
+      // above it (as one of the first tile does): then the maxima are looked for, the references
+      // raised and the weights taken again. Otherwise no maximum is needed.
+      uint32_t w[64];
+      float add;
+      for (int again = j == 0;; ++again) {
+        if (again > 0) {
+          float tm = -INFINITY;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const float4 ks = *reinterpret_cast<const float4*>(d.ks + half * 4);
-        const float4 dl = *reinterpret_cast<const float4*>(d.dl + half * 4);
-        float v[64];
-        tmem_ld(t_s + half * 64, v);
-        float x[4];
+          for (int c = 0; c < 8; ++c) {
+            float v[16];
+            tmem_ld(t_s + c * 16, v);
+            float x = v[0];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[c] = v[16 * c];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) x[c] = fmaxf(x[c], v[16 * c + i]);
+            for (int i = 1; i < 16; ++i) x = fmaxf(x, v[i]);
+            tm = fmaxf(tm, fmaf(x, factor(d.ks[c]), d.dl[c]));
+          }
+          raise(tm, tm, false);
         }
-        tm = fmaxf(tm, fmaxf(fmaxf(fmaf(x[0], factor(ks.x), dl.x), fmaf(x[1], factor(ks.y), dl.y)),
-                             fmaxf(fmaf(x[2], factor(ks.z), dl.z), fmaf(x[3], factor(ks.w), dl.w))));
-      }
-      if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, tm, false);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const float4 ks4 = *reinterpret_cast<const float4*>(d.ks + half * 4);
-        const float4 dl4 = *reinterpret_cast<const float4*>(d.dl + half * 4);
-        const float4 inv4 = *reinterpret_cast<const float4*>(d.inv + half * 4);
-        const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, dl[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
-        const float inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
-        float v[64];
-        tmem_ld(t_s + half * 64, v);
-        uint32_t w[32];
+        add = 0.0f;
+        bool past = false;
+        float v[2][16];
+        tmem_ld_start(t_s, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float a = factor(ks[c]), z = dl[c] - m;
+        for (int c = 0; c < 8; ++c) {
+          const float a = factor(d.ks[c]), z = d.dl[c] - m;
           const uint64_t a2 = pack2(a, a), z2 = pack2(z, z);
           uint64_t sum = pack2(0.0f, 0.0f);
+          tmem_ld_wait(v[c & 1]);
+          if (c < 7) tmem_ld_start(t_s + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 x = unpack2(fma2(pack2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]), a2, z2));
+            const float2 x = unpack2(fma2(pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), a2, z2));
             const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
             sum = add2(sum, pack2(e0, e1));
             w[8 * c + i] = pack_half(e0, e1);
           }
           const float2 both = unpack2(sum);
-          l = fmaf(both.x + both.y, inv[c], l);
+          const float s16 = both.x + both.y;
+          past |= s16 > kMost;
+          add = fmaf(s16, d.inv[c], add);
         }
-        tmem_st(t_s + half * 32, w);
+        if (again > 0 || !__any_sync(0xffffffffu, past)) break;
       }
+      l += add;
       mo = m;
+      tmem_st(t_s, w);
     } else {
       float tm = -INFINITY, to = -INFINITY;
 #pragma unroll 1
@@ -857,9 +869,9 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   volatile int* const quit = &s_quit;
 
   const uint32_t bars = base + L::kBars;
-  // keys in place [2] and their places free [2], values the same, a tile's scales [4], a stream's
-  // scores [2] and weights [2], a segment's products
-  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 40;
+  // keys in place [2] and their places free [2], values in place for each stream [2] and their place
+  // free, a tile's scales [4], a stream's scores [2] and weights [2], a segment's products
+  const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
   const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -869,12 +881,12 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(k_full + 8 * i, kWidenWarps);
+      bar_init(v_full + 8 * i, kWidenWarps);
       bar_init(k_empty + 8 * i, 2);
       bar_init(s_full + 8 * i, 1);
       bar_init(p_ready + 8 * i, 4);
     }
     for (int i = 0; i < 4; ++i) bar_init(m_full + 8 * i, 1);
-    bar_init(v_full, kWidenWarps);
     bar_init(v_empty, 2);
     bar_init(done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
