@@ -42,7 +42,7 @@ enum {
   SAMPLE_OK = 0,
   SAMPLE_ERR_NULL = -1,   /* logits NULL (with rows > 0), tokens without uniforms, or neither
                              tokens nor probs */
-  SAMPLE_ERR_SHAPE = -2,  /* rows < 0 or > 2^27, vocab < 1 or > 2^22, a row stride below vocab,
+  SAMPLE_ERR_SHAPE = -2,  /* rows < 0 or > 2^27, vocab < 1 or > 2^20, a row stride below vocab,
                              param_rows < 1, dtype unknown */
   SAMPLE_ERR_ALIGN = -3,  /* an array not aligned to its elements */
   SAMPLE_ERR_CUDA = -4    /* the launch or a device query failed */

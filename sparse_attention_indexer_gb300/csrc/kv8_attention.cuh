@@ -253,6 +253,18 @@ __device__ __forceinline__ int tiles_of(int len) {
   return max(1, (int)(((uint32_t)len + kKeys - 1) / kKeys));
 }
 
+// What a unit counts when the work is divided: its tiles, and behind a shared prefix, where most
+// units are short, kUnitTiles for its start and end, which take as long (queries, the first
+// loads, the join of its warps, the prefix's part).
+#ifndef KV8_UNIT_TILES
+#define KV8_UNIT_TILES 16
+#endif
+constexpr int kUnitTiles = KV8_UNIT_TILES;
+template <bool TAIL>
+__device__ __forceinline__ int span_of(int len) {
+  return tiles_of(len) + (TAIL ? kUnitTiles : 0);
+}
+
 // 0xFF in each byte that is a NaN code.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
   return __vcmpeq4(c & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -362,12 +374,12 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     if (p.group_rows == 1) {  // all loads of eight rows on their way at once
 #pragma unroll 8
       for (int64_t i = g0; i < g1; ++i)
-        mine += tiles_of(behind<TAIL>(
+        mine += span_of<TAIL>(behind<TAIL>(
             p, (int)i,
             row_len(p, (int)i, p.group_table ? __ldg(p.group_table + i) : (int)i, &err)));
     } else {
 #pragma unroll 2
-      for (int64_t i = g0; i < g1; ++i) mine += tiles_of(group_len<TAIL>(p, (int)i, &err));
+      for (int64_t i = g0; i < g1; ++i) mine += span_of<TAIL>(group_len<TAIL>(p, (int)i, &err));
     }
     if (me) err = 0;  // CTA 0 reports for all
     int64_t before = mine, total = 0;
@@ -393,7 +405,7 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       int ignored = 0;
       int64_t i = g0, at = before * p.kv_heads;
       for (; i + 1 < g1; ++i) {
-        const int64_t here = (int64_t)tiles_of(group_len<TAIL>(p, (int)i, &ignored)) * p.kv_heads;
+        const int64_t here = (int64_t)span_of<TAIL>(group_len<TAIL>(p, (int)i, &ignored)) * p.kv_heads;
         if (w0 < at + here) break;
         at += here;
       }
@@ -406,9 +418,9 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
       g = s_group;
       first_tile = s_first;
       len = group_len<TAIL>(p, g, &ignored);
-      const int tiles = tiles_of(len);
-      h = (int)((w0 - first_tile) / tiles);
-      first_tile += (int64_t)h * tiles;
+      const int span = span_of<TAIL>(len);
+      h = (int)((w0 - first_tile) / span);
+      first_tile += (int64_t)h * span;
     }
   }
 
@@ -422,9 +434,11 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
   Shared mine = {0, 0, 0, -1};
   int64_t w = w0;
   while (w < w1) {
-    const int tiles = tiles_of(len);
-    const int tile0 = (int)(w - first_tile);
-    const int tile1 = (int)min((int64_t)tiles, w1 - first_tile);
+    const int tiles = tiles_of(len), span = span_of<TAIL>(len);
+    const int span1 = (int)min((int64_t)span, w1 - first_tile);
+    const int tile0 = max(0, (int)(w - first_tile) - (span - tiles));
+    const int tile1 = span1 - (span - tiles);
+    if (TAIL && tile1 <= 0) break;  // the range ends in what stands for the unit's start
     const int table = SELECTED ? 0 : p.group_table ? __ldg(p.group_table + g) : g;
     const int start = TAIL ? __ldg(p.start + g) : 0;  // positions of the prefix
 
@@ -927,16 +941,16 @@ kv8_attention_kernel(const __grid_constant__ Params p) {
     }
     if (tile0 == 0) {
       const Shared u = {g, h, (int32_t)me,
-                        whole ? -1 : (int32_t)(((first_tile + tiles) * n - 1) / all)};
+                        whole ? -1 : (int32_t)(((first_tile + span) * n - 1) / all)};
       if (units > kMaxCtas) mine = whole ? mine : u;
       else if (tid == 0) p.shared[(int64_t)g * p.kv_heads + h] = u;
     }
     __syncthreads();  // the shared arrays are free for the next unit
 
     // ---- next unit
-    w = first_tile + tile1;
+    w = first_tile + span1;
     if (tile1 == tiles) {
-      first_tile += tiles;
+      first_tile += span;
       if (++h == p.kv_heads) {
         h = 0;
         ++g;

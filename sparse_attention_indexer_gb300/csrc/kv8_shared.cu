@@ -101,7 +101,7 @@ struct PSmem {
   static constexpr int kLast = kCum + (KV8_MAX_SETS + 2) * 8;
   static_assert(kLast + KV8_MAX_SETS * 4 <= kMeta, "over keys, values and codes");
   static constexpr int kLd = DIM + 4;  // floats between rows where the streams' sums meet
-  static_assert(kK + kTile * kLd * 4 <= kMeta, "the sums fit over keys and values");
+  static_assert(kK + 2 * kTile * kLd * 4 <= kMeta, "the sums fit over keys, values and codes");
   static_assert(kMoreSlots * kHalf <= kOperand, "halves over the second queries");
   static_assert(kTotal <= 227 * 1024, "shared memory of an SM");
 };
@@ -350,7 +350,7 @@ struct __align__(16) Segment {
   }
 };
 
-// Queries, as kv8_attention.cuh brings them to fp16; a negative scale turns their sign.
+// Warps 0-7: the queries, as kv8_attention.cuh brings them to fp16; a negative scale turns their sign.
 template <int DIM, bool FP16>
 __device__ __noinline__ void load_queries(const Prefix& P, const Segment& g, uint32_t base,
                                           float* s_mul) {
@@ -358,7 +358,7 @@ __device__ __noinline__ void load_queries(const Prefix& P, const Segment& g, uin
   constexpr int kPieces = DIM / 16;
   const Params& p = P.p;
   const int tid = threadIdx.x, ratio = p.q_heads / p.kv_heads;
-  for (int x = tid; x < (g.two ? kPRows : kTile) * kPieces; x += kPThreads) {
+  for (int x = tid; x < (g.two ? kPRows : kTile) * kPieces; x += 256) {
     const int r = x / kPieces, c = x % kPieces;  // 16 channels from 16 c
     uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (g.has_row(p, ratio, r)) {
@@ -772,77 +772,78 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
   bar_wait_through(done, g.parity, quit);
   __syncwarp();
   tc_fence_after();
-  // ---- this row's sums, joined with the other stream's where both have it
-  float* const meet = reinterpret_cast<float*>(smem + L::kK);  // [128][kLd]
-  const bool some = count > 0;
-  const float mv = mo + ref;
-  if (!two) {
-    if (b == 1) {
+  // ---- the rows' sums, through shared memory (keys and values are done with), so that a warp
+  // writes a row at a time: a thread that writes its own row takes 15 us here
+  float* const meet = reinterpret_cast<float*>(smem + L::kK) + b * kTile * L::kLd;
 #pragma unroll 1
-      for (int c = 0; c < DIM / 32; ++c) {
-        float o[32];
-        if (some) {
-          tmem_ld(t_o + c * 32, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(meet + r * L::kLd + c * 32 + 4 * i) =
-              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
-      *reinterpret_cast<float4*>(meet + r * L::kLd + DIM) = make_float4(m, mv, l, 0.0f);
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-  }
-  if (two || b == 0) {
-    const int ur = two ? b * kTile + r : r;
-    const bool has = g.has_row(p, ratio, ur);
-    const int64_t row = has ? g.row_at(p, ratio, ur) : 0;
-    int ignored = 0;
-    const int gr = (int)(row / p.group_rows);
-    // a row of length 0 attends to nothing, the prefix neither
-    const bool on =
-        has && row_len(p, (int)row, p.group_table ? __ldg(p.group_table + gr) : gr, &ignored) > 0;
-    float* const dst = g.whole ? P.before + (row * p.q_heads + g.head_at(ratio, ur)) * (DIM + 4)
-                             : g.part + ur * DIM;
-    float* const stat = g.whole ? dst + DIM : g.part + Part<DIM, kPRows>::kStat + ur * 4;
-    float top = m, topv = mv, f0 = 1.0f, f1 = 0.0f;
-    if (!two) {
-      const float4 st = *reinterpret_cast<const float4*>(meet + r * L::kLd + DIM);
-      top = fmaxf(m, st.x);
-      topv = fmaxf(mv, st.y);
-      l = l * exp2_fast(m - top) + st.z * exp2_fast(st.x - top);
-      f0 = exp2_fast(mv - topv);
-      f1 = exp2_fast(st.y - topv);
-    }
-    if (has)
-      *reinterpret_cast<float4*>(stat) = on ? make_float4(top, topv, l, 0.0f)
-                                            : make_float4(kNone, kNone, 0.0f, 0.0f);
-#pragma unroll 1
-    for (int c = 0; c < DIM / 32; ++c) {
-      float o[32];
-      __syncwarp();
+  for (int c = 0; c < DIM / 32; ++c) {
+    float o[32];
+    if (count > 0) {
       tmem_ld(t_o + c * 32, o);
-      if (has) {
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          if (!two) {
-            const float4 y =
-                *reinterpret_cast<const float4*>(meet + r * L::kLd + c * 32 + 4 * i);
-            x.x = x.x * f0 + y.x * f1;
-            x.y = x.y * f0 + y.y * f1;
-            x.z = x.z * f0 + y.z * f1;
-            x.w = x.w * f0 + y.w * f1;
-          }
-          if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          *reinterpret_cast<float4*>(dst + c * 32 + 4 * i) = x;
-        }
-      }
+      for (int i = 0; i < 32; ++i) o[i] = 0.0f;
     }
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(meet + r * L::kLd + c * 32 + 4 * i) =
+          make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  }
+  *reinterpret_cast<float4*>(meet + r * L::kLd + DIM) = make_float4(m, mo + ref, l, 0.0f);
+  // this warp's rows: its own 32, or 16 of those that the streams have together
+  if (two) __syncwarp();
+  else asm volatile("bar.sync 1, 256;" ::: "memory");
+  const int n = two ? 32 : 16;
+  const int r0 = two ? (warp & 3) * 32 : warp * 16;
+  const float* const s0 =
+      reinterpret_cast<const float*>(smem + L::kK) + (two ? b * kTile * L::kLd : 0) + r0 * L::kLd;
+  const float* const s1 = s0 + kTile * L::kLd;  // the other stream's
+  float f0 = 1.0f, f1 = 0.0f;
+  float* dst = nullptr;  // of row r0 + lane; null: there is none
+  if (lane < n) {
+    const int ur = two ? b * kTile + r0 + lane : r0 + lane;
+    if (g.has_row(p, ratio, ur)) {
+      const int64_t row = g.row_at(p, ratio, ur);
+      const int gr = (int)(row / p.group_rows);
+      int ignored = 0;
+      // a row of length 0 attends to nothing, the prefix neither
+      const bool on =
+          row_len(p, (int)row, p.group_table ? __ldg(p.group_table + gr) : gr, &ignored) > 0;
+      dst = g.whole ? P.before + (row * p.q_heads + g.head_at(ratio, ur)) * (DIM + 4)
+                    : g.part + ur * DIM;
+      float4 st = *reinterpret_cast<const float4*>(s0 + lane * L::kLd + DIM);
+      if (!two) {
+        const float4 x = *reinterpret_cast<const float4*>(s1 + lane * L::kLd + DIM);
+        const float top = fmaxf(st.x, x.x), topv = fmaxf(st.y, x.y);
+        f0 = exp2_fast(st.y - topv);
+        f1 = exp2_fast(x.y - topv);
+        st.z = st.z * exp2_fast(st.x - top) + x.z * exp2_fast(x.x - top);
+        st.x = top;
+        st.y = topv;
+      }
+      if (!on) {
+        st = make_float4(kNone, kNone, 0.0f, 0.0f);
+        f0 = -1.0f;  // marks it
+      }
+      float* const stat = g.whole ? dst + DIM : g.part + Part<DIM, kPRows>::kStat + ur * 4;
+      *reinterpret_cast<float4*>(stat) = st;
+    }
+  }
+  constexpr int kLanes = DIM / 4;  // of a row
+  const int sub = lane / kLanes, c4 = lane % kLanes;
+#pragma unroll 4
+  for (int i = 0; i < n; i += 32 / kLanes) {
+    const int k = i + sub;
+    float* const to = reinterpret_cast<float*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), k));
+    const float a = __shfl_sync(0xffffffffu, f0, k), c = __shfl_sync(0xffffffffu, f1, k);
+    float4 x = *reinterpret_cast<const float4*>(s0 + k * L::kLd + c4 * 4);
+    if (!two) {
+      const float4 y = *reinterpret_cast<const float4*>(s1 + k * L::kLd + c4 * 4);
+      x = make_float4(x.x * a + y.x * c, x.y * a + y.y * c, x.z * a + y.z * c, x.w * a + y.w * c);
+    }
+    if (a < 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (to) *reinterpret_cast<float4*>(to + c4 * 4) = x;
   }
 }
 
@@ -1028,10 +1029,13 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
                 (int32_t)(((w + steps) * n - 1) / all), {0, 0}};
     }
     __syncthreads();
-    load_queries<DIM, FP16>(P, seg, base, s_mul);
-    __syncthreads();
-    if (warp >= 8) err |= widen_tiles<DIM>(P, seg, base, meta, bars, quit);
-    else stream_rows<DIM>(P, seg, base, smem, bars, tmem, quit);
+    if (warp >= 8) {
+      err |= widen_tiles<DIM>(P, seg, base, meta, bars, quit);
+    } else {  // while the first codes are on their way
+      load_queries<DIM, FP16>(P, seg, base, s_mul);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      stream_rows<DIM>(P, seg, base, smem, bars, tmem, quit);
+    }
     tiles_done += (uint32_t)(tile1 - tile0);
     turns[0] += (uint32_t)count0;
     turns[1] += (uint32_t)count1;

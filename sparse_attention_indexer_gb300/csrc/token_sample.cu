@@ -22,6 +22,8 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kMaxCluster = 8;
+constexpr int kBins = 512;   // of 16 in z: 1 / 32 of a power of two
+constexpr int kList = 4 * kBins;  // tokens that one CTA searches, in the place of the bins
 
 struct Params {
   const void* logits;
@@ -113,7 +115,7 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 }
 
 template <typename T, int THREADS, bool STAGED>
-__global__ void __launch_bounds__(THREADS) token_sample_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_constant__ Params p) {
   constexpr int kWarps = THREADS / 32, kN = Piece<T>::kN;
   extern __shared__ __align__(16) uint8_t s_stage[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -122,6 +124,10 @@ __global__ void __launch_bounds__(THREADS) token_sample_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ uint64_t s_a[kWarps], s_b[kWarps];
   __shared__ uint64_t s_cta[2][2];  // read by the cluster, in turn
+  __shared__ uint32_t s_bins[4][kBins];  // weights in digits of 13, 13 and 14 bits; tokens
+  __shared__ uint32_t s_n;
+  uint32_t* const s_list = &s_bins[0][0];
+  __shared__ uint64_t s_found[5];
   int turn = 0, err = 0;
 
   // ---- the row's settings
@@ -201,6 +207,7 @@ __global__ void __launch_bounds__(THREADS) token_sample_kernel(const __grid_cons
     turn ^= 1;
   };
 
+  if (tid == 0) s_n = 0;
   // ---- the maximum
   float top = -INFINITY;
   for (int s = 0; s < steps; ++s) {
@@ -232,79 +239,276 @@ __global__ void __launch_bounds__(THREADS) token_sample_kernel(const __grid_cons
   // ---- thresholds: kept are the tokens above `cut` and the first `ties` of those that have it
   uint32_t cut = 0;
   uint64_t ties = 0;
-  // the largest key with F(key) >= target, F(key) the count or the weight of the tokens from
-  // it on; `above` becomes F(key + 1)
-  auto search = [&](bool count, uint64_t target, uint64_t& above) {
-    uint32_t key = 0;
-    above = 0;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-      uint64_t a = 0, b = 0;
-      for (int s = 0; s < steps; ++s) {
-        const Piece<T> x = piece(s);
+  auto logit_of = [](uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); };
+  auto each = [&](auto&& f) {
+    for (int s = 0; s < steps; ++s) {
+      const Piece<T> x = piece(s);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float y = to_float(x.x[i]);
-          if (key_of(y) >= (key | bit)) {
-            const uint64_t w = weight_of(z_of(y));
-            a += count ? (w != 0) : w;
-          }
+      for (int i = 0; i < kN; ++i) f(to_float(x.x[i]));
+    }
+  };
+  // Which bin of z, in the order of the tokens, brings the count (or weight) of the tokens up to
+  // and with it to `target`, which all tokens together reach: rounds of 16 in z, most rows need
+  // one. `before` becomes the count (weight) of the bins before it, `inside` its tokens.
+  bool used = false;  // the bins: others may still be reading them
+  auto find_bin = [&](bool count, uint64_t target, uint64_t& before, uint64_t& inside) {
+    before = 0;
+    for (int round = 0;; ++round) {
+      if (used) cluster.sync();
+      used = true;
+      for (int b = tid; b < kBins * 4; b += THREADS) s_bins[b / kBins][b % kBins] = 0;
+      if (tid == 0) s_found[0] = ~uint64_t(0);
+      __syncthreads();
+      const float z0 = round * 16.0f;
+      each([&](float y) {
+        const float z = z_of(y) - z0;
+        if (!(z >= 0.0f && z < 16.0f) || z + z0 >= 41.0f) return;
+        const int b = (int)(z * (kBins / 16));
+        if (count) {
+          // a weight of 0 is no token: z may come close to 41 or pass 40 without one
+          if (z + z0 < 40.0f || weight_of(z + z0)) atomicAdd(&s_bins[3][b], 1u);
+        } else {
+          const uint64_t w = weight_of(z + z0);
+          const uint32_t w0 = (uint32_t)w & 0x1FFFu, w1 = (uint32_t)(w >> 13) & 0x1FFFu;
+          const uint32_t w2 = (uint32_t)(w >> 26);
+          if (w0) atomicAdd(&s_bins[0][b], w0);
+          if (w1) atomicAdd(&s_bins[1][b], w1);
+          if (w2) atomicAdd(&s_bins[2][b], w2);
+          if (w) atomicAdd(&s_bins[3][b], 1u);
         }
+      });
+      cluster.sync();
+      // every CTA finds it for itself: thread t sums bins t * kEach ..
+      constexpr int kEach = kBins / THREADS;
+      uint64_t value[kEach], mine = 0;
+      uint32_t tokens[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int b = tid * kEach + e;
+        uint64_t a[4] = {};
+        for (int r = 0; r < ranks; ++r) {
+          const uint32_t* h = cluster.map_shared_rank(&s_bins[0][0], r);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            if (d == 3 || !count) a[d] += h[d * kBins + b];
+        }
+        tokens[e] = (uint32_t)a[3];
+        value[e] = count ? a[3] : a[0] + (a[1] << 13) + (a[2] << 26);
+        mine += value[e];
       }
-      reduce(a, b);
+      uint64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_a[warp] = incl;
+      __syncthreads();
+      uint64_t at = before + incl - mine, all = before;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) at += s_a[w];
+        all += s_a[w];
+      }
+      if (at < target && target <= at + mine) {
+        int e = 0;
+        while (at + value[e] < target) at += value[e++];
+        s_found[0] = round * kBins + tid * kEach + e;
+        s_found[1] = at;
+        s_found[2] = tokens[e];
+      }
+      __syncthreads();
+      const uint64_t found = s_found[0];
+      if (found != ~uint64_t(0) || round == 2) {
+        before = s_found[1];
+        inside = s_found[2];
+        return (int)found;
+      }
+      before = all;
+    }
+  };
+  auto bin_of = [&](float z) {  // as find_bin counts them; past the last for a token that weighs 0
+    if (!(z < 41.0f) || (z >= 40.0f && !weight_of(z))) return 3 * kBins;
+    const int round = (int)(z * (1.0f / 16.0f));
+    return round * kBins + (int)((z - round * 16.0f) * (kBins / 16));
+  };
+  // The largest key among the tokens of bins [b0, b1] with F(key) >= target, F(key) the count or the
+  // weight of these tokens from it on; `above` becomes F(key + 1). They are gathered by the
+  // first CTA where they fit its list; else all CTAs search them where they are. `first` and
+  // `second` searches of the same list: a count k, then the weight target(weight of the first k).
+  auto gather = [&](int b0, int b1) {
+    cluster.sync();  // all have read the bins
+    uint32_t* const n = cluster.map_shared_rank(&s_n, 0);
+    uint32_t* const list = cluster.map_shared_rank(s_list, 0);
+    each([&](float y) {
+      const int b = bin_of(z_of(y));
+      if (b >= b0 && b <= b1) {
+        const uint32_t at = atomicAdd(n, 1u);
+        if (at < kList) list[at] = key_of(y);
+      }
+    });
+    cluster.sync();
+  };
+  // ---- searches: bit by bit from the top, with `sum` to add up over the tokens
+  // (bits of `low` and `high`, the least and the largest key, that are the same need no search)
+  auto search = [&](auto&& sum, uint64_t target, uint64_t& above, uint32_t low = 0,
+                    uint32_t high = 0xFFFFFFFFu) {
+    const int bits = 32 - __clz(low ^ high);
+    uint32_t key = bits == 32 ? 0 : high >> bits << bits;
+    above = 0;
+    for (uint32_t bit = bits ? 1u << (bits - 1) : 0u; bit; bit >>= 1) {
+      const uint64_t a = sum(key | bit);
       if (a >= target) key |= bit;
       else above = a;
     }
     return key;
   };
+  auto in_list = [&](bool count, int n) {  // by the first CTA alone
+    return [&, count, n](uint32_t key) {
+      uint64_t a = 0;
+      for (int i = tid; i < n; i += THREADS) {
+        const uint32_t k = s_list[i];
+        if (k >= key) a += count ? 1 : weight_of(z_of(logit_of(k)));
+      }
+      a = warp_sum(a);
+      __syncthreads();
+      if (lane == 0) s_a[warp] = a;
+      __syncthreads();
+      a = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) a += s_a[w];
+      return a;
+    };
+  };
+  auto ends = [&](int n, uint32_t& low, uint32_t& high) {  // of the list
+    low = 0xFFFFFFFFu;
+    high = 0;
+    for (int i = tid; i < n; i += THREADS) {
+      low = min(low, s_list[i]);
+      high = max(high, s_list[i]);
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    __syncthreads();
+    if (lane == 0) s_a[warp] = (uint64_t)low << 32 | high;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      low = min(low, (uint32_t)(s_a[w] >> 32));
+      high = max(high, (uint32_t)s_a[w]);
+    }
+  };
+  auto everywhere = [&](bool count, int b0, int b1) {  // by all
+    return [&, count, b0, b1](uint32_t key) {
+      uint64_t a = 0, b = 0;
+      each([&](float y) {
+        if (key_of(y) >= key) {
+          const float z = z_of(y);
+          const int bin = bin_of(z);
+          if (bin >= b0 && bin <= b1) a += count ? 1 : weight_of(z);
+        }
+      });
+      reduce(a, b);
+      return a;
+    };
+  };
+  auto share = [&] {  // what the first CTA found
+    if (rank == 0 && tid == 0) {
+      s_found[3] = cut;
+      s_found[4] = ties;
+    }
+    cluster.sync();
+    const uint64_t* f = cluster.map_shared_rank(s_found, 0);
+    cut = (uint32_t)f[3];
+    ties = f[4];
+  };
+  auto weight_at = [&](uint32_t key) { return weight_of(z_of(logit_of(key))); };
+  auto target_of = [&](uint64_t total) {
+    return top_p > 0.0f ? max(part_of(top_p, total, true), uint64_t(1)) : uint64_t(1);
+  };
   if (greedy || none) {
     cut = key_of(top);
     ties = none ? 0 : 1;
   } else {
-    // the weights of all tokens, and how many weigh something: only these can be kept
-    uint64_t total = 0, some = 0;
     const bool by_p = top_p < 1.0f;
-    if (by_p || top_k > 0) {
-      for (int s = 0; s < steps; ++s) {
-        const Piece<T> x = piece(s);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint64_t w = weight_of(z_of(to_float(x.x[i])));
+    bool by_k = top_k > 0 && top_k < p.vocab;
+    uint64_t total = 0, some = 0;
+    if (by_k || by_p) {
+      // the weight of all tokens, and how many weigh something: only these can be kept
+      each([&](float y) {
+        const float z = z_of(y);
+        if (z < 41.0f) {
+          const uint64_t w = by_p || z >= 40.0f ? weight_of(z) : 1;
           total += w;
           some += w != 0;
         }
-      }
+      });
       reduce(total, some);
+      by_k = by_k && top_k < some;
     }
-    if (top_k > 0 && top_k < some) {
-      uint64_t above;
-      cut = search(true, top_k, above);
-      ties = top_k - above;
-      if (by_p) {
-        total = 0;
-        for (int s = 0; s < steps; ++s) {
-          const Piece<T> x = piece(s);
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const float y = to_float(x.x[i]);
-            if (key_of(y) > cut) total += weight_of(z_of(y));
+    bool done = false;
+    if (by_k) {
+      uint64_t before, inside;
+      const int b = find_bin(true, top_k, before, inside);
+      const bool all = before + inside <= kList;  // all that top-k can keep fit the list
+      uint64_t above = 0;
+      if (inside <= kList) {
+        gather(all ? 0 : b, b);
+        if (rank == 0) {
+          const int n = (int)(all ? before + inside : inside);
+          uint32_t low, high;
+          ends(n, low, high);
+          cut = search(in_list(true, n), all ? (uint64_t)top_k : top_k - before, above, low, high);
+          ties = top_k - above - (all ? 0 : before);
+          if (all && by_p) {
+            uint64_t w = weight_at(cut);
+            const uint64_t kept = in_list(false, n)(cut + 1) + ties * w;
+            const uint64_t target = target_of(kept);
+            cut = search(in_list(false, n), target, above, low, high);
+            w = weight_at(cut);
+            ties = (target - above + w - 1) / w;
           }
         }
+        share();
+        done = all;
+      } else {
+        cut = search(everywhere(true, b, b), top_k - before, above);
+        ties = top_k - before - above;
+      }
+      if (!done && by_p) {  // the weight of the first k
+        total = 0;
+        each([&](float y) {
+          if (key_of(y) > cut) total += weight_of(z_of(y));
+        });
         uint64_t ignored = 0;
         reduce(total, ignored);
-        total += ties * weight_of(z_of(__uint_as_float(cut & 0x80000000u ? cut & 0x7FFFFFFFu : ~cut)));
+        total += ties * weight_at(cut);
       }
     }
-    if (by_p) {
-      const uint64_t target = top_p > 0.0f ? max(part_of(top_p, total, true), uint64_t(1)) : 1;
-      uint64_t above;
-      cut = search(false, target, above);
-      const uint64_t w = weight_of(z_of(__uint_as_float(cut & 0x80000000u ? cut & 0x7FFFFFFFu : ~cut)));
-      ties = (target - above + w - 1) / w;
+    if (by_p && !done) {
+      const uint64_t target = target_of(total);
+      uint64_t before, inside, above = 0;
+      const int b = find_bin(false, target, before, inside);
+      if (inside <= kList) {
+        if (tid == 0) s_n = 0;  // before all meet in the gathering
+        gather(b, b);
+        if (rank == 0) {
+          uint32_t low, high;
+          ends((int)inside, low, high);
+          cut = search(in_list(false, (int)inside), target - before, above, low, high);
+          const uint64_t w = weight_at(cut);
+          ties = (target - before - above + w - 1) / w;
+        }
+        share();
+      } else {
+        cut = search(everywhere(false, b, b), target - before, above);
+        const uint64_t w = weight_at(cut);
+        ties = (target - before - above + w - 1) / w;
+      }
     }
   }
   const uint64_t tie_weight =
       greedy || none ? uint64_t(1) << 40
-                     : weight_of(z_of(__uint_as_float(cut & 0x80000000u ? cut & 0x7FFFFFFFu : ~cut)));
+                     : weight_at(cut);
   if (tie_weight < least && !greedy) ties = 0;
   // the weight of a token above the cut
   auto strict = [&](float y) {
@@ -431,13 +635,24 @@ __global__ void __launch_bounds__(THREADS) token_sample_kernel(const __grid_cons
       }
       uint64_t rank_of = seen + scan - lane_ties;
       seen += __shfl_sync(0xffffffffu, scan, 31);
+      float prob[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const float y = to_float(x.x[i]);
         uint64_t w;
         if (key_of(y) == cut) w = rank_of++ < ties ? tie_weight : 0;
         else w = strict(y);
-        if (v + i >= 0 && v + i < p.vocab) out[v + i] = (float)w * 0x1p-40f * f;
+        prob[i] = (float)w * 0x1p-40f * f;
+      }
+      if (v >= 0 && v + kN <= p.vocab && (reinterpret_cast<uintptr_t>(out + v) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4)
+          __stcs(reinterpret_cast<float4*>(out + v + i),
+                 make_float4(prob[i], prob[i + 1], prob[i + 2], prob[i + 3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (v + i >= 0 && v + i < p.vocab) out[v + i] = prob[i];
       }
     }
   }
@@ -502,7 +717,8 @@ int run(Params& p, int rows, int dev, int sms, cudaStream_t s) {
   int ranks = kMaxCluster;
   while (ranks > 1 && p.vocab <= ranks / 2 * kPass) ranks >>= 1;
   // a row that starts off a 16-byte boundary covers up to kN - 1 places more
-  const int64_t places = (int64_t)p.vocab + Piece<T>::kN - 1;
+  const bool off = !aligned(p.logits, 16) || (rows > 1 && p.ld % Piece<T>::kN);
+  const int64_t places = (int64_t)p.vocab + (off ? Piece<T>::kN - 1 : 0);
   p.steps = (int)((places + (int64_t)ranks * kPass - 1) / ((int64_t)ranks * kPass));
   const int64_t stage = (int64_t)p.steps * kThreads * 16;
   if (stage <= kMaxStage) return launch<T, kThreads, true>(p, rows, ranks, (int)stage, dev, s);
@@ -516,7 +732,7 @@ extern "C" int token_sample(const void* logits, int64_t ld, int dtype, int rows,
                             const float* min_p, int param_rows, const float* uniforms,
                             int32_t* tokens, float* probs, int64_t probs_ld, int32_t* status,
                             sample_stream_t stream) {
-  if (rows < 0 || rows > (1 << 27) || vocab < 1 || vocab > (1 << 22) || ld < vocab ||
+  if (rows < 0 || rows > (1 << 27) || vocab < 1 || vocab > (1 << 20) || ld < vocab ||
       param_rows < 1 || (dtype != SAMPLE_BF16 && dtype != SAMPLE_FP16 && dtype != SAMPLE_FP32) ||
       (probs && probs_ld < vocab))
     return SAMPLE_ERR_SHAPE;
