@@ -139,3 +139,69 @@ def copy(src, dst, planes, n_pages):
         for x in planes:
             x[d] = x[s]
     return status
+
+
+TOKENS = 64
+
+
+def step(rows, old, new, table, page, num_pages, tokens, mutant=0):
+    """(positions, token_table, slots, lens, starts, status) of a step's tokens, one after
+    another. `mutant` 6: padding rows are row 0; 7: a token's length leaves itself out."""
+    got = [[], [], [], []]
+    starts, status = [0], 0
+    for r, a, b in zip(rows, old, new):
+        if not 0 <= r < table.shape[0]:
+            status |= ROW
+        elif a < 0 or b < a or b > table.shape[1] * page:
+            status |= LEN
+        else:
+            for pos in range(a, b):
+                if len(got[0]) == tokens:
+                    status |= TOKENS
+                    break
+                e = int(table[r, pos // page])
+                slot = -1
+                if e < 0:
+                    status |= NO_PAGE
+                elif e >= num_pages:
+                    status |= PAGE
+                else:
+                    slot = e * page + pos % page
+                for x, y in zip(got, (pos, r, slot, pos + (mutant != 7))):
+                    x.append(y)
+        starts.append(len(got[0]))
+    rest = tokens - len(got[0])
+    for x, y in zip(got, (-1, 0 if mutant == 6 else -1, -1, 0)):
+        x += [y] * rest
+    return tuple(np.asarray(x, np.int32) for x in got) + (np.asarray(starts, np.int32), status)
+
+
+def shared(rows, lens, starts, table, page, num_pages, mutant=0):
+    """(prefix lengths, status). `mutant` 8: rows of length 0 count too."""
+    out, status = [], 0
+    for a, b in zip(starts, starts[1:]):
+        if not 0 <= a <= b <= len(rows):
+            status |= LEN
+            out.append(0)
+            continue
+        live, bad = [], False
+        for r, n in zip(rows[a:b], lens[a:b]):
+            if n == 0 and mutant != 8:
+                continue
+            if not 0 <= r < table.shape[0]:
+                status |= ROW
+                bad = True
+            elif n < 0 or n > table.shape[1] * page:
+                status |= LEN
+                bad = True
+            else:
+                live.append((r, n))
+        pages = 0
+        if len(live) > 1 and not bad:
+            for c in range(min(n for _, n in live) // page):
+                ids = {int(table[r, c]) for r, _ in live}
+                if len(ids) > 1 or not 0 <= min(ids) < num_pages:
+                    break
+                pages += 1
+        out.append(pages * page)
+    return np.asarray(out, np.int32), status

@@ -73,18 +73,65 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// P(f) * 2^24 and n of a z < 41: the weight is (P << 16) >> n. The header's steps, none fused.
+// Two floats to an operation, rounded to nearest each; products and sums are not fused.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// a * b + c with two roundings: the sum as 1 * (a * b) + c, since ptxas fuses mul.rn.f32x2 and
+// add.rn.f32x2 into one operation (3.2 of 8.4 million pairs of f then have other weights).
+__device__ __forceinline__ uint64_t mul_add2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(mul2(a, b)), "l"(pack2(1.0f, 1.0f)), "l"(c));
+  return d;
+}
+
+// The weights of two z in [0, 41], by the header's steps (41 gives 0). Neither floor nor weight
+// is converted: z + 2^23 rounded down has floor(z) in its low bits, and P in [1/2, 1] has its 24
+// bits in its significand: the weight is (significand << 17) >> (n + 1), or >> n where P is 1.
+__device__ __forceinline__ void weights2(float z0, float z1, uint64_t& w0, uint64_t& w1) {
+  const float t0 = __fadd_rd(z0, 0x1p23f), t1 = __fadd_rd(z1, 0x1p23f);
+  const uint64_t n = add2(pack2(t0, t1), pack2(-0x1p23f, -0x1p23f));
+  const float2 nf = unpack2(n);
+  const uint64_t f = pack2(z0 - nf.x, z1 - nf.y);
+  auto both = [](float c) { return pack2(c, c); };
+  uint64_t y = both(0x1.c946d2p-14f);
+  y = mul_add2(y, f, both(-0x1.4e2aeap-10f));
+  y = mul_add2(y, f, both(0x1.39e3fcp-7f));
+  y = mul_add2(y, f, both(-0x1.c6948ep-5f));
+  y = mul_add2(y, f, both(0x1.ebfacp-3f));
+  y = mul_add2(y, f, both(-0x1.62e42cp-1f));
+  y = mul_add2(y, f, both(1.0f));
+  const float2 p = unpack2(y);
+  auto whole = [](float p, float t) {
+    const uint32_t b = __float_as_uint(p);
+    const int down = (int)(__float_as_uint(t) & 63) + 127 - (int)(b >> 23);
+    return ((uint64_t)((b & 0x7FFFFFu) | 0x800000u) << 17) >> down;
+  };
+  w0 = whole(p.x, t0);
+  w1 = whole(p.y, t1);
+}
 __device__ __forceinline__ uint64_t weight_of(float z) {
-  if (!(z < 41.0f)) return 0;
-  const float n = floorf(z), f = z - n;
-  float y = 0x1.c946d2p-14f;
-  y = __fadd_rn(__fmul_rn(y, f), -0x1.4e2aeap-10f);
-  y = __fadd_rn(__fmul_rn(y, f), 0x1.39e3fcp-7f);
-  y = __fadd_rn(__fmul_rn(y, f), -0x1.c6948ep-5f);
-  y = __fadd_rn(__fmul_rn(y, f), 0x1.ebfacp-3f);
-  y = __fadd_rn(__fmul_rn(y, f), -0x1.62e42cp-1f);
-  y = __fadd_rn(__fmul_rn(y, f), 1.0f);
-  return ((uint64_t)(uint32_t)(y * 0x1p24f) << 16) >> (int)n;
+  uint64_t a, b;
+  weights2(fminf(z, 41.0f), 41.0f, a, b);
+  return a;
 }
 
 // floor (or ceil) of r * total, r in [0, 1): the significand times total, 88 bits, moved down.
@@ -115,7 +162,7 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 }
 
 template <typename T, int THREADS, bool STAGED>
-__global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(const __grid_constant__ Params p) {
   constexpr int kWarps = THREADS / 32, kN = Piece<T>::kN;
   extern __shared__ __align__(16) uint8_t s_stage[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -234,25 +281,44 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
   const bool none = top == -INFINITY;
   if (none) err |= SAMPLE_STATUS_EMPTY;
   const bool greedy = temp == 0.0f;
-  auto z_of = [&](float x) { return x == top ? 0.0f : __fmul_rn(__fsub_rn(top, x), scale); };
+  // z, 41 where it is more
+  auto z_of = [&](float x) {
+    return x == top ? 0.0f : fminf(__fmul_rn(__fsub_rn(top, x), scale), 41.0f);
+  };
+  const bool infinite = top == INFINITY;  // the only largest logit whose difference to itself is not 0
+  const uint64_t top2 = pack2(top, top), scale2 = pack2(scale, scale);
+  auto z2_of = [&](float a, float b, float& z0, float& z1) {
+    const float2 z = unpack2(mul2(add2(top2, pack2(-a, -b)), scale2));
+    z0 = infinite && a == top ? 0.0f : fminf(z.x, 41.0f);
+    z1 = infinite && b == top ? 0.0f : fminf(z.y, 41.0f);
+  };
 
   // ---- thresholds: kept are the tokens above `cut` and the first `ties` of those that have it
   uint32_t cut = 0;
   uint64_t ties = 0;
   auto logit_of = [](uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); };
-  auto each = [&](auto&& f) {
+  auto each = [&](auto&& f) {  // f(logit, z, logit, z)
     for (int s = 0; s < steps; ++s) {
       const Piece<T> x = piece(s);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) f(to_float(x.x[i]));
+      for (int i = 0; i < kN; i += 2) {
+        const float a = to_float(x.x[i]), b = to_float(x.x[i + 1]);
+        float z0, z1;
+        z2_of(a, b, z0, z1);
+        f(a, z0, b, z1);
+      }
     }
   };
   // Which bin of z, in the order of the tokens, brings the count (or weight) of the tokens up to
   // and with it to `target`, which all tokens together reach: rounds of 16 in z, most rows need
   // one. `before` becomes the count (weight) of the bins before it, `inside` its tokens.
   bool used = false;  // the bins: others may still be reading them
-  auto find_bin = [&](bool count, uint64_t target, uint64_t& before, uint64_t& inside) {
+  // While the first round passes over the tokens it sums up all weights for a target that
+  // depends on them (target(sum)).
+  auto find_bin = [&](bool count, auto&& target_of_all, uint64_t& before, uint64_t& inside,
+                      uint64_t& target) {
     before = 0;
+    uint64_t all_weights = 0, some = 0;
     for (int round = 0;; ++round) {
       if (used) cluster.sync();
       used = true;
@@ -260,23 +326,34 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       if (tid == 0) s_found[0] = ~uint64_t(0);
       __syncthreads();
       const float z0 = round * 16.0f;
-      each([&](float y) {
-        const float z = z_of(y) - z0;
-        if (!(z >= 0.0f && z < 16.0f) || z + z0 >= 41.0f) return;
-        const int b = (int)(z * (kBins / 16));
-        if (count) {
-          // a weight of 0 is no token: z may come close to 41 or pass 40 without one
-          if (z + z0 < 40.0f || weight_of(z + z0)) atomicAdd(&s_bins[3][b], 1u);
-        } else {
-          const uint64_t w = weight_of(z + z0);
-          const uint32_t w0 = (uint32_t)w & 0x1FFFu, w1 = (uint32_t)(w >> 13) & 0x1FFFu;
-          const uint32_t w2 = (uint32_t)(w >> 26);
-          if (w0) atomicAdd(&s_bins[0][b], w0);
-          if (w1) atomicAdd(&s_bins[1][b], w1);
-          if (w2) atomicAdd(&s_bins[2][b], w2);
-          if (w) atomicAdd(&s_bins[3][b], 1u);
+      auto put = [&](float z, uint64_t w) {
+        const int b = (int)((z - z0) * (kBins / 16));
+        if (!count) {
+          const uint32_t d0 = (uint32_t)w & 0x1FFFu, d1 = (uint32_t)(w >> 13) & 0x1FFFu;
+          const uint32_t d2 = (uint32_t)(w >> 26);
+          if (d0) atomicAdd(&s_bins[0][b], d0);
+          if (d1) atomicAdd(&s_bins[1][b], d1);
+          if (d2) atomicAdd(&s_bins[2][b], d2);
+        }
+        atomicAdd(&s_bins[3][b], 1u);
+      };
+      each([&](float, float za, float, float zb) {
+        const bool ina = za >= z0 && za < z0 + 16.0f, inb = zb >= z0 && zb < z0 + 16.0f;
+        if (count) {  // a weight of 0 is no token: z may pass 40 without one
+          if (ina && (za < 40.0f || weight_of(za))) put(za, 0);
+          if (inb && (zb < 40.0f || weight_of(zb))) put(zb, 0);
+        } else if (round == 0 || ina || inb) {
+          uint64_t wa, wb;
+          weights2(za, zb, wa, wb);
+          all_weights += wa + wb;
+          if (ina && wa) put(za, wa);
+          if (inb && wb) put(zb, wb);
         }
       });
+      if (round == 0) {
+        if (!count) reduce(all_weights, some);
+        target = target_of_all(all_weights);
+      }
       cluster.sync();
       // every CTA finds it for itself: thread t sums bins t * kEach ..
       constexpr int kEach = kBins / THREADS;
@@ -319,18 +396,19 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       }
       __syncthreads();
       const uint64_t found = s_found[0];
-      if (found != ~uint64_t(0) || round == 2) {
+      if (found != ~uint64_t(0)) {
         before = s_found[1];
         inside = s_found[2];
         return (int)found;
       }
+      if (round == 2) return -1;  // a count that all tokens do not reach
       before = all;
     }
   };
-  auto bin_of = [&](float z) {  // as find_bin counts them; past the last for a token that weighs 0
-    if (!(z < 41.0f) || (z >= 40.0f && !weight_of(z))) return 3 * kBins;
-    const int round = (int)(z * (1.0f / 16.0f));
-    return round * kBins + (int)((z - round * 16.0f) * (kBins / 16));
+  // whether a token's z lies in bins [b0, b1], as find_bin counts them
+  auto low_z = [](int b) { return b * (16.0f / kBins); };
+  auto inside_of = [&](float z, float z0, float z1) {
+    return z >= z0 && z < z1 && (z < 40.0f || weight_of(z) != 0);
   };
   // The largest key among the tokens of bins [b0, b1] with F(key) >= target, F(key) the count or the
   // weight of these tokens from it on; `above` becomes F(key + 1). They are gathered by the
@@ -340,12 +418,14 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
     cluster.sync();  // all have read the bins
     uint32_t* const n = cluster.map_shared_rank(&s_n, 0);
     uint32_t* const list = cluster.map_shared_rank(s_list, 0);
-    each([&](float y) {
-      const int b = bin_of(z_of(y));
-      if (b >= b0 && b <= b1) {
-        const uint32_t at = atomicAdd(n, 1u);
-        if (at < kList) list[at] = key_of(y);
-      }
+    const float z0 = low_z(b0), z1 = low_z(b1 + 1);
+    auto put = [&](float y) {
+      const uint32_t at = atomicAdd(n, 1u);
+      if (at < kList) list[at] = key_of(y);
+    };
+    each([&](float a, float za, float b, float zb) {
+      if (inside_of(za, z0, z1)) put(a);
+      if (inside_of(zb, z0, z1)) put(b);
     });
     cluster.sync();
   };
@@ -380,6 +460,27 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       return a;
     };
   };
+  // The same search of a list of at most 256 by every warp for itself, its keys and weights in
+  // registers: no barriers.
+  uint32_t lk[8];
+  uint64_t lw[8];
+  auto take_list = [&](int n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = e * 32 + lane;
+      lk[e] = i < n ? s_list[i] : 0;
+      lw[e] = i < n ? weight_of(z_of(logit_of(lk[e]))) : 0;
+    }
+  };
+  auto in_warp = [&](bool count) {
+    return [&, count](uint32_t key) {
+      uint64_t a = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lk[e] >= key) a += count ? 1 : lw[e];
+      return count ? (uint64_t)__reduce_add_sync(0xffffffffu, (uint32_t)a) : warp_sum(a);
+    };
+  };
   auto ends = [&](int n, uint32_t& low, uint32_t& high) {  // of the list
     low = 0xFFFFFFFFu;
     high = 0;
@@ -400,12 +501,13 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
   auto everywhere = [&](bool count, int b0, int b1) {  // by all
     return [&, count, b0, b1](uint32_t key) {
       uint64_t a = 0, b = 0;
-      each([&](float y) {
-        if (key_of(y) >= key) {
-          const float z = z_of(y);
-          const int bin = bin_of(z);
-          if (bin >= b0 && bin <= b1) a += count ? 1 : weight_of(z);
-        }
+      const float z0 = low_z(b0), z1 = low_z(b1 + 1);
+      auto add = [&](float y, float z) {
+        if (key_of(y) >= key && inside_of(z, z0, z1)) a += count ? 1 : weight_of(z);
+      };
+      each([&](float x, float zx, float y, float zy) {
+        add(x, zx);
+        add(y, zy);
       });
       reduce(a, b);
       return a;
@@ -431,24 +533,13 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
   } else {
     const bool by_p = top_p < 1.0f;
     bool by_k = top_k > 0 && top_k < p.vocab;
-    uint64_t total = 0, some = 0;
-    if (by_k || by_p) {
-      // the weight of all tokens, and how many weigh something: only these can be kept
-      each([&](float y) {
-        const float z = z_of(y);
-        if (z < 41.0f) {
-          const uint64_t w = by_p || z >= 40.0f ? weight_of(z) : 1;
-          total += w;
-          some += w != 0;
-        }
-      });
-      reduce(total, some);
-      by_k = by_k && top_k < some;
-    }
+    uint64_t total = 0;
     bool done = false;
     if (by_k) {
-      uint64_t before, inside;
-      const int b = find_bin(true, top_k, before, inside);
+      uint64_t before = 0, inside = 0, k;
+      const int b = find_bin(true, [&](uint64_t) { return (uint64_t)top_k; }, before, inside, k);
+      by_k = b >= 0;
+      if (by_k) {
       const bool all = before + inside <= kList;  // all that top-k can keep fit the list
       uint64_t above = 0;
       if (inside <= kList) {
@@ -457,15 +548,22 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
           const int n = (int)(all ? before + inside : inside);
           uint32_t low, high;
           ends(n, low, high);
-          cut = search(in_list(true, n), all ? (uint64_t)top_k : top_k - before, above, low, high);
-          ties = top_k - above - (all ? 0 : before);
-          if (all && by_p) {
-            uint64_t w = weight_at(cut);
-            const uint64_t kept = in_list(false, n)(cut + 1) + ties * w;
-            const uint64_t target = target_of(kept);
-            cut = search(in_list(false, n), target, above, low, high);
-            w = weight_at(cut);
-            ties = (target - above + w - 1) / w;
+          auto solve = [&](auto&& counts, auto&& weights) {
+            cut = search(counts, all ? (uint64_t)top_k : top_k - before, above, low, high);
+            ties = top_k - above - (all ? 0 : before);
+            if (all && by_p) {
+              uint64_t w = weight_at(cut);
+              const uint64_t target = target_of(weights(cut + 1) + ties * w);
+              cut = search(weights, target, above, low, high);
+              w = weight_at(cut);
+              ties = (target - above + w - 1) / w;
+            }
+          };
+          if (n <= 256) {
+            take_list(n);
+            solve(in_warp(true), in_warp(false));
+          } else {
+            solve(in_list(true, n), in_list(false, n));
           }
         }
         share();
@@ -476,25 +574,35 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       }
       if (!done && by_p) {  // the weight of the first k
         total = 0;
-        each([&](float y) {
-          if (key_of(y) > cut) total += weight_of(z_of(y));
+        auto add = [&](float y, float z) {
+          if (key_of(y) > cut) total += weight_of(z);
+        };
+        each([&](float x, float zx, float y, float zy) {
+          add(x, zx);
+          add(y, zy);
         });
         uint64_t ignored = 0;
         reduce(total, ignored);
         total += ties * weight_at(cut);
       }
+      }
     }
     if (by_p && !done) {
-      const uint64_t target = target_of(total);
-      uint64_t before, inside, above = 0;
-      const int b = find_bin(false, target, before, inside);
+      uint64_t before = 0, inside = 0, above = 0, target;
+      const int b = find_bin(
+          false, [&](uint64_t all) { return target_of(by_k ? total : all); }, before, inside, target);
       if (inside <= kList) {
         if (tid == 0) s_n = 0;  // before all meet in the gathering
         gather(b, b);
         if (rank == 0) {
           uint32_t low, high;
           ends((int)inside, low, high);
-          cut = search(in_list(false, (int)inside), target - before, above, low, high);
+          if (inside <= 256) {
+            take_list((int)inside);
+            cut = search(in_warp(false), target - before, above, low, high);
+          } else {
+            cut = search(in_list(false, (int)inside), target - before, above, low, high);
+          }
           const uint64_t w = weight_at(cut);
           ties = (target - before - above + w - 1) / w;
         }
@@ -510,22 +618,55 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       greedy || none ? uint64_t(1) << 40
                      : weight_at(cut);
   if (tie_weight < least && !greedy) ties = 0;
-  // the weight of a token above the cut
-  auto strict = [&](float y) {
-    const uint64_t w = key_of(y) > cut ? weight_of(z_of(y)) : 0;
-    return w >= least ? w : 0;
+  const float border = cut ? logit_of(cut) : -INFINITY;
+  // the weights of the tokens of a piece that are above the cut; 0 of others
+  auto strict = [&](const Piece<T>& x, uint64_t (&w)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+      const float a = to_float(x.x[i]), b = to_float(x.x[i + 1]);
+      w[i] = w[i + 1] = 0;
+      if (a > border || b > border) {
+        float z0, z1;
+        z2_of(a, b, z0, z1);
+        weights2(z0, z1, w[i], w[i + 1]);
+        if (!(a > border) || w[i] < least) w[i] = 0;
+        if (!(b > border) || w[i + 1] < least) w[i + 1] = 0;
+      }
+    }
+  };
+  auto ties_of = [&](const Piece<T>& x) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) n += to_float(x.x[i]) == border;
+    return border > -INFINITY ? n : 0;
+  };
+  // the weights of a piece that are kept, the ties in the order of the tokens behind `seen` of them
+  auto kept = [&](const Piece<T>& x, uint64_t& seen, uint64_t (&w)[kN]) {
+    strict(x, w);
+    const int mine = ties_of(x);
+    if (!__any_sync(0xffffffffu, mine)) return;
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    uint64_t rank_of = seen + scan - mine;
+    seen += __shfl_sync(0xffffffffu, scan, 31);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (to_float(x.x[i]) == border) w[i] = rank_of++ < ties ? tie_weight : 0;
   };
 
   // ---- kept weights of this warp's range: those above the cut, and how many have it
   uint64_t sum = 0, tied = 0;
   for (int s = 0; s < steps; ++s) {
     const Piece<T> x = piece(s);
+    uint64_t w[kN];
+    strict(x, w);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float y = to_float(x.x[i]);
-      sum += strict(y);
-      tied += key_of(y) == cut && y > -INFINITY;
-    }
+    for (int i = 0; i < kN; ++i) sum += w[i];
+    tied += ties_of(x);
   }
   sum = warp_sum(sum);
   tied = warp_sum(tied);
@@ -575,24 +716,9 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
       for (int s = 0; s < steps; ++s) {
         const Piece<T> x = piece(s);
         uint64_t w[kN], lane_sum = 0;
-        int lane_ties = 0;
+        kept(x, seen, w);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) lane_ties += key_of(to_float(x.x[i])) == cut;
-        int scan = lane_ties;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, scan, o);
-          if (lane >= o) scan += y;
-        }
-        uint64_t rank_of = seen + scan - lane_ties;
-        seen += __shfl_sync(0xffffffffu, scan, 31);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float y = to_float(x.x[i]);
-          if (key_of(y) == cut) w[i] = rank_of++ < ties ? tie_weight : 0;
-          else w[i] = strict(y);
-          lane_sum += w[i];
-        }
+        for (int i = 0; i < kN; ++i) lane_sum += w[i];
         uint64_t incl = lane_sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -624,26 +750,11 @@ __global__ void __launch_bounds__(THREADS, 3) token_sample_kernel(const __grid_c
     for (int s = 0; s < steps; ++s) {
       const Piece<T> x = piece(s);
       const int64_t v = first + (int64_t)s * (32 * kN);
-      int lane_ties = 0;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) lane_ties += key_of(to_float(x.x[i])) == cut;
-      int scan = lane_ties;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += y;
-      }
-      uint64_t rank_of = seen + scan - lane_ties;
-      seen += __shfl_sync(0xffffffffu, scan, 31);
+      uint64_t w[kN];
+      kept(x, seen, w);
       float prob[kN];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const float y = to_float(x.x[i]);
-        uint64_t w;
-        if (key_of(y) == cut) w = rank_of++ < ties ? tie_weight : 0;
-        else w = strict(y);
-        prob[i] = (float)w * 0x1p-40f * f;
-      }
+      for (int i = 0; i < kN; ++i) prob[i] = (float)w[i] * 0x1p-40f * f;
       if (v >= 0 && v + kN <= p.vocab && (reinterpret_cast<uintptr_t>(out + v) & 15) == 0) {
 #pragma unroll
         for (int i = 0; i < kN; i += 4)
@@ -710,9 +821,8 @@ int launch(const Params& p, int rows, int ranks, int stage, int dev, cudaStream_
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SAMPLE_OK : SAMPLE_ERR_CUDA;
 }
 
-template <typename T>
-int run(Params& p, int rows, int dev, int sms, cudaStream_t s) {
-  constexpr int kThreads = 256;
+template <typename T, int kThreads>
+int run(Params& p, int rows, int dev, cudaStream_t s) {
   constexpr int kPass = kThreads * Piece<T>::kN;  // logits of a step of a CTA
   int ranks = kMaxCluster;
   while (ranks > 1 && p.vocab <= ranks / 2 * kPass) ranks >>= 1;
@@ -746,7 +856,12 @@ extern "C" int token_sample(const void* logits, int64_t ld, int dtype, int rows,
   if (sms < 0) return SAMPLE_ERR_CUDA;
   Params p{logits,   ld,     vocab, temperature, top_k,  top_p, min_p, param_rows,
            uniforms, tokens, probs, probs_ld,    status, 0};
-  if (dtype == SAMPLE_FP32) return run<float>(p, rows, dev, sms, (cudaStream_t)stream);
-  if (dtype == SAMPLE_FP16) return run<__half>(p, rows, dev, sms, (cudaStream_t)stream);
-  return run<__nv_bfloat16>(p, rows, dev, sms, (cudaStream_t)stream);
+  // CTAs of 512 threads while each has an SM, so that few rows take less time each
+  const bool few = (int64_t)rows * kMaxCluster <= sms;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == SAMPLE_FP32)
+    return few ? run<float, 512>(p, rows, dev, s) : run<float, 256>(p, rows, dev, s);
+  if (dtype == SAMPLE_FP16)
+    return few ? run<__half, 512>(p, rows, dev, s) : run<__half, 256>(p, rows, dev, s);
+  return few ? run<__nv_bfloat16, 512>(p, rows, dev, s) : run<__nv_bfloat16, 256>(p, rows, dev, s);
 }
