@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;   // of 16 in z: 1 / 32 of a power of two
+constexpr int kAtOnce = 4;   // pieces
 constexpr int kList = 4 * kBins;  // tokens that one CTA searches, in the place of the bins
 
 struct Params {
@@ -206,21 +207,27 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
   Piece<T>* const stage = reinterpret_cast<Piece<T>*>(s_stage) + (int64_t)warp * p.steps * 32 + lane;
   auto read = [&](int s) {
     const int64_t v = first + (int64_t)s * (32 * kN);
+    const int64_t v0 = v - lane * kN;  // of the warp
     Piece<T> x;
-    if (v >= 0 && v + kN <= p.vocab) {
+    if (v0 >= 0 && v0 + 32 * kN <= p.vocab) {
       *reinterpret_cast<uint4*>(&x) = __ldg(reinterpret_cast<const uint4*>(logits + v));
     } else {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         x.x[i] = v + i >= 0 && v + i < p.vocab ? logits[v + i] : lowest<T>();
     }
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (to_float(x.x[i]) != to_float(x.x[i])) {
-        x.x[i] = lowest<T>();
-        err |= SAMPLE_STATUS_NAN;
-      }
     return x;
+  };
+  auto clean = [&](Piece<T>& x) {  // a NaN is -infinity
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) bad |= to_float(x.x[i]) != to_float(x.x[i]);
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (to_float(x.x[i]) != to_float(x.x[i])) x.x[i] = lowest<T>();
+      err |= SAMPLE_STATUS_NAN;
+    }
   };
   const int steps = (int)min((int64_t)p.steps,
                              max((int64_t)0, ((int64_t)p.vocab - first + lane * kN + 32 * kN - 1) / (32 * kN)));
@@ -257,13 +264,24 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
   if (tid == 0) s_n = 0;
   // ---- the maximum
   float top = -INFINITY;
-  for (int s = 0; s < steps; ++s) {
-    const Piece<T> x = read(s);
-    if (STAGED) stage[s * 32] = x;
+  for (int s = 0; s < steps; s += kAtOnce) {  // their loads on their way together
+    Piece<T> x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) top = fmaxf(top, to_float(x.x[i]));
+    for (int u = 0; u < kAtOnce; ++u) x[u] = read(s + u);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      clean(x[u]);
+      if (STAGED && s + u < steps) stage[(s + u) * 32] = x[u];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) top = fmaxf(top, to_float(x[u].x[i]));
+    }
   }
-  auto piece = [&](int s) { return STAGED ? stage[s * 32] : read(s); };
+  auto piece = [&](int s) {
+    if (STAGED) return stage[s * 32];
+    Piece<T> x = read(s);
+    clean(x);
+    return x;
+  };
   {
     const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(top));
     if (lane == 0) s_a[warp] = k;
@@ -298,6 +316,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
   uint64_t ties = 0;
   auto logit_of = [](uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); };
   auto each = [&](auto&& f) {  // f(logit, z, logit, z)
+#pragma unroll 2
     for (int s = 0; s < steps; ++s) {
       const Piece<T> x = piece(s);
 #pragma unroll
@@ -443,13 +462,24 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
     }
     return key;
   };
-  auto in_list = [&](bool count, int n) {  // by the first CTA alone
-    return [&, count, n](uint32_t key) {
+  // Lists are searched from registers, eight tokens and their weights to a thread (`at`: the
+  // thread's place, `stride`: the threads).
+  uint32_t lk[kList / THREADS];
+  uint64_t lw[kList / THREADS];
+  auto take_list = [&](int n, int at, int stride) {
+#pragma unroll
+    for (int e = 0; e < kList / THREADS; ++e) {
+      const int i = e * stride + at;
+      lk[e] = i < n ? s_list[i] : 0;
+      lw[e] = i < n ? weight_of(z_of(logit_of(lk[e]))) : 0;
+    }
+  };
+  auto in_list = [&](bool count) {  // by the first CTA alone
+    return [&, count](uint32_t key) {
       uint64_t a = 0;
-      for (int i = tid; i < n; i += THREADS) {
-        const uint32_t k = s_list[i];
-        if (k >= key) a += count ? 1 : weight_of(z_of(logit_of(k)));
-      }
+#pragma unroll
+      for (int e = 0; e < kList / THREADS; ++e)
+        if (lk[e] >= key) a += count ? 1 : lw[e];
       a = warp_sum(a);
       __syncthreads();
       if (lane == 0) s_a[warp] = a;
@@ -460,23 +490,13 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
       return a;
     };
   };
-  // The same search of a list of at most 256 by every warp for itself, its keys and weights in
-  // registers: no barriers.
-  uint32_t lk[8];
-  uint64_t lw[8];
-  auto take_list = [&](int n) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = e * 32 + lane;
-      lk[e] = i < n ? s_list[i] : 0;
-      lw[e] = i < n ? weight_of(z_of(logit_of(lk[e]))) : 0;
-    }
-  };
+  // Short ones by every warp for itself: no barriers.
+  constexpr int kShort = 32 * (kList / THREADS);
   auto in_warp = [&](bool count) {
     return [&, count](uint32_t key) {
       uint64_t a = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < kList / THREADS; ++e)
         if (lk[e] >= key) a += count ? 1 : lw[e];
       return count ? (uint64_t)__reduce_add_sync(0xffffffffu, (uint32_t)a) : warp_sum(a);
     };
@@ -559,11 +579,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
               ties = (target - above + w - 1) / w;
             }
           };
-          if (n <= 256) {
-            take_list(n);
+          if (n <= kShort) {
+            take_list(n, lane, 32);
             solve(in_warp(true), in_warp(false));
           } else {
-            solve(in_list(true, n), in_list(false, n));
+            take_list(n, tid, THREADS);
+            solve(in_list(true), in_list(false));
           }
         }
         share();
@@ -597,11 +618,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
         if (rank == 0) {
           uint32_t low, high;
           ends((int)inside, low, high);
-          if (inside <= 256) {
-            take_list((int)inside);
+          if (inside <= kShort) {
+            take_list((int)inside, lane, 32);
             cut = search(in_warp(false), target - before, above, low, high);
           } else {
-            cut = search(in_list(false, (int)inside), target - before, above, low, high);
+            take_list((int)inside, tid, THREADS);
+            cut = search(in_list(false), target - before, above, low, high);
           }
           const uint64_t w = weight_at(cut);
           ties = (target - before - above + w - 1) / w;
