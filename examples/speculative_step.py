@@ -2,10 +2,13 @@
 package in its place:
 
     KvPages.reserve / fork / free / compact   whose pages, copy on write, roll back
+    KvPages.step                              the places of a step's tokens
     Kv8Cache.store                            the drafts' K/V into the 8-bit cache
     indexer_k_prologue, indexer_mqa_logits    the indexer's keys and scores
     PagedTopK                                 the positions each query row attends to
     Kv8Cache.attention_selected               attention over their slots
+    KvPages.shared, Kv8Cache.attention_shared the same over all positions, shared prompts read once
+    sample_tokens, token_probs                drafts, and the probabilities that top-p leaves
     verify_drafts                             which drafts stand, and one token more
 
 The "model" is one attention layer with random weights and a random output matrix: what
@@ -25,7 +28,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from sparse_attention_indexer_gb300 import (Kv8Cache, KvPages, PagedTopK, binding as B,  # noqa: E402
-                                            verify_drafts)
+                                            sample_tokens, token_probs, verify_drafts)
 
 PAGE, KV_HEADS, Q_HEADS, DIM, INDEX_HEADS, VOCAB = 64, 2, 16, 128, 64, 1000
 
@@ -89,7 +92,16 @@ class Layer:
             dense, _ = self.cache.attention(q, lens, max_len, self.table, 1 / math.sqrt(DIM), group,
                                             rows)
             assert torch.allclose(o.float(), dense.float(), rtol=2e-2, atol=2e-3)
-        return torch.softmax(o.view(n, -1).float() @ self.out, -1)
+            # the samples of a prompt read its pages once for all
+            last = lens.view(-1, group)[:, -1].contiguous()
+            sets = i32(range(0, rows.shape[0] + 1, 2))
+            prefix = self.pool.shared(rows, last, sets)
+            both, _ = self.cache.attention_shared(q, lens, max_len, self.table, 1 / math.sqrt(DIM), sets,
+                                                  prefix, max_len, group, rows)
+            assert torch.allclose(both.float(), dense.float(), rtol=2e-2, atol=2e-3)
+        logits = o.view(n, -1).float() @ self.out
+        full = lambda x: torch.full((n,), x, device="cuda")  # noqa: E731
+        return token_probs(logits, temperature=full(1.5), top_p=full(0.98))
 
 
 def main(steps: int = 4, prompt: int = 300, drafts: int = 3, k: int = 2048, seed: int = 0) -> dict:
@@ -116,15 +128,17 @@ def main(steps: int = 4, prompt: int = 300, drafts: int = 3, k: int = 2048, seed
     texts = [last]
     group = drafts + 1
     for _ in range(steps):
-        drafted = rand_tokens(samples, drafts)
+        # a draft from nowhere: nearly uniform probabilities
+        guess = torch.randn((samples * drafts, VOCAB), generator=gen, device="cuda") / 8
+        drafted, q = sample_tokens(guess, torch.rand(samples * drafts, generator=gen, device="cuda"), with_probs=True)
+        drafted = drafted.view(samples, drafts)
         fed = torch.cat([last[:, None], drafted], 1)                 # [samples, drafts + 1]
         layer.pool.reserve(rows, lens, lens + group)                 # the shared tail is copied
-        at = (lens[:, None] + torch.arange(group, device="cuda", dtype=torch.int32)).contiguous()
-        layer.write(fed.view(-1), rows.repeat_interleave(group).contiguous(), at.view(-1))
-        p = layer.probabilities(fed.view(-1), rows, (at + 1).view(-1), group, max_len, k)
+        at = layer.pool.step(rows, lens, lens + group, samples * group)
+        layer.write(fed.view(-1), at.token_table, at.positions)
+        p = layer.probabilities(fed.view(-1), rows, at.lens, group, max_len, k)
         u = torch.rand((samples, group), generator=gen, device="cuda")
-        # a draft from nowhere: uniform probabilities
-        q = torch.full((samples, drafts, VOCAB), 1 / VOCAB, device="cuda")
+        q = q.view(samples, drafts, VOCAB)
         tokens, kept = verify_drafts(p.view(samples, group, VOCAB), q, drafted, u)
         lens = lens + kept + 1
         layer.pool.free(rows, lens)                                  # the refused drafts' pages
