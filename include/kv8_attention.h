@@ -156,7 +156,9 @@ int64_t kv8_attention_shared_workspace_bytes(int rows, int q_heads, int kv_heads
  *                them). They are read through the row of the set's first group that has keys, as
  *                far as they lie below the least length > 0 of the set's rows. A set of one
  *                such group, or less than 128 positions, is left to the rows' own pass
- *   max_prefix   bound on every prefix length
+ *   max_prefix   bound on every prefix length. Where (groups - 1) * max_prefix positions are less
+ *                than 256 MB of keys and values, sharing saves no time: the call is
+ *                kv8_attention's (two launches), and sets and prefixes are not looked at
  *   workspace    of kv8_attention_shared_workspace_bytes; the four launches belong together
  * Numbers are held as in kv8_attention; where value scales of a prefix lie within 2^8 of its
  * first one, weights keep 2^-31 of the row's largest weight * value scale, else each row's

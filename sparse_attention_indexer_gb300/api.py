@@ -452,16 +452,15 @@ class KvPages(_Handle):
         if tokens < 0:
             raise ValueError("tokens < 0")
         handle = self._stream(stream)
-        with _on(stream):  # one allocation: 16 bytes from output to output, as a warp writes them
-            each = -(-tokens // 4) * 4
-            made = torch.empty(4 * each + n + 1, dtype=torch.int32, device=self.refs.device)
+        with _on(stream):  # one allocation and one call for its parts
+            made = torch.empty(4 * tokens + n + 1, dtype=torch.int32, device=self.refs.device)
         at = made.data_ptr()
         code = self._lib.kvpages_step(
             rows.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), n, *self._table_args,
-            self.page_size, self.num_pages, tokens, at, at + 4 * each, at + 8 * each,
-            at + 12 * each, at + 16 * each, self._status, handle)
+            self.page_size, self.num_pages, tokens, at, at + 4 * tokens, at + 8 * tokens,
+            at + 12 * tokens, at + 16 * tokens, self._status, handle)
         B._kvp(code, "kvpages_step")
-        return Step(*(made[i * each:i * each + tokens] for i in range(4)), made[4 * each:])
+        return Step._make(made.split_with_sizes((tokens, tokens, tokens, tokens, n + 1)))
 
     def shared(self, rows: torch.Tensor, lens: torch.Tensor, set_starts: torch.Tensor,
                stream=None) -> torch.Tensor:

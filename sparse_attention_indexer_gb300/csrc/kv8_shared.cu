@@ -43,6 +43,12 @@ constexpr int kWidenWarps = 8;  // behind the eight of the streams
 constexpr int kPThreads = 256 + 32 * kWidenWarps;
 constexpr int kPRows = 2 * kTile;
 constexpr int kLeast = 128;     // positions of the least prefix that is read for all
+// Bytes of keys and values that sharing has to save by the caller's bounds, (groups - 1) *
+// max_prefix positions: below, the rows' own pass reads the prefixes again, mostly from L2, and is
+// done before two launches more would be (one set on 8 key heads of 128, rows' own pass against
+// this: 8 requests of 8192 positions 32 / 39 us, 117 MB; 4 of 32768 49 / 58, 201 MB; 8 of 32768
+// 81 / 58, 470 MB; 32 of 8192 84 / 55, 520 MB; on 2 key heads 32 of 32768 81 / 60, 520 MB).
+constexpr double kWorth = 256e6;
 constexpr float kRaise = 11.0f, kBelow = 7.0f;  // log2: a reference is raised from here, to there
 constexpr float kMost = 32768.0f;  // of 16 weights together: 2^15, which is 2^kRaise for the largest
 constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
@@ -1116,7 +1122,7 @@ int launch_prefix(const Prefix& P, int dev, cudaStream_t s) {
   kernel<<<(unsigned)grid, kPThreads, kBytes, s>>>(P);
   if (cudaGetLastError() != cudaSuccess) return KV8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 8);
+  cfg.gridDim = dim3((unsigned)grid, kPRows / kJoinWarps);  // a row to a warp
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -1179,7 +1185,10 @@ extern "C" int kv8_attention_shared(
   p.page_size = page_size;
   p.page_shift = shift_of(page_size);
   cudaStream_t s = (cudaStream_t)stream;
-  if (n_sets == 0 || max_prefix < kLeast) return run<false>(p, dim, dtype, workspace, own, s);
+  const int groups = (int)(((int64_t)rows + group_rows - 1) / group_rows);
+  if (n_sets == 0 || max_prefix < kLeast ||
+      (double)(groups - 1) * max_prefix * kv_heads * 2.0 * dim < kWorth)
+    return run<false>(p, dim, dtype, workspace, own, s);
   char* const ws = reinterpret_cast<char*>(workspace);
   Prefix P = {};
   P.p = p;
@@ -1187,7 +1196,7 @@ extern "C" int kv8_attention_shared(
   P.n_sets = n_sets;
   P.prefix_lens = prefix_lens;
   P.max_prefix = max_prefix;
-  P.groups = (rows + group_rows - 1) / group_rows;
+  P.groups = groups;
   P.start = reinterpret_cast<int32_t*>(ws + at.start);
   P.splits = reinterpret_cast<Split*>(ws + at.splits);
   P.parts = reinterpret_cast<float*>(ws + at.parts);

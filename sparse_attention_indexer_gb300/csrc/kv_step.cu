@@ -10,7 +10,7 @@
 // thousand single tokens.
 //
 // shared: a cluster of 8 CTAs takes a set. An item is 512 columns of one member's row, compared
-// with the same columns of the set's first live row; 64 warps take the items in turn and the
+// with the same columns of the set's first live row; 256 warps take the items in turn and the
 // least column that differs is joined through distributed shared memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -28,7 +28,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kEach = 16;                   // requests of a thread in a round
 constexpr int kRound = kThreads * kEach;    // requests of a round
 constexpr int kSpan = 1024;                 // tokens that a CTA's range is a multiple of
+constexpr int kAtOnce = 4;                  // tokens of a thread whose loads are on their way together
 constexpr int kCluster = 8;
+constexpr int kSetThreads = 1024;
 constexpr int kColumns = 512;               // table columns of an item
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
@@ -47,6 +49,7 @@ struct Step {
   int32_t *positions, *token_table, *slots, *lens, *starts;
   int32_t* status;
   int span;  // tokens of a CTA
+  int page_shift;  // log2 of a page that is a power of two, else -1
 };
 
 // Tokens of request i; 0 where it fails a check.
@@ -112,25 +115,44 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     __syncthreads();
     // tokens of this round inside the CTA's range
     const int64_t t1 = min(last, (int64_t)s_start[here]);
-    for (int64_t t = max(first, min(sum, (int64_t)p.tokens)) + tid; t < t1; t += kThreads) {
-      int lo = 0, hi = here;  // s_start[lo] <= t < s_start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= t) lo = mid;
-        else hi = mid;
+    for (int64_t t0 = max(first, min(sum, (int64_t)p.tokens)) + tid; t0 < t1;
+         t0 += kThreads * kAtOnce) {
+      int of[kAtOnce], row[kAtOnce], pos[kAtOnce], col[kAtOnce], page[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t t = min(t0 + u * kThreads, t1 - 1);  // places past the end repeat the last
+        int lo = 0, hi = here;  // s_start[lo] <= t < s_start[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_start[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+        of[u] = lo;
       }
-      const int row = __ldg(p.rows + i0 + lo);
-      const int pos = __ldg(p.old_lens + i0 + lo) + (int)(t - s_start[lo]);
-      const int col = pos / p.page;
-      const int32_t page = __ldg(p.table + row * p.ld + col);
-      int slot = -1;
-      if (page < 0) err |= KVPAGES_STATUS_NO_PAGE;
-      else if (page >= p.num_pages) err |= KVPAGES_STATUS_PAGE;
-      else slot = page * p.page + (pos - col * p.page);
-      p.positions[t] = pos;
-      p.token_table[t] = row;
-      p.slots[t] = slot;
-      p.lens[t] = pos + 1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        row[u] = __ldg(p.rows + i0 + of[u]);
+        pos[u] = __ldg(p.old_lens + i0 + of[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        pos[u] += (int)(min(t0 + u * kThreads, t1 - 1) - s_start[of[u]]);
+        col[u] = p.page_shift >= 0 ? pos[u] >> p.page_shift : pos[u] / p.page;
+        page[u] = __ldg(p.table + row[u] * p.ld + col[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t t = t0 + u * kThreads;
+        if (t >= t1) break;
+        int slot = -1;
+        if (page[u] < 0) err |= KVPAGES_STATUS_NO_PAGE;
+        else if (page[u] >= p.num_pages) err |= KVPAGES_STATUS_PAGE;
+        else slot = page[u] * p.page + (pos[u] - col[u] * p.page);
+        p.positions[t] = pos[u];
+        p.token_table[t] = row[u];
+        p.slots[t] = slot;
+        p.lens[t] = pos[u] + 1;
+      }
     }
     sum = end;
   }
@@ -158,7 +180,7 @@ struct Sets {
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant__ Sets p) {
+__global__ void __launch_bounds__(kSetThreads) shared_kernel(const __grid_constant__ Sets p) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int s_lead, s_least, s_live, s_bad, s_col;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -176,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
     a = b = 0;
   }
   // ---- the set's live rows
-  for (int i = a + tid; i < b; i += kThreads) {
+  for (int i = a + tid; i < b; i += kSetThreads) {
     const int row = __ldg(p.rows + i), len = __ldg(p.lens + i);
     if (len == 0) continue;
     int bad = 0;
@@ -201,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
     const int32_t* lead = p.table + __ldg(p.rows + s_lead) * p.ld;
     const int per = (cols + kColumns - 1) / kColumns;
     const int64_t items = (int64_t)(b - a) * per;
-    for (int64_t item = (int64_t)warp * kCluster + rank; item < items; item += kWarps * kCluster) {
+    for (int64_t item = (int64_t)warp * kCluster + rank; item < items; item += kSetThreads / 32 * kCluster) {
       const int i = a + (int)(item / per);
       const int c0 = (int)(item % per) * kColumns + lane;
       if (__ldg(p.lens + i) == 0) continue;
@@ -262,11 +284,14 @@ extern "C" int kvpages_step(const int32_t* rows, const int32_t* old_lens, const 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return KVPAGES_ERR_CUDA;
   const int64_t spans = ((int64_t)tokens + kSpan - 1) / kSpan;
-  const int64_t most = (int64_t)sms * 4;
+  const int64_t most = (int64_t)sms * 8;
   const int64_t each = spans <= most ? 1 : (spans + most - 1) / most;
   const int grid = spans ? (int)((spans + each - 1) / each) : 1;
+  int shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) shift = i;
   const Step p{rows,   old_lens,  new_lens,    n,     block_table, n_tables, table_ld, page_size, num_pages,
-               tokens, positions, token_table, slots, lens,        starts,   status,   (int)(each * kSpan)};
+               tokens, positions, token_table, slots, lens,        starts,   status,   (int)(each * kSpan), shift};
   step_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KVPAGES_OK : KVPAGES_ERR_CUDA;
 }
@@ -287,7 +312,7 @@ extern "C" int kvpages_shared(const int32_t* rows, const int32_t* lens, int n,
                prefix_lens, status};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_sets * kCluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kSetThreads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

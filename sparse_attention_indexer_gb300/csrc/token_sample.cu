@@ -656,15 +656,30 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
       }
     }
   };
+  // fp32 logits that are kept in shared memory give way to their weights (an fp32 number holds one
+  // exactly; kTie stands for a tie) in the pass that needs them first
+  constexpr bool kInPlace = STAGED && sizeof(T) == 4;
+  constexpr float kTie = -1.0f;
+  bool replaced = false;
   auto ties_of = [&](const Piece<T>& x) {
     int n = 0;
+    if (kInPlace && replaced) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) n += to_float(x.x[i]) == kTie;
+      return n;
+    }
 #pragma unroll
     for (int i = 0; i < kN; ++i) n += to_float(x.x[i]) == border;
     return border > -INFINITY ? n : 0;
   };
   // the weights of a piece that are kept, the ties in the order of the tokens behind `seen` of them
   auto kept = [&](const Piece<T>& x, uint64_t& seen, uint64_t (&w)[kN]) {
-    strict(x, w);
+    if (kInPlace) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] = to_float(x.x[i]) > 0.0f ? (uint64_t)to_float(x.x[i]) : 0;
+    } else {
+      strict(x, w);
+    }
     const int mine = ties_of(x);
     if (!__any_sync(0xffffffffu, mine)) return;
     int scan = mine;
@@ -677,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
     seen += __shfl_sync(0xffffffffu, scan, 31);
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (to_float(x.x[i]) == border) w[i] = rank_of++ < ties ? tie_weight : 0;
+      if (to_float(x.x[i]) == (kInPlace ? kTie : border)) w[i] = rank_of++ < ties ? tie_weight : 0;
   };
 
   // ---- kept weights of this warp's range: those above the cut, and how many have it
@@ -689,7 +704,15 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
 #pragma unroll
     for (int i = 0; i < kN; ++i) sum += w[i];
     tied += ties_of(x);
+    if constexpr (kInPlace) {
+      Piece<T> y;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        y.x[i] = border > -INFINITY && x.x[i] == border ? kTie : (float)w[i];
+      stage[s * 32] = y;
+    }
   }
+  replaced = kInPlace;
   sum = warp_sum(sum);
   tied = warp_sum(tied);
   __syncthreads();
@@ -772,11 +795,21 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
     for (int s = 0; s < steps; ++s) {
       const Piece<T> x = piece(s);
       const int64_t v = first + (int64_t)s * (32 * kN);
-      uint64_t w[kN];
-      kept(x, seen, w);
       float prob[kN];
+      bool tie = !kInPlace;
+      if constexpr (kInPlace) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) prob[i] = (float)w[i] * 0x1p-40f * f;
+        for (int i = 0; i < kN; ++i) {
+          prob[i] = x.x[i] * 0x1p-40f * f;
+          tie |= x.x[i] == kTie;
+        }
+      }
+      if (__any_sync(0xffffffffu, tie)) {
+        uint64_t w[kN];
+        kept(x, seen, w);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) prob[i] = (float)w[i] * 0x1p-40f * f;
+      }
       if (v >= 0 && v + kN <= p.vocab && (reinterpret_cast<uintptr_t>(out + v) & 15) == 0) {
 #pragma unroll
         for (int i = 0; i < kN; i += 4)

@@ -4,6 +4,7 @@ The oracle knows nothing of prefixes: each row attends to the slots of its own t
 tolerances are those of the attention tests (tests/test_kv8_gpu.py); the pass over a prefix holds
 more of each weight (a reference 2^7 below the row's largest) and joins one part more, which the
 2^-18 * a of that bound counts as it counts the others. Everything that no row attends to is NaN.
+The bound on the prefixes is given as LARGE, so that short ones too are read once for all.
 """
 import numpy as np
 import pytest
@@ -19,6 +20,7 @@ if not torch.cuda.is_available():
 from sparse_attention_indexer_gb300 import KvPages, binding as B  # noqa: E402
 from tests.test_kv8_gpu import DEV, TYPES, Dense, attention_cache, close  # noqa: E402
 
+LARGE = 1 << 30
 I32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)  # noqa: E731
 
 
@@ -92,7 +94,7 @@ class Sets(Dense):
         q, lens, max_len, table, scale, group, group_table = self.args()
         a = dict(q=q, lens=lens, max_len=max_len, block_table=table, sm_scale=float(scale),
                  set_starts=I32(self.starts), prefix_lens=I32(self.prefix),
-                 max_prefix=max(self.prefix + [0]), group_rows=group, group_table=group_table)
+                 max_prefix=LARGE, group_rows=group, group_table=group_table)
         a.update(kw)
         return h.attention_shared(**a)
 
@@ -246,7 +248,8 @@ def test_refused_entries_and_sets():
         d.starts = starts
         d.check(status=B.KV8_STATUS_SETS)
     d.starts = [0, 2, 4]
-    d.check(status=B.KV8_STATUS_SETS, max_prefix=300)  # the first set's is past the bound
+    d.prefix = [LARGE, 256]  # the first set's is past the bound
+    d.check(status=B.KV8_STATUS_SETS, max_prefix=LARGE - 1)
     d.prefix = [-1, 256]
     d.check(status=B.KV8_STATUS_SETS)
     d.lens[2] = 9999
@@ -265,6 +268,15 @@ def test_no_sets_and_no_rows():
     none = I32([])
     out, lse = h.attention_shared(d.q[:0], none, 10, I32(d.table), 0.1, I32([0, 0]), I32([128]), 128)
     assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+
+
+def test_prefixes_that_are_left_to_the_rows():
+    """By the bound no time is saved: the plain attention's bits, whatever the sets say."""
+    d = Sets(25, [(300, [5, 60, 7])], 1, 8, 2, 128, 64, 64, "bf16")
+    out, lse = d.check(max_prefix=300)
+    h = d.handle()
+    ref = h.attention(*d.args())
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
 
 def test_strided_rows():
@@ -287,7 +299,7 @@ def test_runs_streams_and_graphs_agree():
     more.call(big)
     a = d.args()
     kw = dict(q=a[0], lens=a[1], max_len=a[2], block_table=a[3], sm_scale=float(a[4]), group_rows=a[5],
-              group_table=a[6], set_starts=I32(d.starts), prefix_lens=I32(d.prefix), max_prefix=3000)
+              group_table=a[6], set_starts=I32(d.starts), prefix_lens=I32(d.prefix), max_prefix=LARGE)
     graphs = []
     for _ in range(2):
         o, l = torch.zeros_like(out), torch.zeros_like(lse)
@@ -329,7 +341,7 @@ def test_with_the_pages_that_make_such_batches():
     prefix = pool.shared(rows, lens + 1, starts)
     assert prefix.tolist() == [448, 256]
     q = torch.randn((5, 16, dim), device=DEV).to(torch.bfloat16)
-    got = h.attention_shared(q, lens + 1, 501, table, 0.09, starts, prefix, 640, group_table=rows)
+    got = h.attention_shared(q, lens + 1, 501, table, 0.09, starts, prefix, LARGE, group_table=rows)
     ref = h.attention(q, lens + 1, 501, table, 0.09, group_table=rows)
     assert torch.allclose(got[1], ref[1], rtol=0, atol=1e-3)
     assert torch.allclose(got[0].float(), ref[0].float(), rtol=2 ** -6, atol=2 ** -8)

@@ -8,7 +8,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from sparse_attention_indexer_gb300 import KvPages, binding as B, sample_tokens, token_probs  # noqa: E402
-from tests.test_kv8_shared_gpu import I32, Sets  # noqa: E402
+from tests.test_kv8_shared_gpu import I32, LARGE, Sets  # noqa: E402
 
 
 def test_attention_shared():
@@ -19,11 +19,11 @@ def test_attention_shared():
     ws = torch.empty(B.kv8_attention_shared_workspace_bytes(3, 8, 2, 128, 1), dtype=torch.uint8, device="cuda")
     o, l = torch.zeros_like(out), torch.zeros_like(lse)
     status = I32([0])
-    B.kv8_attention_shared(q, float(scale), lens, max_len, group, group_table, I32(d.starts), I32(d.prefix), 300, table, 64, 64,
+    B.kv8_attention_shared(q, float(scale), lens, max_len, group, group_table, I32(d.starts), I32(d.prefix), LARGE, table, 64, 64,
                            h.k, h.v, h.k_scale, h.v_scale, o, l, ws, status)
     assert torch.equal(o, out) and torch.equal(l, lse) and int(status) == 0
     with pytest.raises(B.Kv8Error):
-        B.kv8_attention_shared(q, float(scale), lens, max_len, group, group_table, I32(d.starts), I32(d.prefix), 300, table, 64,
+        B.kv8_attention_shared(q, float(scale), lens, max_len, group, group_table, I32(d.starts), I32(d.prefix), LARGE, table, 64,
                                64, h.k, h.v, h.k_scale, h.v_scale, o, l, ws[:1024], status)
 
 
