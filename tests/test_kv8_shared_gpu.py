@@ -346,3 +346,21 @@ def test_with_the_pages_that_make_such_batches():
     assert torch.allclose(got[1], ref[1], rtol=0, atol=1e-3)
     assert torch.allclose(got[0].float(), ref[0].float(), rtol=2 ** -6, atol=2 ** -8)
     assert int(h.status.item()) == 0 and int(pool.status.item()) == 0
+
+
+def test_offsets_past_32_bits():
+    """Codes and workspace rows behind 2^32 bytes: the prefix's pages lie at the end of a large cache."""
+    from sparse_attention_indexer_gb300 import Kv8Cache
+    page, hk, dim, pages = 64, 8, 128, 70000  # 4.6e9 bytes of keys
+    d = Sets(26, [(300, [5, 60])], 1, 16, hk, dim, page, page, "bf16", poison=False)
+    small = d.handle()
+    n = d.cache[0].shape[0] // page
+    code = lambda: torch.full((pages * page, hk, dim), 0x7F, dtype=torch.uint8, device=DEV)  # noqa: E731
+    scale = lambda: torch.full((pages, hk), float("nan"), device=DEV)  # noqa: E731
+    large = Kv8Cache(code(), code(), scale(), scale(), page, page)
+    for x, y in ((large.k, small.k), (large.v, small.v), (large.k_scale, small.k_scale), (large.v_scale, small.v_scale)):
+        x[-y.shape[0]:] = y
+    ref = d.call(small)
+    got = d.call(large, block_table=I32(np.where(d.table >= 0, d.table + pages - n, -1)))
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    assert int(large.status.item()) == 0
