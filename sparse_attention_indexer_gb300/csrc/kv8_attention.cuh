@@ -255,11 +255,9 @@ __device__ __forceinline__ int tiles_of(int len) {
 
 // What a unit counts when the work is divided: its tiles, and behind a shared prefix, where most
 // units are short, kUnitTiles for its start and end, which take as long (queries, the first
-// loads, the join of its warps, the prefix's part).
-#ifndef KV8_UNIT_TILES
-#define KV8_UNIT_TILES 16
-#endif
-constexpr int kUnitTiles = KV8_UNIT_TILES;
+// loads, the join of its warps, the prefix's part). 64 requests of 64-4096 tokens of their own on 8
+// key heads: 70 us with tiles alone, 48 with 3 more, 37 with 8, 33 with 16.
+constexpr int kUnitTiles = 16;
 template <bool TAIL>
 __device__ __forceinline__ int span_of(int len) {
   return tiles_of(len) + (TAIL ? kUnitTiles : 0);
