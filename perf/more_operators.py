@@ -306,8 +306,8 @@ def _plain_shared(s):
         oslots = table[a:b, tail // page].clamp(min=0) * page + tail % page
         x = q[a * g:b * g].float().view(n, g, hk, ratio, dim).permute(2, 0, 1, 3, 4)  # [hk, n, g, ratio, dim]
         kp, ko = _keys(c, "k", pslots, block), _keys(c, "k", oslots, block)
-        sp = torch.matmul(x.reshape(hk, -1, dim), kp.permute(1, 2, 0)).view(hk, n, g, ratio, pre) * s["scale"]
-        so = torch.matmul(x.reshape(hk, n, g * ratio, dim), ko.permute(2, 0, 3, 1)).view(hk, n, g, ratio, len(tail)) * s["scale"]
+        sp = torch.matmul(x.reshape(hk, -1, dim), kp.permute(1, 2, 0)).view(hk, n, g, ratio, -1) * s["scale"]
+        so = torch.matmul(x.reshape(hk, n, g * ratio, dim), ko.permute(2, 0, 3, 1)).view(hk, n, g, ratio, -1) * s["scale"]
         del kp, ko
         see = lens[None, :, :, None, None]
         sp = sp.masked_fill(t[:pre] >= see, -math.inf)
@@ -317,8 +317,8 @@ def _plain_shared(s):
         sp, so = torch.exp(sp - safe), torch.exp(so - safe)
         total = sp.sum(-1) + so.sum(-1)
         vp, vo = _keys(c, "v", pslots, block), _keys(c, "v", oslots, block)
-        o = torch.matmul(sp.reshape(hk, n * g * ratio, pre), vp.permute(1, 0, 2)).view(hk, n, g, ratio, dim)
-        o = o + torch.matmul(so.reshape(hk, n, g * ratio, len(tail)), vo.permute(2, 0, 1, 3)).view(hk, n, g, ratio, dim)
+        o = torch.matmul(sp.view(hk, -1, pre), vp.permute(1, 0, 2)).view(hk, n, g, ratio, dim)
+        o = o + torch.matmul(so.view(hk, n, g * ratio, -1), vo.permute(2, 0, 1, 3)).view(hk, n, g, ratio, dim)
         o = torch.where(total[..., None] > 0, o / total[..., None], 0.0)
         out[a * g:b * g] = o.permute(1, 2, 0, 3, 4).reshape(n * g, hq, dim).to(q.dtype)
         lse[a * g:b * g] = (torch.log(total) + top[..., 0]).permute(1, 2, 0, 3).reshape(n * g, hq)
