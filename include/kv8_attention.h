@@ -78,8 +78,9 @@ enum {
   KV8_STATUS_SETS = 64,        /* kv8_attention_shared: set_starts falls or leaves [0, groups]: no
                                   prefix is read once for several rows; or a prefix length
                                   outside [0, max_prefix]: that set's is not */
-  KV8_STATUS_TIMEOUT = 128     /* kv8_attention_shared: a wait inside the kernel ran out (200 ms):
-                                  the results are not valid */
+  KV8_STATUS_TIMEOUT = 128     /* kv8_attention_shared: a wait inside the kernel ran out (200 ms of
+                                  wall time): rows and heads whose prefix it was to give are NaN
+                                  in out and lse, the others are right */
 };
 
 /* Quantises `tokens` tokens into the cache. One launch.
@@ -175,6 +176,21 @@ int kv8_attention_shared(const void* q, int64_t q_ld, int dtype, int rows, int q
                          int64_t num_slots, void* out, int64_t out_ld, float* lse,
                          void* workspace, int64_t ws_bytes, int32_t* status,
                          kv8_stream_t stream);
+
+/* Test entry: kv8_attention_shared with a CTA (skip_cta >= 0; -1 = none) of the prefixes' pass
+ * whose keys and values never come, so that its waits run out: the call ends after 200 ms with
+ * KV8_STATUS_TIMEOUT and NaN for the rows and heads of that CTA. */
+int kv8_attention_shared_test(const void* q, int64_t q_ld, int dtype, int rows, int q_heads,
+                              int kv_heads, int dim, float sm_scale, const int32_t* lens,
+                              int max_len, int group_rows, const int32_t* group_table,
+                              const int32_t* set_starts, int n_sets, const int32_t* prefix_lens,
+                              int max_prefix, const int32_t* block_table, int n_tables,
+                              int64_t table_ld, int page_size, int block_tokens,
+                              const uint8_t* k_cache, const uint8_t* v_cache,
+                              const float* k_scale, const float* v_scale, int64_t num_slots,
+                              void* out, int64_t out_ld, float* lse, void* workspace,
+                              int64_t ws_bytes, int32_t* status, kv8_stream_t stream,
+                              int skip_cta);
 
 #ifdef __cplusplus
 }

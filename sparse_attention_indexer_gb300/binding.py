@@ -39,6 +39,7 @@ EXPORTS = (
     "kvpages_workspace_bytes", "kvpages_reserve", "kvpages_fork", "kvpages_free",
     "kvpages_compact", "kvpages_copy", "draft_verify", "kvpages_step", "kvpages_shared",
     "token_sample", "kv8_attention_shared", "kv8_attention_shared_workspace_bytes",
+    "kv8_attention_shared_test",
 )
 
 
@@ -103,6 +104,12 @@ _SIGS = {
                                         _c.c_int, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64,
                                         _c.c_int, _c.c_int, _VP, _VP, _VP, _VP, _c.c_int64, _VP,
                                         _c.c_int64, _VP, _VP, _c.c_int64, _VP, _VP]),
+    "kv8_attention_shared_test": (_c.c_int, [_VP, _c.c_int64, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                                             _c.c_int, _c.c_float, _VP, _c.c_int, _c.c_int, _VP,
+                                             _VP, _c.c_int, _VP, _c.c_int, _VP, _c.c_int,
+                                             _c.c_int64, _c.c_int, _c.c_int, _VP, _VP, _VP, _VP,
+                                             _c.c_int64, _VP, _c.c_int64, _VP, _VP, _c.c_int64,
+                                             _VP, _VP, _c.c_int]),
     "kvpages_workspace_bytes": (_c.c_size_t, [_c.c_int, _c.c_int]),
     "kvpages_reserve": (_c.c_int, [_VP, _VP, _VP, _c.c_int, _VP, _c.c_int, _c.c_int64, _c.c_int,
                                    _VP, _c.c_int, _VP, _c.c_int, _VP, _c.c_size_t, _VP, _VP]),
@@ -484,18 +491,20 @@ def kv8_attention_shared_workspace_bytes(rows: int, q_heads: int, kv_heads: int,
 def kv8_attention_shared(q, sm_scale: float, lens, max_len: int, group_rows: int, group_table,
                          set_starts, prefix_lens, max_prefix: int, block_table, page_size: int,
                          block_tokens: int, k_cache, v_cache, k_scale, v_scale, out, lse,
-                         workspace, status=None, stream=None) -> int:
+                         workspace, status=None, stream=None, skip_cta: int = -1) -> int:
     """kv8_attention_shared of include/kv8_attention.h: set_starts int32 [n_sets + 1],
-    prefix_lens int32 [n_sets], the rest as in kv8_attention. Argument marshalling only."""
+    prefix_lens int32 [n_sets], the rest as in kv8_attention. Argument marshalling only.
+    skip_cta >= 0: kv8_attention_shared_test."""
     rows, heads, dim = q.shape
-    return _kv8(lib().kv8_attention_shared(
+    entry = lib().kv8_attention_shared_test if skip_cta >= 0 else lib().kv8_attention_shared
+    return _kv8(entry(
         _ptr(q), _ld(q), _KV8_TYPES[q.dtype], rows, heads, k_cache.shape[1], dim, sm_scale,
         _ptr(lens), max_len, group_rows, _ptr(group_table), _ptr(set_starts),
         set_starts.shape[0] - 1, _ptr(prefix_lens), max_prefix, _ptr(block_table),
         block_table.shape[0], block_table.shape[1], page_size, block_tokens, _ptr(k_cache),
         _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), k_cache.shape[0], _ptr(out), _ld(out),
         _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-        _stream(stream)), "kv8_attention_shared")
+        _stream(stream), *([skip_cta] if skip_cta >= 0 else [])), "kv8_attention_shared")
 
 
 # include/kv_pages.h

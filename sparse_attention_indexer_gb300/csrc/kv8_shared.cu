@@ -36,7 +36,9 @@
 // positions 77 us (2.1 TB/s), half of a stream's rows empty. Start and end take 9 us.
 //
 // Every mbarrier wait is bounded; one that runs out sets KV8_STATUS_TIMEOUT and ends the CTA's
-// work after its products in flight.
+// work after its products in flight. Instead of the sums of all its units that are not finished
+// the CTA then writes NaN, which the join and the rows' own pass carry into out and lse: what an
+// earlier call left in these places of the workspace would give numbers like any other.
 #include <cfloat>
 
 #include "kv8_attention.cuh"
@@ -77,6 +79,7 @@ struct Prefix {
   float* before;     // [rows * q_heads][dim + 4] (written)
   Split* splits;     // [CTAs] (written): the split unit that starts in each
   float* parts;      // two parts of kPRows rows for each CTA
+  int skip;          // a CTA whose keys and values never come (tests), or -1
 };
 
 // What the softmax needs to know of a tile; sixteen keys of it have one scale.
@@ -858,6 +861,25 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
   }
 }
 
+// All warps, in a CTA that gave up: NaN for the unit's sums of weights, of which every row of it
+// becomes NaN.
+template <int DIM>
+__device__ __noinline__ void void_rows(const Prefix& P, const Segment& g) {
+  const Params& p = P.p;
+  const int ratio = p.q_heads / p.kv_heads;
+  for (int r = threadIdx.x; r < (g.two ? kPRows : kTile); r += kPThreads) {
+    if (!g.has_row(p, ratio, r)) continue;
+    const int64_t row = g.row_at(p, ratio, r);
+    float* const stat = g.whole ? P.before + (row * p.q_heads + g.head_at(ratio, r)) * (DIM + 4) + DIM
+                                : g.part + Part<DIM, kPRows>::kStat + r * 4;
+    const int gr = (int)(row / p.group_rows);
+    int ignored = 0;
+    const bool on =  // as in stream_rows
+        row_len(p, (int)row, p.group_table ? __ldg(p.group_table + gr) : gr, &ignored) > 0;
+    *reinterpret_cast<float4*>(stat) = make_float4(kNone, kNone, on ? NAN : 0.0f, 0.0f);
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 template <int DIM, bool FP16>
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -997,6 +1019,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   __syncthreads();  // s_cum gives way to keys
   Split mine = {0, 0, 0, 0, 0, -1, {0, 0}};
   uint32_t tiles_done = 0, turns[2] = {0, 0}, segments = 0;
+  bool gave_up = false;
   for (int64_t w = w0; w < w1;) {
     // ---- the segment: a unit's steps [i0, i1) of `steps`
     for (int64_t of_set; (of_set = steps_of(set) * p.kv_heads) <= w - before; ++set) before += of_set;
@@ -1040,8 +1063,10 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
                 (int32_t)(((w + steps) * n - 1) / all), {0, 0}};
     }
     __syncthreads();
-    if (warp >= 8) {
-      err |= widen_tiles<DIM>(P, seg, base, meta, bars, quit);
+    if (gave_up) {
+      // no unit is begun any more
+    } else if (warp >= 8) {
+      if (me != P.skip) err |= widen_tiles<DIM>(P, seg, base, meta, bars, quit);
     } else {  // while the first codes are on their way
       load_queries<DIM, FP16>(P, seg, base, s_mul);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1055,7 +1080,11 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*quit) break;
+    gave_up = *quit;  // no thread waits before the next unit's barrier: all see the same
+    if (gave_up) {
+      void_rows<DIM>(P, seg);
+      __syncthreads();
+    }
   }
   if (tid == 0) {
     P.splits[me] = mine;
@@ -1151,14 +1180,16 @@ extern "C" int64_t kv8_attention_shared_workspace_bytes(int rows, int q_heads, i
   return shared_work(own, sms, rows, q_heads, dim, group_rows).total;
 }
 
-extern "C" int kv8_attention_shared(
+namespace {
+
+int attention_shared(
     const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads, int dim,
     float sm_scale, const int32_t* lens, int max_len, int group_rows, const int32_t* group_table,
     const int32_t* set_starts, int n_sets, const int32_t* prefix_lens, int max_prefix,
     const int32_t* block_table, int n_tables, int64_t table_ld, int page_size, int block_tokens,
     const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
     int64_t num_slots, void* out, int64_t out_ld, float* lse, void* workspace, int64_t ws_bytes,
-    int32_t* status, kv8_stream_t stream) {
+    int32_t* status, kv8_stream_t stream, int skip_cta) {
   if (max_len < 0 || n_tables < 1 || table_ld < 1 || page_size < 1 || block_tokens < 16 ||
       page_size % block_tokens || num_slots % page_size || n_sets < 0 || n_sets > KV8_MAX_SETS ||
       max_prefix < 0)
@@ -1206,6 +1237,7 @@ extern "C" int kv8_attention_shared(
   P.splits = reinterpret_cast<Split*>(ws + at.splits);
   P.parts = reinterpret_cast<float*>(ws + at.parts);
   P.before = reinterpret_cast<float*>(ws + at.before);
+  P.skip = skip_cta;
   const int code = dim == 128 ? dtype == KV8_FP16 ? launch_prefix<128, true>(P, dev, s)
                                                   : launch_prefix<128, false>(P, dev, s)
                    : dtype == KV8_FP16 ? launch_prefix<64, true>(P, dev, s)
@@ -1214,4 +1246,36 @@ extern "C" int kv8_attention_shared(
   p.start = P.start;
   p.before = P.before;
   return run<false, true>(p, dim, dtype, workspace, own, s);
+}
+
+}  // namespace
+
+extern "C" int kv8_attention_shared(
+    const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads, int dim,
+    float sm_scale, const int32_t* lens, int max_len, int group_rows, const int32_t* group_table,
+    const int32_t* set_starts, int n_sets, const int32_t* prefix_lens, int max_prefix,
+    const int32_t* block_table, int n_tables, int64_t table_ld, int page_size, int block_tokens,
+    const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    int64_t num_slots, void* out, int64_t out_ld, float* lse, void* workspace, int64_t ws_bytes,
+    int32_t* status, kv8_stream_t stream) {
+  return attention_shared(q, q_ld, dtype, rows, q_heads, kv_heads, dim, sm_scale, lens, max_len,
+                          group_rows, group_table, set_starts, n_sets, prefix_lens, max_prefix,
+                          block_table, n_tables, table_ld, page_size, block_tokens, k_cache,
+                          v_cache, k_scale, v_scale, num_slots, out, out_ld, lse, workspace,
+                          ws_bytes, status, stream, -1);
+}
+
+extern "C" int kv8_attention_shared_test(
+    const void* q, int64_t q_ld, int dtype, int rows, int q_heads, int kv_heads, int dim,
+    float sm_scale, const int32_t* lens, int max_len, int group_rows, const int32_t* group_table,
+    const int32_t* set_starts, int n_sets, const int32_t* prefix_lens, int max_prefix,
+    const int32_t* block_table, int n_tables, int64_t table_ld, int page_size, int block_tokens,
+    const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+    int64_t num_slots, void* out, int64_t out_ld, float* lse, void* workspace, int64_t ws_bytes,
+    int32_t* status, kv8_stream_t stream, int skip_cta) {
+  return attention_shared(q, q_ld, dtype, rows, q_heads, kv_heads, dim, sm_scale, lens, max_len,
+                          group_rows, group_table, set_starts, n_sets, prefix_lens, max_prefix,
+                          block_table, n_tables, table_ld, page_size, block_tokens, k_cache,
+                          v_cache, k_scale, v_scale, num_slots, out, out_ld, lse, workspace,
+                          ws_bytes, status, stream, skip_cta);
 }
