@@ -595,6 +595,7 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
   const Params& p = P.p;
   const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
   const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
+  const uint32_t summed = bars + 136;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ratio = p.q_heads / p.kv_heads;
   const Meta* const meta = reinterpret_cast<const Meta*>(smem + L::kMeta);
@@ -610,12 +611,16 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
   const float mul = s_mul[two ? b * kTile + r : r];
   // Products of this stream, issued by its first thread: the scores of its turn j, and the
   // sums of its turn j once its four warps have their weights in place. Keys and values are
-  // given back by both streams, by one of them twice where it alone had them.
+  // given back by both streams, by one of them twice where it alone had them. Scores go where the
+  // weights of the turn before lie, which its sums' product reads: products with different
+  // accumulators are not ordered, so they wait for it.
   constexpr uint32_t kIdS = idesc_f16(kTile, kTile, false), kIdO = idesc_f16(kTile, DIM, true);
   auto tile_at = [&](int j) { return tiles_done + (uint32_t)(two ? j : 2 * j + b); };
   auto issue_scores = [&](int j) {
     const uint32_t t = tile_at(j), st = t & 1;
-    if (!bar_wait(k_full + 8 * st, (t >> 1) & 1, quit)) return;
+    if (!bar_wait(k_full + 8 * st, (t >> 1) & 1, quit) ||
+        (j > 0 && !bar_wait(summed + 8 * b, (turns + j - 1) & 1, quit)))
+      return;
     tc_fence_after();
     const uint32_t q = base + (two ? b : 0) * L::kOperand, k = base + L::kK + st * L::kOperand;
 #pragma unroll
@@ -637,6 +642,7 @@ __device__ __noinline__ void stream_rows(const Prefix& P, const Segment& g, uint
     for (int i = 0; i < kTile / 16; ++i)
       mma_ts(tmem + 2 * kTile + b * DIM, tmem + b * kTile + i * 8,
              sdesc(v + i * 2048, kTile * 128), kIdO, j > 0 || i > 0);
+    tc_commit(summed + 8 * b);
     tc_commit(v_empty);
     if (!two) tc_commit(v_empty);
   };
@@ -904,9 +910,11 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
 
   const uint32_t bars = base + L::kBars;
   // keys in place [2] and their places free [2], values in place for each stream [2] and their place
-  // free, a tile's scales [4], a stream's scores [2] and weights [2], a segment's products
+  // free, a tile's scales [4], a stream's scores [2] and weights [2], a segment's products, a
+  // stream's sums [2]
   const uint32_t k_full = bars, k_empty = bars + 16, v_full = bars + 32, v_empty = bars + 48;
   const uint32_t m_full = bars + 64, s_full = bars + 96, p_ready = bars + 112, done = bars + 128;
+  const uint32_t summed = bars + 136;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ratio = p.q_heads / p.kv_heads;
@@ -919,6 +927,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
       bar_init(k_empty + 8 * i, 2);
       bar_init(s_full + 8 * i, 1);
       bar_init(p_ready + 8 * i, 4);
+      bar_init(summed + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) bar_init(m_full + 8 * i, 1);
     bar_init(v_empty, 2);
