@@ -19,7 +19,6 @@ LIB = os.path.join(PKG, "libtopk_paged.so")
 SOURCES = ["select.cu", "short.cu", "medium.cu", "rowcluster.cu", "plan.cu", "abi.cu", "noalloc.cu",
            "prologue.cu", "resolver.cu", "logits.cu", "kv8_store.cu", "kv8_attention.cu", "kv8_shared.cu",
            "kv_pages.cu", "kv_step.cu", "draft_verify.cu", "token_sample.cu"]
-HEADERS = ["common.cuh", "keys.cuh", "plan_logic.cuh", "kv8_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -50,12 +49,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     lib = LIB.replace(".so", "_trace.so") if trace else LIB
     defs = ["-DTOPK_TRACE"] if trace else []
     os.makedirs(bdir, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", h)
-                                                        for h in ("topk_paged.h", "indexer_prologue.h",
-                                                                  "indexer_logits.h",
-                                                                  "hisparse_resolver.h",
-                                                                  "kv8_attention.h",
-                                                                  "kv_pages.h", "draft_verify.h")]
+    hdrs = [os.path.join(d, h) for d, end in ((CSRC, ".cuh"), (os.path.join(ROOT, "include"), ".h"))
+            for h in sorted(os.listdir(d)) if h.endswith(end)]
     objs = []
     jobs = []
     for src in SOURCES:
