@@ -1218,6 +1218,13 @@ int attention_shared(
   if (sms < 0) return KV8_ERR_CUDA;
   const SharedWork at = shared_work(own, sms, rows, q_heads, dim, group_rows);
   if (ws_bytes < at.total) return KV8_ERR_WORKSPACE;
+  const int groups = (int)(((int64_t)rows + group_rows - 1) / group_rows);
+  if (n_sets == 0 || max_prefix < kLeast ||
+      (double)(groups - 1) * max_prefix * kv_heads * 2.0 * dim < kWorth)
+    return kv8_attention(q, q_ld, dtype, rows, q_heads, kv_heads, dim, sm_scale, lens, max_len,
+                         group_rows, group_table, block_table, n_tables, table_ld, page_size,
+                         block_tokens, k_cache, v_cache, k_scale, v_scale, num_slots, out, out_ld,
+                         lse, workspace, own, status, stream);
   Params p = common(q, q_ld, rows, q_heads, kv_heads, sm_scale, block_tokens, k_cache, v_cache,
                     k_scale, v_scale, num_slots, out, out_ld, lse, status);
   p.lens = lens;
@@ -1230,10 +1237,6 @@ int attention_shared(
   p.page_size = page_size;
   p.page_shift = shift_of(page_size);
   cudaStream_t s = (cudaStream_t)stream;
-  const int groups = (int)(((int64_t)rows + group_rows - 1) / group_rows);
-  if (n_sets == 0 || max_prefix < kLeast ||
-      (double)(groups - 1) * max_prefix * kv_heads * 2.0 * dim < kWorth)
-    return run<false>(p, dim, dtype, workspace, own, s);
   char* const ws = reinterpret_cast<char*>(workspace);
   Prefix P = {};
   P.p = p;
