@@ -988,7 +988,7 @@ kv8_prefix_kernel(const __grid_constant__ Prefix P) {
   // rows of a set on one key head; its steps on one: pairs of 128 rows take a tile to a step,
   // 128 rows left over two
   auto rows_of = [&](int s) { return (s_start[s + 1] - s_start[s]) * p.group_rows * ratio; };
-  auto tiles_in = [&](int s) { return (s_eff[s] + kTile - 1) / kTile; };
+  auto tiles_in = [&](int s) { return (int)(((uint32_t)s_eff[s] + kTile - 1) / kTile); };
   auto steps_of = [&](int s) -> int64_t {
     const int m = (rows_of(s) + kTile - 1) / kTile, t = tiles_in(s);
     return (int64_t)(m >> 1) * t + (m & 1) * ((t + 1) >> 1);
