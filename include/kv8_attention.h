@@ -57,12 +57,15 @@ enum {
                              multiple of block_tokens, num_slots < 0, >= 2^31 or not a
                              multiple of page_size (of block_tokens for the selected form),
                              n_tables < 1, table_ld < 1, a row stride below the row or not
-                             a multiple of 8, slots_ld < k, sm_scale not finite, or more
-                             than 2^33 pairs of a group and a key head */
+                             a multiple of 8, slots_ld < k, sm_scale not finite, more
+                             than 2^33 pairs of a group and a key head; of the shared form
+                             n_sets outside [0, KV8_MAX_SETS], max_prefix < 0 or
+                             (rows + group_rows) * (q_heads / kv_heads) >= 2^31 */
   KV8_ERR_ALIGN = -3,     /* q, out, k, v, caches or workspace not 16-byte aligned, or
                              another array not 4-byte aligned */
   KV8_ERR_CUDA = -4,      /* a launch or a device query failed */
-  KV8_ERR_WORKSPACE = -5  /* workspace smaller than kv8_attention_workspace_bytes */
+  KV8_ERR_WORKSPACE = -5  /* workspace smaller than kv8_attention_workspace_bytes, or for the shared
+                             form kv8_attention_shared_workspace_bytes, whatever its bounds */
 };
 
 /* Device status bits, OR-ed into *status. */
@@ -159,7 +162,8 @@ int64_t kv8_attention_shared_workspace_bytes(int rows, int q_heads, int kv_heads
  *                such group, or less than 128 positions, is left to the rows' own pass
  *   max_prefix   bound on every prefix length. Where (groups - 1) * max_prefix positions are less
  *                than 256 MB of keys and values, sharing saves no time: the call is
- *                kv8_attention's (two launches), and sets and prefixes are not looked at
+ *                kv8_attention's (two launches), and sets and prefixes are not looked at. A loose
+ *                bound, or many groups of no set, cost two launches more (about 25 us)
  *   workspace    of kv8_attention_shared_workspace_bytes; the four launches belong together
  * Numbers are held as in kv8_attention; where value scales of a prefix lie within 2^8 of its
  * first one, weights keep 2^-31 of the row's largest weight * value scale, else each row's

@@ -10,7 +10,7 @@
  *   rounded to nearest: 2^-f for f in [0, 1) within 2^-22.3 of its value
  *   (c1 .. c6 = -0x1.62e42cp-1, 0x1.ebfacp-3, -0x1.c6948ep-5, 0x1.39e3fcp-7, -0x1.4e2aeap-10,
  *   0x1.c946d2p-14: the minimax polynomial of that form, rounded to fp32).
- * So 2^40 stands for the largest token, and a token below 2^-41 of it (28 in l / T) weighs 0. The
+ * So 2^40 stands for the largest token, and a token below 2^-40 of it (27.7 in l / T) weighs 0. The
  * order of the tokens is by logit, larger first, then by index, smaller first. Kept are
  *   - of all tokens, the first k (top-k; k <= 0: all),
  *   - of these, the shortest beginning whose weights sum to at least p times the sum of them

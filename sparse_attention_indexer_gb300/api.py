@@ -238,7 +238,8 @@ class Kv8Cache(_Handle):
         """attention() for requests that share prefixes: the groups set_starts[s] ..
         set_starts[s + 1] - 1 (int32 [n_sets + 1]) hold the same keys below position
         prefix_lens[s] (int32 [n_sets], at most max_prefix; KvPages.shared finds them), which
-        are read once for all of them. Returns (out, lse)."""
+        are read once for all of them. Returns (out, lse); what a wait that ran out leaves open is
+        NaN there (KV8_STATUS_TIMEOUT in status)."""
         _rows(q, "q", self._device)
         rows, heads, dim = q.shape
         _int32(lens, (rows,), "lens", self._device)
@@ -567,7 +568,7 @@ def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None
                 out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
     """The probabilities from which sample_tokens would draw, float32 [rows, vocab]: a
-    target's as verify_drafts takes them."""
+    target's as verify_drafts takes them. out may not overlap the logits."""
     device = _sample_args(logits, (temperature, top_k, top_p, min_p), param_rows, status)
     if out is None:
         with _on(stream):

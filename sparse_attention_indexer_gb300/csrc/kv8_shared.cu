@@ -23,17 +23,18 @@
 //   - Warps 0-3 and 4-7 are the two streams, a thread to a row. The first thread of each issues
 //     its tcgen05.mma (kind::f16): S = Q K^T into tensor memory, and O += P V with the weights P
 //     read from tensor memory. All take the scores from there and put weights back over them
-//     as fp16. O stays in tensor memory; a row's reference is raised, and its O rescaled, only
-//     when sixteen of its weights together pass 2^15. It is set 2^7 below the row's largest, so
-//     that fp16 holds weights down to 2^-32 of it.
+//     as fp16; the next scores wait until O += P V has read them (1 % of the time). O stays in
+//     tensor memory; a row's reference is raised, and its O rescaled, only when sixteen of its
+//     weights together pass 2^15. It is set 2^7 below the row's largest, so that fp16 holds
+//     weights down to 2^-31 of it.
 //   - Scales belong to 16 keys at least (block_tokens): key scales multiply the scores, value
 //     scales join the exponent, relative to the first of the segment, and come out of the
 //     row's sum again. Where they lie more than 2^8 apart, sums and weights get references
 //     of their own and an exponential each.
-// Measured: 64 requests behind 32768 positions, 64 / 8 heads of 128, 103 us (67 Gflop, 650
-// TFLOP/s): a stream takes 5400 cycles for 128 keys, where the products of both streams are 2048;
+// Measured: 64 requests behind 32768 positions, 64 / 8 heads of 128, 105 us (69 Gflop, 650
+// TFLOP/s): a stream takes 5500 cycles for 128 keys, where the products of both streams are 2048;
 // within a stream scores, weights and sums of a tile follow one another. 8 requests behind 80000
-// positions 77 us (2.1 TB/s), half of a stream's rows empty. Start and end take 9 us.
+// positions 78 us (2.1 TB/s), half of a stream's rows empty. Start and end take 9 us.
 //
 // Every mbarrier wait is bounded; one that runs out sets KV8_STATUS_TIMEOUT and ends the CTA's
 // work after its products in flight. Instead of the sums of all its units that are not finished
@@ -52,9 +53,12 @@ constexpr int kPRows = 2 * kTile;
 constexpr int kLeast = 128;     // positions of the least prefix that is read for all
 // Bytes of keys and values that sharing has to save by the caller's bounds, (groups - 1) *
 // max_prefix positions: below, the rows' own pass reads the prefixes again, mostly from L2, and is
-// done before two launches more would be (one set on 8 key heads of 128, rows' own pass against
-// this: 8 requests of 8192 positions 32 / 39 us, 117 MB; 4 of 32768 49 / 58, 201 MB; 8 of 32768
-// 81 / 58, 470 MB; 32 of 8192 84 / 55, 520 MB; on 2 key heads 32 of 32768 81 / 60, 520 MB).
+// done before two launches more would be (one set on 8 key heads of 128, 64 tokens of their own, rows'
+// own pass against this: 8 requests of 8192 positions 33 / 38 us, 117 MB; 4 of 32768 49 / 60,
+// 201 MB; 8 of 32768 82 / 61, 470 MB; 32 of 8192 82 / 58, 520 MB; on 2 key heads 32 of 32768 81 / 62,
+// 520 MB). The bounds count all groups and the longest prefix: where two requests of a batch share
+// 512 positions under a bound of 32768, the call takes about 25 us more than kv8_attention's (64 of
+// 4096 tokens 142 / 116, 256 of 512 141 / 117).
 constexpr double kWorth = 256e6;
 constexpr float kRaise = 11.0f, kBelow = 7.0f;  // log2: a reference is raised from here, to there
 constexpr float kMost = 32768.0f;  // of 16 weights together: 2^15, which is 2^kRaise for the largest

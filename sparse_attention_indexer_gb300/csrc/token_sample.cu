@@ -14,9 +14,11 @@
 //   - the probabilities, from the weights of the pass before where the logits are fp32.
 // Sums are 64-bit integers, so neither the split nor the order shows in the result.
 //
-// Bound by instructions, about 100 a logit with top-p: 256 rows of 131072 fp32 logits with
-// probabilities 279 us (0.96 TB/s), 64 rows of 100003 in bf16 68 us; one row by its eight cluster
-// barriers, 32 us. (A search bit by bit over all logits in place of the bins: 1436, 440 and 296 us;
+// Bound by instructions, about 110 a logit with top-p, and by cluster barriers: 256 rows of 131072 fp32
+// logits with probabilities 279 us (0.96 TB/s), 64 rows of 100003 in bf16 68 us; one row by its
+// eight cluster barriers, 32 us. Where the bin of a threshold holds more than 2048 tokens (flat
+// rows, one value in many places) all search it bit by bit: 64 rows of 131072 fp32 normal logits
+// with top-p 119 us at T = 1, 603 at T = 5, 715 at T = 20, of two values 413. (A search bit by bit over all logits in place of the bins: 1436, 440 and 296 us;
 // weights one by one in place of two to an operation, lists searched from shared memory: 435,
 // 112, 61.) Few rows take CTAs of 512 threads, more of them 256, three to an SM.
 #include <cooperative_groups.h>
@@ -444,8 +446,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
   };
   // The largest key among the tokens of bins [b0, b1] with F(key) >= target, F(key) the count or the
   // weight of these tokens from it on; `above` becomes F(key + 1). They are gathered by the
-  // first CTA where they fit its list; else all CTAs search them where they are. `first` and
-  // `second` searches of the same list: a count k, then the weight target(weight of the first k).
+  // first CTA where they fit its list; else all CTAs search them where they are. One list may be
+  // searched twice: for a count k, then for a share of the weight of the first k.
   auto gather = [&](int b0, int b1) {
     cluster.sync();  // all have read the bins
     uint32_t* const n = cluster.map_shared_rank(&s_n, 0);
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_sample_kernel(co
     }
     return key;
   };
-  // Lists are searched from registers, eight tokens and their weights to a thread (`at`: the
+  // Lists are searched from registers, kList / THREADS tokens and their weights to a thread (`at`: the
   // thread's place, `stride`: the threads).
   uint32_t lk[kList / THREADS];
   uint64_t lw[kList / THREADS];
