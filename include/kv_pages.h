@@ -126,8 +126,8 @@ int kvpages_copy(const int32_t* src, const int32_t* dst, int n, int num_pages,
  *   lens         device int32 [tokens] (written): pos + 1, what a causal query row sees
  *   starts       device int32 [n + 1] (written): min(tokens, tokens of the requests before)
  * `tokens` is the number of places, for graphs a bound on the step's tokens: the places behind
- * the last token hold -1, -1, -1 and 0 (an attention row of length 0 attends to nothing; a
- * store skips a token of row -1 and sets its status bit for that). A request that fails a
+ * the last token hold -1, -1, -1 and 0 (an attention row of length 0 attends to nothing, a
+ * store skips a token of row -1; both set their status bits for that row). A request that fails a
  * check brings no tokens. num_pages * page_size < 2^31. One launch. */
 int kvpages_step(const int32_t* rows, const int32_t* old_lens, const int32_t* new_lens, int n,
                  const int32_t* block_table, int n_tables, int64_t table_ld, int page_size,

@@ -108,7 +108,7 @@ def test_rows_too_long_to_keep(dtype):
     batch(x, u, settings_of(rng, 24, live), rows=[0, 23])
 
 
-def test_target_of_a_verify_step_in_place():
+def test_target_of_a_verify_step():
     """Probabilities of many rows into a strided output: what lies between its rows stays."""
     rng = np.random.default_rng(5)
     x = logits_of(rng, N, 5003, "bf16", 2.0)
